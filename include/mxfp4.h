@@ -430,6 +430,161 @@ fp4_status fp4_nv_gemm(int64_t m, int64_t n, int64_t k,
                        const float* b_factors, int64_t b_factor_stride,
                        float* c, int64_t ldc, int accumulate, hipStream_t stream);
 
+/* Element type of an activation or gradient tensor, and the code format of a
+ * producer's output (int-sized enumerations, like fp4_round). */
+#ifdef __cplusplus
+enum fp4_dtype : int { FP4_BF16 = 0, FP4_F32 = 1 };
+enum fp4_format : int { FP4_E2M1 = 0, FP4_E4M3 = 1 };
+#else
+typedef enum { FP4_BF16 = 0, FP4_F32 = 1 } fp4_dtype;
+typedef enum { FP4_E2M1 = 0, FP4_E4M3 = 1 } fp4_format;
+#endif
+
+/*
+ * Counter-based dropout, optionally added to a residual stream:
+ *   out = bf16(keep ? x * s : 0)                 (residual NULL)
+ *   out = bf16(keep ? fma(x, s, residual) : residual)
+ * with s = RN_fp32(65536 / (65536 - thr)), thr = floor(65536 p + 1/2) (p is
+ * taken to a multiple of 2^-16, and s is the inverse of the probability that
+ * this gives).  The mask is never stored: element c of row r has index
+ * i = r * 8 ceil(cols / 8) + c, and is kept iff half i & 1 (0: the low one) of
+ * word (i >> 1) & 3 of Philox4x32-10 at counter (lo32(i>>3), hi32(i>>3),
+ * lo32(offset), hi32(offset)) under key (lo32(seed), hi32(seed)) is >= thr.
+ * The backward pass is the same call on the output's gradient (no residual).
+ * Callers advance `offset` per call, as for the SR producers.  A dropped
+ * element leaves no trace: infinities and NaN under the mask vanish.  thr = 0
+ * keeps everything, p = 1 drops everything.
+ *   x         [rows][ldx] bf16 or fp32 (x_type; fp32: a GEMM's C)
+ *   residual  [rows][ldr] bf16, or NULL
+ *   out       [rows][ldo] bf16; columns cols .. ldo - 1 are left as they were
+ * Any cols and any ld >= cols; rows that all start on 16-byte boundaries (ldx,
+ * ldr, ldo multiples of 8) go by wide loads, others element by element.
+ * Errors: FP4_EINVAL bad x_type, p outside [0, 1] or null pointer; FP4_ESHAPE
+ * negative rows or cols, a leading dimension below cols, or more than 2^56
+ * groups of eight columns (2^31 - 1 in a row); FP4_EALIGN a pointer not
+ * aligned to its element.
+ */
+fp4_status fp4_dropout(int64_t rows, int64_t cols, const void* x, fp4_dtype x_type, int64_t ldx,
+                       const uint16_t* residual, int64_t ldr, float p, uint64_t seed, uint64_t offset,
+                       uint16_t* out, int64_t ldo, hipStream_t stream);
+
+/*
+ * RMSNorm producer: the boundary in front of a quantized linear layer (§3.1,
+ * §3.2: a producer keeps the residual and the row statistics and emits the
+ * codes its consumer reads).
+ *   s    = dropout(x) + residual as fp4_dropout (p = 0: x + residual; no
+ *          residual: x), rounded to bf16
+ *   rstd = 1 / sqrt(mean(s^2) + eps)             fp32, of the rounded s
+ *   y    = bf16((s * rstd) * gamma)              fp32, single roundings
+ * and the codes of y in blocks of 32 along d:
+ *   FP4_E2M1: the bytes of fp4_quantize_rows(y, FP4_RTN) (input of fp4_gemm
+ *             and fp4_swiglu_producer);
+ *   FP4_E4M3: MXFP8 -- E8M0 scale with e the smallest integer >= -127 with
+ *             amax <= 448 * 2^e, OCP E4M3FN bytes of y / 2^e, nearest even
+ *             (input of fp4_matvec and fp4_swiglu_matvec).
+ *   x         [t][ldx] bf16 or fp32,  residual [t][ldr] bf16 or NULL
+ *   gamma     [d] bf16
+ *   sum       [t][d] bf16 or NULL: s, which the backward pass reads
+ *   rstd      [t] fp32
+ *   y         [t][d] bf16 or NULL (e.g. for fp4_quantize_cols)
+ *   codes     [t][d/2] (E2M1) or [t][d] (E4M3), scales [t][d/32]; both or
+ *             neither NULL
+ * |s| must stay below 2^63 / sqrt(d) (the squares are summed in fp32).
+ * Errors: FP4_EINVAL bad x_type or format, p outside [0, 1], eps not a
+ * positive finite number, exactly one of codes, scales NULL, or another null
+ * pointer; FP4_ESHAPE t negative or above 2^31 - 1, d not a non-negative
+ * multiple of 32 or above 32768 (a row stays in one workgroup's registers), or
+ * a leading dimension below d; FP4_EALIGN x, residual, gamma, sum, y or codes
+ * not 16-byte aligned, ldx (bf16) or ldr not a multiple of 8, or ldx (fp32)
+ * not a multiple of 4.
+ */
+fp4_status fp4_rmsnorm_producer(int64_t t, int64_t d, const void* x, fp4_dtype x_type, int64_t ldx,
+                                const uint16_t* residual, int64_t ldr, const uint16_t* gamma, float eps,
+                                float p, uint64_t seed, uint64_t offset,
+                                uint16_t* sum, float* rstd, uint16_t* y,
+                                fp4_format format, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/*
+ * Gradients of that boundary.  With dy the gradient of y (fp32: the consumer's
+ * Dgrad output), xh = s * rstd, g = dy * gamma, all in fp32:
+ *   ds'    = rstd * (g - xh * mean(g * xh)) [+ ds]
+ *   dsum   = bf16(ds')                 gradient of s, hence of the residual
+ *   dx     = bf16(dropout(ds'))        same (p, seed, offset) as the forward;
+ *                                      written only when p rounds above 0,
+ *                                      otherwise dx = dsum and dx may be NULL
+ *   dgamma (+)= sum over the t rows of dy * xh    fp32 [d]
+ * ds is the gradient that reaches s along the residual stream.  Deterministic:
+ * at most 512 partial sums of dgamma meet in the workspace and are added in
+ * order.
+ *   dy [t][lddy] bf16 or fp32; s [t][lds] bf16; rstd [t]; gamma [d] bf16
+ *   ds [t][ldds] bf16 or NULL; dsum, dx [t][d] bf16
+ *   workspace  fp4_rmsnorm_backward_workspace(t, d) bytes, 16-byte aligned,
+ *              in use until the call's work on the stream is done
+ * t = 0 sets dgamma to 0 (leaves it unchanged when accumulating).
+ * Errors: FP4_EINVAL bad dy_type, p outside [0, 1], accumulate not 0 or 1, or
+ * null pointer; FP4_ESHAPE as the producer, or a workspace below that size;
+ * FP4_EALIGN a tensor or the workspace not 16-byte aligned (rstd and dgamma: 4), lddy
+ * (bf16), lds or ldds not a multiple of 8, or lddy (fp32) not a multiple of 4.
+ */
+fp4_status fp4_rmsnorm_backward(int64_t t, int64_t d, const void* dy, fp4_dtype dy_type, int64_t lddy,
+                                const uint16_t* s, int64_t lds, const float* rstd, const uint16_t* gamma,
+                                const uint16_t* ds, int64_t ldds, float p, uint64_t seed, uint64_t offset,
+                                uint16_t* dsum, uint16_t* dx, float* dgamma, int accumulate,
+                                void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of the workspace above; -1 for a shape the call refuses.  Host-only. */
+int64_t fp4_rmsnorm_backward_workspace(int64_t t, int64_t d);
+
+/*
+ * A few rows against MXFP4 weights, the single-token and small-batch form of
+ * fp4_gemm: C[m][n] (+)= sum_k x[m][k] * dec(W)[n][k] in fp32, m <= 64.
+ * W is the row layout of fp4_quantize_w2d32 (or fp4_quantize_rows).  x stays
+ * in bf16, or is E4M3 codes with E8M0 scales as fp4_rmsnorm_producer emits
+ * (x_scales not NULL).  Every decoded value is exact in bf16, the products run
+ * on the bf16 matrix cores with fp32 sums.  Deterministic.
+ *   x        bf16 [m][ldx], or E4M3 [m][k] (ldx = k) with x_scales [m][k/32]
+ *   w_codes  [n][k/2], w_scales [n][k/32]
+ *   c        [m][ldc] fp32, any ldc >= n
+ * Any n; an empty reduction (k = 0) writes 0.  Decoded weights must be below
+ * 2^128 in magnitude (scale byte 253 with codes 4 and 6 is not).
+ * Errors: FP4_EINVAL accumulate not 0 or 1, or null pointer; FP4_ESHAPE m
+ * outside [0, 64], n negative or above 2^34, k not a non-negative multiple of
+ * 32 or >= 2^24, ldx < k, ldx >= 2^24 (32-bit offsets within x), ldx != k with
+ * x_scales, or ldc < n; FP4_EALIGN x or w_codes not 16-byte aligned, ldx not a
+ * multiple of 8 (bf16), or c not 4-byte aligned.
+ */
+fp4_status fp4_matvec(int64_t m, int64_t n, int64_t k, const void* x, int64_t ldx, const uint8_t* x_scales,
+                      const uint8_t* w_codes, const uint8_t* w_scales, float* c, int64_t ldc, int accumulate,
+                      hipStream_t stream);
+
+/*
+ * The same for CTA-local NVFP4 weights (the row layout of
+ * fp4_nv_quantize_w2d16 with w_factor_stride 0, or of fp4_nv_quantize_rows
+ * with stride 1) and bf16 x:
+ *   C[m][n] (+)= w_factors[(n / 256) * w_factor_stride] * sum_k x[m][k] (delta q)[n][k]
+ *   w_codes [n][k/2], w_scales [n][k/16] E4M3
+ * Errors as fp4_matvec; FP4_EINVAL also for a negative stride; FP4_EALIGN also
+ * for w_scales not 2-byte or w_factors not 4-byte aligned.
+ */
+fp4_status fp4_nv_matvec(int64_t m, int64_t n, int64_t k, const uint16_t* x, int64_t ldx,
+                         const uint8_t* w_codes, const uint8_t* w_scales, const float* w_factors,
+                         int64_t w_factor_stride, float* c, int64_t ldc, int accumulate, hipStream_t stream);
+
+/*
+ * The gated FFN's first half for a few rows, the small form of
+ * fp4_swiglu_producer: a = bf16(x W1^T), b = bf16(x W3^T),
+ *   h = bf16((a * sig(a)) * b)
+ * with that call's precision chain and exponential; h goes to the W2 product
+ * of fp4_matvec as it is.
+ *   x as fp4_matvec (m <= 64 rows of d values)
+ *   w13_codes [2f][d/2], w13_scales [2f][d/32] (rows 0..f-1: W1, f..2f-1: W3)
+ *   h [m][f] bf16
+ * Errors as fp4_matvec, with f for n; FP4_EALIGN h not 2-byte aligned.
+ */
+fp4_status fp4_swiglu_matvec(int64_t m, int64_t f, int64_t d, const void* x, int64_t ldx, const uint8_t* x_scales,
+                             const uint8_t* w13_codes, const uint8_t* w13_scales, uint16_t* h,
+                             hipStream_t stream);
+
 /*
  * Fixed 16-entry sign vector for H32 as a bit mask (bit j set => d_j = -1).
  * App. A.1 fixes one 16-entry sign vector, shared by both Wgrad operands and

@@ -18,6 +18,8 @@ import torch
 from .build import lib_path
 
 FP4_RTN, FP4_SR = 0, 1
+FP4_BF16, FP4_F32 = 0, 1
+FP4_E2M1, FP4_E4M3 = 0, 1
 STATUS = {0: "FP4_OK", 1: "FP4_EINVAL", 2: "FP4_ESHAPE", 3: "FP4_EALIGN", 4: "FP4_EHIP"}
 
 _lib = None
@@ -39,10 +41,20 @@ _SIGS = {
     "fp4_nv_quantize_rows": [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _int, _u64, _u64, _vp],
     "fp4_nv_quantize_w2d16": [_vp, _i64, _i64, _i64] + [_vp] * 7,
     "fp4_nv_gemm": [_i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _int, _vp],
+    "fp4_dropout": [_i64, _i64, _vp, _int, _i64, _vp, _i64, ctypes.c_float, _u64, _u64, _vp, _i64, _vp],
+    "fp4_rmsnorm_producer": [_i64, _i64, _vp, _int, _i64, _vp, _i64, _vp, ctypes.c_float, ctypes.c_float, _u64, _u64,
+                             _vp, _vp, _vp, _int, _vp, _vp, _vp],
+    "fp4_rmsnorm_backward": [_i64, _i64, _vp, _int, _i64, _vp, _i64, _vp, _vp, _vp, _i64, ctypes.c_float, _u64, _u64,
+                             _vp, _vp, _vp, _int, _vp, _i64, _vp],
+    "fp4_rmsnorm_backward_workspace": [_i64, _i64],
+    "fp4_matvec": [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _int, _vp],
+    "fp4_nv_matvec": [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _int, _vp],
+    "fp4_swiglu_matvec": [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp],
     "fp4_sign_mask_from_seed": [_u64],
     "fp4_last_hip_error": [],
     "fp4_abi_version": [],
 }
+_RESTYPES = {"fp4_sign_mask_from_seed": _u32, "fp4_rmsnorm_backward_workspace": _i64}
 EXPORTS = tuple(_SIGS)
 
 
@@ -63,7 +75,7 @@ def load(path=None):
     for name, args in _SIGS.items():
         fn = getattr(lib, name)
         fn.argtypes = args
-        fn.restype = ctypes.c_uint32 if name == "fp4_sign_mask_from_seed" else ctypes.c_int
+        fn.restype = _RESTYPES.get(name, ctypes.c_int)
     _lib = lib
     return lib
 
@@ -424,6 +436,173 @@ def fp4_nv_gemm(a_codes, a_scales, a_factors, b_codes, b_scales, b_factors, c=No
                               _p(b_scales), _p(b_factors), strides[1], _p(c), c.stride(0), 1 if accumulate else 0,
                               _stream()))
     return c
+
+
+_BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _rows2d(x, name, shape=None, f32=False):
+    """A 2-D tensor of bf16 values (or, with f32, fp32 ones) with unit column
+    stride; returns its leading dimension."""
+    _dev(x, name)
+    if x.dtype not in _BITS16 and not (f32 and x.dtype == torch.float32):
+        raise Fp4Error(f"{name} must hold bf16 values or their 16-bit patterns" + (", or fp32 values" if f32 else ""))
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise Fp4Error(f"{name} must be 2-D with unit column stride")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise Fp4Error(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    # the stride of a single row says nothing
+    return x.stride(0) if x.shape[0] > 1 else -(-x.shape[1] // 8) * 8
+
+
+def _vec(t, name, n, dtypes):
+    _dev(t, name)
+    if t.dtype not in dtypes or t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+        raise Fp4Error(f"{name} must be a contiguous vector of {n} elements of {dtypes[0]}")
+    return t
+
+
+def _out16(t, shape, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    _dev(t, name)
+    if tuple(t.shape) != tuple(shape) or t.dtype not in _BITS16 or not t.is_contiguous():
+        raise Fp4Error(f"{name} must be a contiguous bf16 tensor of shape {tuple(shape)}")
+    return t
+
+
+def _dtype(x):
+    return FP4_F32 if x.dtype == torch.float32 else FP4_BF16
+
+
+def fp4_dropout(x, p, seed=0, offset=0, residual=None, out=None):
+    """bf16(dropout(x) [+ residual]) with a mask drawn from (seed, offset) and
+    never stored; the same call on the output's gradient (without residual) is
+    the backward pass.  Without `out` the result's rows lie at a pitch of a
+    multiple of eight elements (what the quantizers read)."""
+    ldx = _rows2d(x, "x", f32=True)
+    rows, cols = x.shape
+    ldr = 0 if residual is None else _rows2d(residual, "residual", (rows, cols))
+    if out is None:
+        out = torch.empty((rows, -(-cols // 8) * 8), dtype=torch.bfloat16, device=x.device)[:, :cols]
+    ldo = _rows2d(out, "out", (rows, cols))
+    _check(load().fp4_dropout(rows, cols, _p(x), _dtype(x), ldx, _p(residual), ldr, float(p), int(seed), int(offset),
+                              _p(out), ldo, _stream()))
+    return out
+
+
+def fp4_rmsnorm_producer(x, gamma, eps=1e-5, residual=None, p=0.0, seed=0, offset=0, fmt=FP4_E4M3, emit_sum=True,
+                         emit_y=False, emit_codes=True, out=None):
+    """Dropout of x, addition to the residual, RMSNorm and its codes: returns
+    (s, rstd, y, codes, scales), None where not emitted.  `out` may hold those
+    five buffers (None: allocated)."""
+    ldx = _rows2d(x, "x", f32=True)
+    t, d = x.shape
+    ldr = 0 if residual is None else _rows2d(residual, "residual", (t, d))
+    _vec(gamma, "gamma", d, _BITS16)
+    dev = x.device
+    if d % 32:
+        raise Fp4Error("the row length must be a multiple of 32")
+    out = list(out) if out is not None else [None] * 5
+    s = _out16(out[0], (t, d), dev, "sum") if emit_sum else None
+    rstd = _out(out[1], (t,), torch.float32, dev, "rstd")
+    y = _out16(out[2], (t, d), dev, "y") if emit_y else None
+    codes = scales = None
+    if emit_codes:
+        codes = _out(out[3], (t, d // 2 if fmt == FP4_E2M1 else d), torch.uint8, dev, "codes")
+        scales = _out(out[4], (t, d // 32), torch.uint8, dev, "scales")
+    _check(load().fp4_rmsnorm_producer(t, d, _p(x), _dtype(x), ldx, _p(residual), ldr, _p(gamma), float(eps), float(p),
+                                       int(seed), int(offset), _p(s), _p(rstd), _p(y), int(fmt), _p(codes),
+                                       _p(scales), _stream()))
+    return s, rstd, y, codes, scales
+
+
+def fp4_rmsnorm_backward(dy, s, rstd, gamma, ds=None, p=0.0, seed=0, offset=0, accumulate=False, out=None):
+    """Gradients of fp4_rmsnorm_producer's boundary: returns (dsum, dx, dgamma);
+    dx is dsum where nothing is dropped.  `ds` is the gradient that reaches s
+    along the residual stream; `out` may hold the three buffers."""
+    lddy = _rows2d(dy, "dy", f32=True)
+    t, d = dy.shape
+    lds = _rows2d(s, "s", (t, d))
+    ldds = 0 if ds is None else _rows2d(ds, "ds", (t, d))
+    _vec(rstd, "rstd", t, (torch.float32,))
+    _vec(gamma, "gamma", d, _BITS16)
+    dev = dy.device
+    out = list(out) if out is not None else [None] * 3
+    if accumulate and out[2] is None:
+        raise Fp4Error("accumulate needs a dgamma tensor")
+    dsum = _out16(out[0], (t, d), dev, "dsum")
+    dx = _out16(out[1], (t, d), dev, "dx") if int(float(p) * 65536 + 0.5) > 0 else None
+    dgamma = _out(out[2], (d,), torch.float32, dev, "dgamma")
+    lib = load()
+    size = lib.fp4_rmsnorm_backward_workspace(t, d)
+    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
+    _check(lib.fp4_rmsnorm_backward(t, d, _p(dy), _dtype(dy), lddy, _p(s), lds, _p(rstd), _p(gamma), _p(ds), ldds,
+                                    float(p), int(seed), int(offset), _p(dsum), _p(dx), _p(dgamma),
+                                    1 if accumulate else 0, _p(ws), size, _stream()))
+    return dsum, dsum if dx is None else dx, dgamma
+
+
+def _few_rows(x, x_scales, w_codes):
+    """Shapes of the few-row products: returns (m, k, ldx)."""
+    _u8_2d(w_codes, "w_codes")
+    if x_scales is None:
+        ldx = _rows2d(x, "x")
+    else:
+        _u8_2d(x, "x")
+        _u8_2d(x_scales, "x_scales", (x.shape[0], x.shape[1] // 32))
+        ldx = x.shape[1]
+    m, k = x.shape
+    if 2 * w_codes.shape[1] != k:
+        raise Fp4Error(f"w_codes has {2 * w_codes.shape[1]} values per row, x {k}")
+    return m, k, ldx
+
+
+def fp4_matvec(x, w_codes, w_scales, x_scales=None, c=None, accumulate=False):
+    """C (+)= x dec(W)^T for up to 64 rows of x, bf16 or E4M3 codes with
+    x_scales, and MXFP4 weights in the row layout."""
+    m, k, ldx = _few_rows(x, x_scales, w_codes)
+    n = w_codes.shape[0]
+    _u8_2d(w_scales, "w_scales", (n, k // 32))
+    c = _gemm_out(c, m, n, accumulate, x.device)
+    _check(load().fp4_matvec(m, n, k, _p(x), ldx, _p(x_scales), _p(w_codes), _p(w_scales), _p(c), _ldc(c),
+                             1 if accumulate else 0, _stream()))
+    return c
+
+
+def fp4_nv_matvec(x, w_codes, w_scales, w_factors, c=None, accumulate=False):
+    """C (+)= x dec(W)^T for up to 64 rows of bf16 x and CTA-local NVFP4
+    weights in the row layout; a factor vector of one element is shared by all
+    rows of W, otherwise it holds one per 256-row panel."""
+    m, k, ldx = _few_rows(x, None, w_codes)
+    n = w_codes.shape[0]
+    _u8_2d(w_scales, "w_scales", (n, k // 16))
+    panels = (n + 255) // 256
+    _dev(w_factors, "w_factors")
+    if (w_factors.dtype != torch.float32 or w_factors.dim() != 1 or not w_factors.is_contiguous()
+            or w_factors.numel() not in (1, panels)):
+        raise Fp4Error(f"w_factors must be a contiguous fp32 vector of 1 or {panels} elements")
+    c = _gemm_out(c, m, n, accumulate, x.device)
+    _check(load().fp4_nv_matvec(m, n, k, _p(x), ldx, _p(w_codes), _p(w_scales), _p(w_factors),
+                                0 if w_factors.numel() == 1 else 1, _p(c), _ldc(c), 1 if accumulate else 0, _stream()))
+    return c
+
+
+def fp4_swiglu_matvec(x, w13_codes, w13_scales, x_scales=None, h=None):
+    """h = bf16(SiLU(a) b) with a = bf16(x W1^T), b = bf16(x W3^T) for up to 64
+    rows of x (as fp4_matvec) and the stacked MXFP4 rows of W1 and W3."""
+    m, d, ldx = _few_rows(x, x_scales, w13_codes)
+    if w13_codes.shape[0] % 2:
+        raise Fp4Error("w13_codes must stack W1 and W3: an even number of rows")
+    f = w13_codes.shape[0] // 2
+    _u8_2d(w13_scales, "w13_scales", (2 * f, d // 32))
+    h = _out16(h, (m, f), x.device, "h")
+    _check(load().fp4_swiglu_matvec(m, f, d, _p(x), ldx, _p(x_scales), _p(w13_codes), _p(w13_scales), _p(h), _stream()))
+    return h
+
+
+def _ldc(c):
+    return c.stride(0) if c.shape[0] > 1 else c.shape[1]
 
 
 def fp4_sign_mask_from_seed(seed):
