@@ -89,7 +89,9 @@ def _check(status):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the handle itself: torch.cuda.current_stream() builds a Stream object
+    # around it, 3 us of a small call's 10
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dev(t, name):
@@ -97,7 +99,7 @@ def _dev(t, name):
         raise Fp4Error(f"{name} must be a CUDA (HIP) tensor")
     # the kernels run on the current device's current stream: a tensor on
     # another device would be read through that device's memory, unmapped here
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise Fp4Error(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return t
 
@@ -121,7 +123,7 @@ def _out(t, shape, dtype, device, name):
 
 
 def _p(t):
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def fp4_quantize_rows(x, mode=FP4_RTN, seed=0, offset=0, codes=None, scales=None):
@@ -445,14 +447,15 @@ def _rows2d(x, name, shape=None, f32=False):
     """A 2-D tensor of bf16 values (or, with f32, fp32 ones) with unit column
     stride; returns its leading dimension."""
     _dev(x, name)
-    if x.dtype not in _BITS16 and not (f32 and x.dtype == torch.float32):
+    if x.dtype not in _BITS16 and not (f32 and x.dtype is torch.float32):
         raise Fp4Error(f"{name} must hold bf16 values or their 16-bit patterns" + (", or fp32 values" if f32 else ""))
-    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+    size, stride = x.shape, x.stride()
+    if len(size) != 2 or (stride[1] != 1 and size[1] > 1):
         raise Fp4Error(f"{name} must be 2-D with unit column stride")
-    if shape is not None and tuple(x.shape) != tuple(shape):
-        raise Fp4Error(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    if shape is not None and size != shape:
+        raise Fp4Error(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
     # the stride of a single row says nothing
-    return x.stride(0) if x.shape[0] > 1 else -(-x.shape[1] // 8) * 8
+    return stride[0] if size[0] > 1 else -(-size[1] // 8) * 8
 
 
 def _vec(t, name, n, dtypes):
@@ -482,10 +485,10 @@ def fp4_dropout(x, p, seed=0, offset=0, residual=None, out=None):
     multiple of eight elements (what the quantizers read)."""
     ldx = _rows2d(x, "x", f32=True)
     rows, cols = x.shape
-    ldr = 0 if residual is None else _rows2d(residual, "residual", (rows, cols))
+    ldr = 0 if residual is None else _rows2d(residual, "residual", x.shape)
     if out is None:
         out = torch.empty((rows, -(-cols // 8) * 8), dtype=torch.bfloat16, device=x.device)[:, :cols]
-    ldo = _rows2d(out, "out", (rows, cols))
+    ldo = _rows2d(out, "out", x.shape)
     _check(load().fp4_dropout(rows, cols, _p(x), _dtype(x), ldx, _p(residual), ldr, float(p), int(seed), int(offset),
                               _p(out), ldo, _stream()))
     return out
@@ -498,7 +501,7 @@ def fp4_rmsnorm_producer(x, gamma, eps=1e-5, residual=None, p=0.0, seed=0, offse
     five buffers (None: allocated)."""
     ldx = _rows2d(x, "x", f32=True)
     t, d = x.shape
-    ldr = 0 if residual is None else _rows2d(residual, "residual", (t, d))
+    ldr = 0 if residual is None else _rows2d(residual, "residual", x.shape)
     _vec(gamma, "gamma", d, _BITS16)
     dev = x.device
     if d % 32:
@@ -523,8 +526,8 @@ def fp4_rmsnorm_backward(dy, s, rstd, gamma, ds=None, p=0.0, seed=0, offset=0, a
     along the residual stream; `out` may hold the three buffers."""
     lddy = _rows2d(dy, "dy", f32=True)
     t, d = dy.shape
-    lds = _rows2d(s, "s", (t, d))
-    ldds = 0 if ds is None else _rows2d(ds, "ds", (t, d))
+    lds = _rows2d(s, "s", dy.shape)
+    ldds = 0 if ds is None else _rows2d(ds, "ds", dy.shape)
     _vec(rstd, "rstd", t, (torch.float32,))
     _vec(gamma, "gamma", d, _BITS16)
     dev = dy.device

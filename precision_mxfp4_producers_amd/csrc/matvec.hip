@@ -85,110 +85,287 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
   b = bf16x8_t{p[4][0], p[4][1], p[5][0], p[5][1], p[6][0], p[6][1], p[7][0], p[7][1]};
 }
 
-// One workgroup computes 16 RT rows of W (gated: 16 RT rows of W1 and of W3)
-// against all m <= 16 MT rows of x.  Its waves split K: wave w takes the
-// 128-value steps w, w + NW, ...; lane (r = lane & 15, g = lane >> 4) holds
-// values 32 g .. 32 g + 31 of the step of W row r and of x row r, which the
-// 16x16x32 bf16 products take eight at a time (both operands list K in the
-// same order).  The partial sums meet in LDS and are added in wave order:
-// deterministic, no atomics, no workspace.
-template <int XT, int WT, int MT, int RT, int NW, bool GATE>
-__global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a) {
-  constexpr int NT = GATE ? 2 * RT : RT;                 // 16-row tiles of W
-  __shared__ v4f red[NW * MT * NT * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+// NW waves form a workgroup: sixteen, or eight for four tiles of x rows, whose
+// operands take the registers of two waves.  A tile is 16 rows of W (gated: 8
+// of W1 and the same 8 of W3); KW waves share one and split K, the workgroup
+// works on NW / KW tiles at a time and walks groups of them blockIdx.x,
+// blockIdx.x + gridDim.x, ...  A step is 128 values of K: lane (r = lane & 15,
+// g = lane >> 4) holds values 32 g .. 32 g + 31 of the step of W row r and of x
+// row r, which the 16x16x32 bf16 products take eight at a time (both operands
+// list K in the same order).  An item is U consecutive steps; wave kw takes
+// items kw, kw + KW, ... of a tile, and the loads of its next item, across the
+// end of a tile too, are in flight during the products of the current one.
+// No branch surrounds a load: the compiler could not count the outstanding
+// ones and would wait for all.  The partial sums meet in LDS and are added in
+// wave order: deterministic, no atomics, no workspace.
+//
+// x is staged once per workgroup in LDS as bf16 where it fits (STAGED: its
+// loads would otherwise carry 64 useful bytes per instruction and row), else
+// each wave loads its part of x with the item.
+// WHOLE: K is a multiple of U steps and the scales are aligned, so that an
+// item's scale bytes of a row come with one load.
+constexpr int kLds = 160 * 1024;
+constexpr int kStageBytes = 120 * 1024;                  // most of x in LDS; the rest is the partial sums'
+
+// Bytes between staged rows of x: 16 past the rounded row, so that equal
+// columns of neighbouring rows fall into different banks.
+__host__ __device__ constexpr int64_t stage_pitch(int64_t k) { return (k + 127) / 128 * 256 + 16; }
+
+// How a launch splits the work (host side).
+struct MvPlan {
+  int kw_log2;                                           // waves per tile
+  int batch;                                             // groups of tiles between two meetings of the partial sums
+};
+
+// The scale bytes of an item: WHOLE: a row's bytes for U steps (4 U, NVFP4
+// 8 U); else this lane's own of one step.
+template <int WT, int U>
+struct MvItem {
+  v4i c[U];
+  uint32_t s[WT == kMx ? U : 2 * U];
+};
+
+template <int XT, int MT, int U>
+struct MvX {
+  v4i v[MT][U][XT == kXBf16 ? 4 : 2];
+  uint32_t s[MT][U];
+};
+
+// Waits for this wave's LDS accesses and meets the workgroup's other waves;
+// global loads stay in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <int XT, int WT, int MT, int NW, int U, bool GATE, bool STAGED, bool WHOLE>
+__global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan plan) {
+  static_assert(WHOLE || U == 1, "a partial step is an item of its own");
+  constexpr int ROWS = GATE ? 8 : 16;                    // output columns of a tile
+  constexpr bool AHEAD = !STAGED && MT <= 2;             // x of the next item too
+  constexpr int kSlot = NW * MT * 64;                    // partial sums of one group of tiles, in v4f
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+  v4f* const red = reinterpret_cast<v4f*>(lds);
+  uint8_t* const stage = lds + (uint32_t)plan.batch * (kSlot * 16);
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int kw = wave & ((1 << plan.kw_log2) - 1), rt = wave >> plan.kw_log2, RT = NW >> plan.kw_log2;
   const int64_t kc = a.k >> 1, ks = a.k >> (WT == kMx ? 5 : 4);   // bytes of a row's codes and scales
-  __amdgpu_buffer_rsrc_t rc[NT], rs[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int64_t row = n0 + 16 * (GATE ? i >> 1 : i);
-    const int64_t rows = std::max<int64_t>(0, std::min<int64_t>(16, a.n - row));
-    const int64_t at = row + (GATE && (i & 1) ? a.n : 0);
-    rc[i] = buffer_rsrc(a.codes + at * kc, rows * kc);
-    rs[i] = buffer_rsrc(a.scales + at * ks, rows * ks);
-  }
+  const int steps = (int)((a.k + 127) >> 7), items = (steps + U - 1) / U;
+  const int per = (items + (1 << plan.kw_log2) - 1) >> plan.kw_log2;   // turns of a wave per tile
+  const int64_t tiles = (a.n + ROWS - 1) / ROWS, groups = (tiles + RT - 1) / RT;
   const __amdgpu_buffer_rsrc_t rx =
       buffer_rsrc(a.x, XT == kXBf16 ? ((a.m - 1) * a.ldx + a.k) * 2 : (int64_t)a.m * a.k);
   const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(a.x_scales, XT == kXBf16 ? 0 : (int64_t)a.m * (a.k >> 5));
-  v4f acc[MT][NT];
+
+  // Row r of a tile: a row past the end reads the last one (its sums are not stored).
+  const auto load_w = [&](MvItem<WT, U>& it, int64_t group, int turn) {
+    const int64_t out = std::min((group * RT + rt) * ROWS + (r & (ROWS - 1)), a.n - 1);
+    const int64_t row = out + (GATE && r >= ROWS ? a.n : 0);
+    const int item = std::min(kw + (turn << plan.kw_log2), items - 1);   // a wave without an item reads the last
+    const uint8_t* const c = a.codes + row * kc;
+    const uint8_t* const s = a.scales + row * ks;
+    if constexpr (WHOLE) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+      for (int u = 0; u < U; ++u)
+        it.c[u] = *reinterpret_cast<const v4i*>(c + (item * U + u) * 64 + g * 16);
+      constexpr int kBytes = (WT == kMx ? 4 : 8) * U;
+      const uint8_t* const p = s + item * kBytes;
+      if constexpr (kBytes % 16 == 0) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const int steps = (int)((a.k + 127) >> 7);
-  for (int st = wave; st < steps; st += NW) {
-    const uint32_t kb = (uint32_t)st * 4 + g;            // this lane's block of 32 values
-    const bool in = kb * 32 < (uint32_t)a.k;             // k is a multiple of 32: a block is whole or absent
-    bf16x8_t x[MT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int row = 16 * i + r;
-      const bool ok = in && row < a.m;
-      if constexpr (XT == kXBf16) {
-        const uint32_t off = ok ? ((uint32_t)row * (uint32_t)a.ldx + kb * 32) * 2 : kOffNone;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          x[i][q] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rx, off + 16 * q, 0, 0));
+        for (int b = 0; b < kBytes / 16; ++b) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * b);
+          it.s[4 * b] = v.x; it.s[4 * b + 1] = v.y; it.s[4 * b + 2] = v.z; it.s[4 * b + 3] = v.w;
+        }
       } else {
-        const uint32_t off = ok ? (uint32_t)row * (uint32_t)a.k + kb * 32 : kOffNone;
-        const uint32_t so = ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + kb : kOffNone;
-        const uint32_t sc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rxs, so, 0, 0);
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          decode_x16(__builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off + 16 * q, 0, 0)), sc,
-                     x[i][2 * q], x[i][2 * q + 1]);
+        for (int b = 0; b < kBytes / 4; ++b) it.s[b] = reinterpret_cast<const uint32_t*>(p)[b];
       }
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const uint32_t off = in ? (uint32_t)r * (uint32_t)kc + kb * 16 : kOffNone;
-      const v4i w = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rc[j], off, 0, kLoadOnce));
+    } else {
+      const int kb = item * 4 + g;                       // a block of 32 values is whole or absent
+      const bool in = kb * 32 < (int)a.k;
+      const int at = in ? kb : 0;
+      const v4i v = *reinterpret_cast<const v4i*>(c + at * 16);
       uint32_t sc;
-      if constexpr (WT == kMx)
-        sc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs[j], in ? (uint32_t)r * (uint32_t)ks + kb : kOffNone, 0, 0);
-      else
-        sc = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[j], in ? (uint32_t)r * (uint32_t)ks + kb * 2 : kOffNone, 0, 0);
-      bf16x8_t wf[4];
-      decode32<WT>(w, sc, wf);
+      if constexpr (WT == kMx) sc = s[at];
+      else sc = *reinterpret_cast<const uint16_t*>(s + 2 * at);
+      it.c[0] = in ? v : v4i{0, 0, 0, 0};
+      it.s[0] = in ? sc : 0;
+    }
+  };
+  const auto load_x = [&](MvX<XT, MT, U>& it, int turn) {
+    const int item = std::min(kw + (turn << plan.kw_log2), items - 1);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t kb = (uint32_t)(item * U + u) * 4 + g;
+        const int row = 16 * i + r;
+        const bool ok = kb * 32 < (uint32_t)a.k && row < a.m;
+        if constexpr (XT == kXBf16) {
+          const uint32_t off = ok ? ((uint32_t)row * (uint32_t)a.ldx + kb * 32) * 2 : kOffNone;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            it.v[i][u][q] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off + 16 * q, 0, 0));
+        } else {
+          const uint32_t off = ok ? (uint32_t)row * (uint32_t)a.k + kb * 32 : kOffNone;
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            it.v[i][u][q] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off + 16 * q, 0, 0));
+          it.s[i][u] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+              rxs, ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + kb : kOffNone, 0, 0);
+        }
+      }
+  };
+
+  v4f acc[MT];
+  const auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  const uint32_t xrow = STAGED ? (uint32_t)(r < a.m ? r : 0) * (uint32_t)stage_pitch(a.k) + g * 64 : 0;
+  const auto multiply = [&](const MvItem<WT, U>& it, const MvX<XT, MT, U>& xi, int turn) {
+    const int item = kw + (turn << plan.kw_log2);
+    if (item >= items) return;                           // wave-uniform
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      bf16x8_t x[MT][4], w[4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if constexpr (STAGED) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x[i][q] = *reinterpret_cast<const bf16x8_t*>(stage + xrow + (uint32_t)(item * U + u) * 256 + 16 * q);
+        } else if constexpr (XT == kXBf16) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[i][q] = __builtin_bit_cast(bf16x8_t, xi.v[i][u][q]);
+        } else {
+          decode_x16(xi.v[i][u][0], xi.s[i][u], x[i][0], x[i][1]);
+          decode_x16(xi.v[i][u][1], xi.s[i][u], x[i][2], x[i][3]);
+        }
+      }
+      uint32_t sc = it.s[u];
+      if constexpr (WHOLE && WT == kMx) sc = (sc >> (8 * g)) & 0xFFu;
+      if constexpr (WHOLE && WT == kNv) sc = ((g & 2) ? it.s[2 * u + 1] : it.s[2 * u]) >> (16 * (g & 1));
+      decode32<WT>(it.c[u], sc, w);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[q], x[i][q], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < MT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[q], x[i][q], acc[i], 0, 0, 0);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) red[((wave * MT + i) * NT + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-  // lane l of a tile holds rows 4 (l >> 4) .. + 3 of W against row l & 15 of x
-  const float* rf = reinterpret_cast<const float*>(red);
-  const auto total = [&](int i, int j, int nl, int ml) {
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w)
-      v = __fadd_rn(v, rf[((((w * MT + i) * NT + j) * 64) + (nl >> 2) * 16 + ml) * 4 + (nl & 3)]);
-    return v;
   };
-  for (int e = threadIdx.x; e < MT * RT * 256; e += NW * 64) {
-    const int tile = e >> 8, i = tile / RT, j = tile % RT, ml = (e >> 4) & 15, nl = e & 15;
-    const int mr = 16 * i + ml;
-    const int64_t row = n0 + 16 * j + nl;
-    if (mr >= a.m || row >= a.n) continue;
-    if constexpr (GATE) {
-      const float av = bf16_bits_to_f32(f32_to_bf16_rne(total(i, 2 * j, nl, ml)));
-      const float bv = bf16_bits_to_f32(f32_to_bf16_rne(total(i, 2 * j + 1, nl, ml)));
-      float sig, s;
-      sigmoid_silu(av, sig, s);
-      a.h[mr * a.n + row] = (uint16_t)f32_to_bf16_rne(__fmul_rn(s, bv));
-    } else {
-      float v = total(i, j, nl, ml);
-      if constexpr (WT == kNv) v = __fmul_rn(a.factors[(row >> 8) * a.factor_stride], v);
-      float* p = a.c + mr * a.ldc + row;
-      *p = a.accumulate ? __fadd_rn(*p, v) : v;
+  // lane l of a partial tile holds rows 4 (l >> 4) .. + 3 of W against row l & 15 of x
+  const float* const rf = reinterpret_cast<const float*>(red);
+  const auto finish = [&](int64_t group, int slots) {     // group: the first one since the last meeting
+    lds_barrier();
+    const int count = slots * RT * MT * (16 * ROWS);
+    for (int e = threadIdx.x; e < count; e += NW * 64) {
+      const int nl = e & (ROWS - 1), ml = (e / ROWS) & 15;
+      int rest = e / (16 * ROWS);
+      const int i = rest % MT;
+      rest /= MT;
+      const int t = rest & (RT - 1), slot = rest / RT;
+      const int mr = 16 * i + ml;
+      const int64_t row = ((group + (int64_t)slot * gridDim.x) * RT + t) * ROWS + nl;
+      if (mr >= a.m || row >= a.n) continue;
+      const auto total = [&](int wr) {
+        const float* p = rf + ((slot * NW + (t << plan.kw_log2)) * MT + i) * 256 + ((wr >> 2) * 16 + ml) * 4 + (wr & 3);
+        float v = 0.0f;
+        for (int w = 0; w < 1 << plan.kw_log2; ++w) v = __fadd_rn(v, p[w * (MT * 256)]);
+        return v;
+      };
+      if constexpr (GATE) {
+        const float av = bf16_bits_to_f32(f32_to_bf16_rne(total(nl)));
+        const float bv = bf16_bits_to_f32(f32_to_bf16_rne(total(nl + ROWS)));
+        float sig, s;
+        sigmoid_silu(av, sig, s);
+        a.h[mr * a.n + row] = (uint16_t)f32_to_bf16_rne(__fmul_rn(s, bv));
+      } else {
+        float v = total(nl);
+        if constexpr (WT == kNv) v = __fmul_rn(a.factors[(row >> 8) * a.factor_stride], v);
+        float* p = a.c + mr * a.ldc + row;
+        *p = a.accumulate ? __fadd_rn(*p, v) : v;
+      }
     }
+    lds_barrier();                                       // the partial sums' room is free again
+  };
+
+  MvItem<WT, U> w0, w1;
+  MvX<XT, MT, U> x0, x1;
+  const int64_t first = blockIdx.x;
+  load_w(w0, first, 0);
+  if constexpr (AHEAD) load_x(x0, 0);
+  if constexpr (STAGED) {
+    const int chunks = steps * 16;                       // of eight values, zero past k
+    const uint32_t pitch = (uint32_t)stage_pitch(a.k);
+    for (int row = 0; row < a.m; ++row)
+      for (int c = threadIdx.x; c < chunks; c += NW * 64) {
+        v4i o;
+        const bool ok = c * 8 < a.k;
+        if constexpr (XT == kXBf16) {
+          o = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                          rx, ok ? ((uint32_t)row * (uint32_t)a.ldx + c * 8) * 2 : kOffNone, 0, 0));
+        } else {
+          typedef int v2i __attribute__((ext_vector_type(2)));
+          const v2i v = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(
+                                                    rx, ok ? (uint32_t)row * (uint32_t)a.k + c * 8 : kOffNone, 0, 0));
+          const uint32_t sc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+              rxs, ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + (c >> 2) : kOffNone, 0, 0);
+          bf16x8_t lo, unused;
+          decode_x16(v4i{v.x, v.y, 0, 0}, sc, lo, unused);
+          o = __builtin_bit_cast(v4i, lo);
+        }
+        *reinterpret_cast<v4i*>(stage + row * pitch + c * 16) = o;
+      }
+    lds_barrier();
+  }
+  clear();
+  // the workgroup's items in order: (group, turn), the same count for every wave, so that all reach the barriers
+  int64_t left = (groups - first + gridDim.x - 1) / gridDim.x * per;
+  int64_t group = first, met = first;
+  int turn = 0, slots = 0;
+  const auto advance = [&](int64_t& gr, int& tn) {
+    if (++tn == per) { tn = 0; gr += gridDim.x; }
+  };
+  // the products of an item; at a tile's end its sums go to LDS, and every `batch` tiles and at the end they meet
+  const auto use = [&](const MvItem<WT, U>& w, const MvX<XT, MT, U>& x) {
+    multiply(w, x, turn);
+    --left;
+    if (turn + 1 == per) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) red[slots * kSlot + (wave * MT + i) * 64 + lane] = acc[i];
+      clear();
+      if (++slots == plan.batch || left == 0) {
+        finish(met, slots);
+        slots = 0;
+        met = group + gridDim.x;
+      }
+    }
+    advance(group, turn);
+  };
+  const auto ahead = [&](MvItem<WT, U>& w, MvX<XT, MT, U>& x) {   // loads of the item after the current one
+    int64_t gr = group;
+    int tn = turn;
+    advance(gr, tn);
+    load_w(w, gr, tn);
+    if constexpr (AHEAD) load_x(x, tn);
+  };
+  const auto now = [&](MvX<XT, MT, U>& x) {
+    if constexpr (!STAGED && !AHEAD) load_x(x, turn);
+  };
+  while (left > 2) {
+    now(x0);
+    ahead(w1, x1);
+    use(w0, x0);
+    now(x1);
+    ahead(w0, x0);
+    use(w1, x1);
+  }
+  now(x0);
+  if (left == 2) {
+    ahead(w1, x1);
+    use(w0, x0);
+    now(x1);
+    use(w1, x1);
+  } else {
+    use(w0, x0);
   }
 }
 
@@ -201,6 +378,7 @@ __global__ void matvec_zero_kernel(MatvecArgs a) {
 }
 
 constexpr int kMatvecMaxM = 64;
+constexpr int64_t kMatvecGrid = 256;                     // one workgroup of 16 waves per CU
 
 template <int XT, int WT, bool GATE>
 static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
@@ -210,12 +388,47 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(matvec_zero_kernel, dim3((unsigned)grid), dim3(256), 0, stream, a);
     return launch_status();
   }
-  const auto go = [&](auto kernel, int rows, int nw) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.n + rows - 1) / rows)), dim3(nw * 64), 0, stream, a);
+  constexpr int ROWS = GATE ? 8 : 16;
+  const int64_t tiles = (a.n + ROWS - 1) / ROWS, steps = (a.k + 127) / 128;
+  const bool staged = a.m <= 16 && a.m * stage_pitch(a.k) <= kStageBytes;
+  const int mt = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4, nw = mt == 4 ? 8 : 16;
+  // Waves per tile and steps per item: the pair whose longest workgroup has
+  // the fewest steps to walk; longer items and more waves a tile where equal.
+  const bool al16 = aligned16(a.scales);
+  int u = 1, kw = 4;
+  int64_t best = INT64_MAX;
+  for (int uu = mt > 1 ? 1 : staged ? 4 : 2; uu >= 1; uu >>= 1) {
+    if (uu > 1 && (a.k % (128 * uu) != 0 || !al16)) continue;
+    for (int log2 = nw == 16 ? 4 : 3; log2 >= 2; --log2) {
+      const int64_t rounds = ((tiles + (nw >> log2) - 1) / (nw >> log2) + kMatvecGrid - 1) / kMatvecGrid;
+      const int64_t cost = rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2) * uu;
+      if (cost < best) best = cost, u = uu, kw = log2;
+    }
+  }
+  // U = 1 has whole steps too, with a row's word of scales (two for NVFP4) aligned
+  const bool whole = u > 1 || (a.k % 128 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0);
+  const int64_t groups = (tiles + (nw >> kw) - 1) / (nw >> kw), slot = (int64_t)nw * mt * 1024;
+  const int64_t room = (kLds - (staged ? a.m * stage_pitch(a.k) : 0)) / slot;
+  const MvPlan plan{kw, (int)std::min<int64_t>(room, 4)};
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(groups, kMatvecGrid)), dim3(nw * 64), 0, stream, a, plan);
   };
-  if (a.m <= 16) go(matvec_kernel<XT, WT, 1, 1, 8, GATE>, 16, 8);
-  else if (a.m <= 32) go(matvec_kernel<XT, WT, 2, 1, 8, GATE>, 16, 8);
-  else go(matvec_kernel<XT, WT, 4, 1, 8, GATE>, 16, 8);
+  if (staged) {
+    if (u == 4) go(matvec_kernel<XT, WT, 1, 16, 4, GATE, true, true>);
+    else if (u == 2) go(matvec_kernel<XT, WT, 1, 16, 2, GATE, true, true>);
+    else if (whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, true, true>);
+    else go(matvec_kernel<XT, WT, 1, 16, 1, GATE, true, false>);
+  } else if (mt == 1) {
+    if (u == 2) go(matvec_kernel<XT, WT, 1, 16, 2, GATE, false, true>);
+    else if (whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, true>);
+    else go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, false>);
+  } else if (mt == 2) {
+    if (whole) go(matvec_kernel<XT, WT, 2, 16, 1, GATE, false, true>);
+    else go(matvec_kernel<XT, WT, 2, 16, 1, GATE, false, false>);
+  } else {
+    if (whole) go(matvec_kernel<XT, WT, 4, 8, 1, GATE, false, true>);
+    else go(matvec_kernel<XT, WT, 4, 8, 1, GATE, false, false>);
+  }
   return launch_status();
 }
 
