@@ -42,34 +42,70 @@ struct MatvecArgs {
   uint16_t* h;                                           // gated: [m][n]
 };
 
-// Four words of 32 E2M1 codes -> 32 bf16 values times their group scale(s),
-// exact: E2M1 has 2 significant bits, with an E4M3 scale the product has 6.
+// Eight E2M1 codes -> eight bf16 values times their group scale (an E8M0 or
+// E4M3 byte), exact: E2M1 has 2 significant bits, with an E4M3 scale the
+// product has 6.
 template <int WT>
-__device__ __forceinline__ void decode32(const v4i w, uint32_t sc, bf16x8_t (&o)[4]) {
+__device__ __forceinline__ bf16x8_t decode8(uint32_t w, uint32_t sc) {
+  bf16x2_t p[4];
+  if constexpr (WT == kMx) {
+    const float s = __uint_as_float(sc << 23);           // the converter reads the exponent field: 2^(byte - 127)
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+  } else {
+    const f32x2_t d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(sc, 1.0f, false);
+    const float d = d2[0];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    bf16x2_t p[4];
-    if constexpr (WT == kMx) {
-      const float s = __uint_as_float(sc << 23);         // the converter reads the exponent field: 2^(byte - 127)
-      p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[q], s, 0);
-      p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[q], s, 1);
-      p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[q], s, 2);
-      p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[q], s, 3);
-    } else {
-      const f32x2_t d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((q < 2 ? sc : sc >> 8) & 0xFFu, 1.0f, false);
-      const float d = d2[0];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f32x2_t v;
-        if (j == 0) v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[q], 1.0f, 0);
-        else if (j == 1) v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[q], 1.0f, 1);
-        else if (j == 2) v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[q], 1.0f, 2);
-        else v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[q], 1.0f, 3);
-        p[j] = bf16x2_t{(__bf16)__fmul_rn(v[0], d), (__bf16)__fmul_rn(v[1], d)};
-      }
+    for (int j = 0; j < 4; ++j) {
+      f32x2_t v;
+      if (j == 0) v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+      else if (j == 1) v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+      else if (j == 2) v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+      else v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+      p[j] = bf16x2_t{(__bf16)__fmul_rn(v[0], d), (__bf16)__fmul_rn(v[1], d)};
     }
-    o[q] = bf16x8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
   }
+  return bf16x8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+}
+
+// Each of these exchanges a register bit (a: 0, b: 1) with one bit of the lane
+// index: afterwards a lane whose bit is 0 holds its own a and its partner's a,
+// one whose bit is 1 its partner's b and its own b.
+__device__ __forceinline__ void exchange_bit5(uint32_t& a, uint32_t& b) {
+  const auto v = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = v[0]; b = v[1];
+}
+__device__ __forceinline__ void exchange_bit4(uint32_t& a, uint32_t& b) {
+  const auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = v[0]; b = v[1];
+}
+template <int BIT>                                       // 0 or 1: the partner is in the quad
+__device__ __forceinline__ void exchange_quad(uint32_t& a, uint32_t& b, bool set) {
+  constexpr int kPerm = BIT == 0 ? 0xB1 : 0x4E;          // quad_perm [1,0,3,2], [2,3,0,1]
+  const uint32_t pa = (uint32_t)__builtin_amdgcn_mov_dpp((int)a, kPerm, 0xF, 0xF, false);
+  const uint32_t pb = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, kPerm, 0xF, 0xF, false);
+  a = set ? pb : a;
+  b = set ? b : pa;
+}
+
+// The codes of a step as loaded, lane 4 rho + c holding 16-byte piece c of a
+// row, to the products' operand: word q of lane 16 g + r becomes word g of
+// piece q of row r, rho = 4 (r & 3) + (r >> 2).  The four lanes of a row load
+// 64 consecutive bytes: the address unit takes four neighbouring lanes at a
+// time, and loads laid out as the operand (neighbouring lanes: different rows)
+// took four times as long even from the L1.
+__device__ __forceinline__ void to_operand(uint32_t (&c)[4], int lane) {
+  exchange_bit5(c[0], c[2]);
+  exchange_bit5(c[1], c[3]);
+  exchange_bit4(c[0], c[1]);
+  exchange_bit4(c[2], c[3]);
+  const bool b1 = lane & 2, b0 = lane & 1;
+  exchange_quad<1>(c[0], c[2], b1);
+  exchange_quad<1>(c[1], c[3], b1);
+  exchange_quad<0>(c[0], c[1], b0);
+  exchange_quad<0>(c[2], c[3], b0);
 }
 
 // Sixteen E4M3 codes with one E8M0 scale -> two fragments of eight bf16 values.
@@ -85,27 +121,29 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
   b = bf16x8_t{p[4][0], p[4][1], p[5][0], p[5][1], p[6][0], p[6][1], p[7][0], p[7][1]};
 }
 
-// NW waves form a workgroup: sixteen, or eight for four tiles of x rows, whose
-// operands take the registers of two waves.  A tile is 16 rows of W (gated: 8
+// NW waves form a workgroup: sixteen, or eight for three or four tiles of x
+// rows, whose operands take the registers of two waves.  A tile is 16 rows of W (gated: 8
 // of W1 and the same 8 of W3); KW waves share one and split K, the workgroup
 // works on NW / KW tiles at a time and walks groups of them blockIdx.x,
-// blockIdx.x + gridDim.x, ...  A step is 128 values of K: lane (r = lane & 15,
-// g = lane >> 4) holds values 32 g .. 32 g + 31 of the step of W row r and of x
-// row r, which the 16x16x32 bf16 products take eight at a time (both operands
-// list K in the same order).  An item is U consecutive steps; wave kw takes
-// items kw, kw + KW, ... of a tile, and the loads of its next item, across the
-// end of a tile too, are in flight during the products of the current one.
-// No branch surrounds a load: the compiler could not count the outstanding
-// ones and would wait for all.  The partial sums meet in LDS and are added in
-// wave order: deterministic, no atomics, no workspace.
+// blockIdx.x + gridDim.x, ...  A step is 128 values of K; product q = 0 .. 3 of
+// its four 16x16x32 bf16 products takes values 32 q + 8 g .. + 7 in lane (r =
+// lane & 15, g = lane >> 4), row r of W and of x.  An item is U consecutive
+// steps; wave kw takes items kw, kw + KW, ... of a tile, and the loads of its
+// next item, across the end of a tile too, are in flight during the products
+// of the current one.  No branch surrounds a load: the compiler could not
+// count the outstanding ones and would wait for all.  The partial sums meet in
+// LDS and are added in wave order: deterministic, no atomics, no workspace.
 //
-// x is staged once per workgroup in LDS as bf16 where it fits (STAGED: its
-// loads would otherwise carry 64 useful bytes per instruction and row), else
-// each wave loads its part of x with the item.
+// x goes through LDS as bf16: all of it once per workgroup where it fits
+// (STAGED), else each wave brings its own steps, with the item, into a room of
+// its own (no barrier: one wave's LDS accesses keep their order).
 // WHOLE: K is a multiple of U steps and the scales are aligned, so that an
 // item's scale bytes of a row come with one load.
 constexpr int kLds = 160 * 1024;
-constexpr int kStageBytes = 120 * 1024;                  // most of x in LDS; the rest is the partial sums'
+constexpr int kStageBytes = 144 * 1024;                  // most of x in LDS; the rest is the partial sums'
+constexpr int kXPitch = 256 + 16;                        // of a wave's own step of x
+// A wave's own room: 16 MT rows of a step; its partial sums take the same place.
+__host__ __device__ constexpr int room_bytes(int mt) { return 16 * mt * kXPitch; }
 
 // Bytes between staged rows of x: 16 past the rounded row, so that equal
 // columns of neighbouring rows fall into different banks.
@@ -117,18 +155,19 @@ struct MvPlan {
   int batch;                                             // groups of tiles between two meetings of the partial sums
 };
 
-// The scale bytes of an item: WHOLE: a row's bytes for U steps (4 U, NVFP4
-// 8 U); else this lane's own of one step.
-template <int WT, int U>
+// One item of W: a row's scale bytes of the U steps (MXFP4 4 U, NVFP4 8 U), or
+// of a partial step the four that this lane's products take.
+template <int WT, int U, bool WHOLE>
 struct MvItem {
   v4i c[U];
-  uint32_t s[WT == kMx ? U : 2 * U];
+  uint32_t s[!WHOLE ? 4 : WT == kMx ? U : 2 * U];
 };
 
+// One item of x, as loaded: sixteen bytes a lane, 16 (bf16) or 8 (E4M3) lanes a row.
 template <int XT, int MT, int U>
 struct MvX {
-  v4i v[MT][U][XT == kXBf16 ? 4 : 2];
-  uint32_t s[MT][U];
+  v4i v[U][XT == kXBf16 ? 4 * MT : 2 * MT];
+  uint32_t s[U][2 * MT];
 };
 
 // Waits for this wave's LDS accesses and meets the workgroup's other waves;
@@ -139,13 +178,14 @@ template <int XT, int WT, int MT, int NW, int U, bool GATE, bool STAGED, bool WH
 __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan plan) {
   static_assert(WHOLE || U == 1, "a partial step is an item of its own");
   constexpr int ROWS = GATE ? 8 : 16;                    // output columns of a tile
-  constexpr bool AHEAD = !STAGED && MT <= 2;             // x of the next item too
+  constexpr bool AHEAD = !STAGED;                        // x of the next item too
   constexpr int kSlot = NW * MT * 64;                    // partial sums of one group of tiles, in v4f
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
-  v4f* const red = reinterpret_cast<v4f*>(lds);
-  uint8_t* const stage = lds + (uint32_t)plan.batch * (kSlot * 16);
+  constexpr int kWaveFloats = STAGED ? MT * 256 : room_bytes(MT) / 4;   // between two waves' partial sums
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  // the staged x behind the partial sums; or this wave's room
+  uint8_t* const stage = lds + (STAGED ? (uint32_t)plan.batch * (kSlot * 16) : (uint32_t)wave * room_bytes(MT));
   const int kw = wave & ((1 << plan.kw_log2) - 1), rt = wave >> plan.kw_log2, RT = NW >> plan.kw_log2;
   const int64_t kc = a.k >> 1, ks = a.k >> (WT == kMx ? 5 : 4);   // bytes of a row's codes and scales
   const int steps = (int)((a.k + 127) >> 7), items = (steps + U - 1) / U;
@@ -155,17 +195,26 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
       buffer_rsrc(a.x, XT == kXBf16 ? ((a.m - 1) * a.ldx + a.k) * 2 : (int64_t)a.m * a.k);
   const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(a.x_scales, XT == kXBf16 ? 0 : (int64_t)a.m * (a.k >> 5));
 
-  // Row r of a tile: a row past the end reads the last one (its sums are not stored).
-  const auto load_w = [&](MvItem<WT, U>& it, int64_t group, int turn) {
-    const int64_t out = std::min((group * RT + rt) * ROWS + (r & (ROWS - 1)), a.n - 1);
-    const int64_t row = out + (GATE && r >= ROWS ? a.n : 0);
-    const int item = std::min(kw + (turn << plan.kw_log2), items - 1);   // a wave without an item reads the last
-    const uint8_t* const c = a.codes + row * kc;
-    const uint8_t* const s = a.scales + row * ks;
+  // Workgroups that read x from L2 start at different places of K: their
+  // requests would otherwise meet in the few channels that hold one place of
+  // every row (rows of x lie a multiple of 4 KB apart).
+  const int turned = STAGED ? 0 : (int)(blockIdx.x * 7u % (uint32_t)items);
+  // Place in K of the wave's item of a turn (a wave that has none takes the last).
+  const auto item_of = [&](int turn) {
+    const int it = std::min(kw + (turn << plan.kw_log2), items - 1) + turned;
+    return it < items ? it : it - items;
+  };
+  // A row past the end reads the last one (its sums are not stored).
+  const auto row_of = [&](int64_t group, int r) {
+    return std::min((group * RT + rt) * ROWS + (r & (ROWS - 1)), a.n - 1) + (GATE && r >= ROWS ? a.n : 0);
+  };
+  const auto load_w = [&](MvItem<WT, U, WHOLE>& it, int64_t group, int turn) {
+    const int item = item_of(turn), piece = lane & 3;
+    const uint8_t* const c = a.codes + row_of(group, 4 * ((lane >> 2) & 3) + (lane >> 4)) * kc;
+    const uint8_t* const s = a.scales + row_of(group, r) * ks;
     if constexpr (WHOLE) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        it.c[u] = *reinterpret_cast<const v4i*>(c + (item * U + u) * 64 + g * 16);
+      for (int u = 0; u < U; ++u) it.c[u] = *reinterpret_cast<const v4i*>(c + (item * U + u) * 64 + piece * 16);
       constexpr int kBytes = (WT == kMx ? 4 : 8) * U;
       const uint8_t* const p = s + item * kBytes;
       if constexpr (kBytes % 16 == 0) {
@@ -179,40 +228,42 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
         for (int b = 0; b < kBytes / 4; ++b) it.s[b] = reinterpret_cast<const uint32_t*>(p)[b];
       }
     } else {
-      const int kb = item * 4 + g;                       // a block of 32 values is whole or absent
-      const bool in = kb * 32 < (int)a.k;
-      const int at = in ? kb : 0;
-      const v4i v = *reinterpret_cast<const v4i*>(c + at * 16);
-      uint32_t sc;
-      if constexpr (WT == kMx) sc = s[at];
-      else sc = *reinterpret_cast<const uint16_t*>(s + 2 * at);
-      it.c[0] = in ? v : v4i{0, 0, 0, 0};
-      it.s[0] = in ? sc : 0;
+      const int blocks = (int)(a.k >> 5), kb = item * 4;  // a block of 32 values is whole or absent
+      const v4i v = *reinterpret_cast<const v4i*>(c + std::min(kb + piece, blocks - 1) * 16);
+      it.c[0] = kb + piece < blocks ? v : v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int at = std::min(kb + q, blocks - 1);
+        it.s[q] = WT == kMx ? s[at] : s[2 * at + (g >> 1)];
+      }
     }
   };
   const auto load_x = [&](MvX<XT, MT, U>& it, int turn) {
-    const int item = std::min(kw + (turn << plan.kw_log2), items - 1);
+    const int item = item_of(turn);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int u = 0; u < U; ++u) {
+      const uint32_t k0 = (uint32_t)(item * U + u) * 128;
+      if constexpr (XT == kXBf16) {
+        const uint32_t at = k0 + 8 * (lane & 15);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t kb = (uint32_t)(item * U + u) * 4 + g;
-        const int row = 16 * i + r;
-        const bool ok = kb * 32 < (uint32_t)a.k && row < a.m;
-        if constexpr (XT == kXBf16) {
-          const uint32_t off = ok ? ((uint32_t)row * (uint32_t)a.ldx + kb * 32) * 2 : kOffNone;
+        for (int j = 0; j < 4 * MT; ++j) {
+          const int row = 4 * j + (lane >> 4);
+          const uint32_t off = row < a.m && at < (uint32_t)a.k ? ((uint32_t)row * (uint32_t)a.ldx + at) * 2 : kOffNone;
+          it.v[u][j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off, 0, 0));
+        }
+      } else {
+        const uint32_t at = k0 + 16 * (lane & 7);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            it.v[i][u][q] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off + 16 * q, 0, 0));
-        } else {
-          const uint32_t off = ok ? (uint32_t)row * (uint32_t)a.k + kb * 32 : kOffNone;
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            it.v[i][u][q] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off + 16 * q, 0, 0));
-          it.s[i][u] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-              rxs, ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + kb : kOffNone, 0, 0);
+        for (int j = 0; j < 2 * MT; ++j) {
+          const int row = 8 * j + (lane >> 3);
+          const bool ok = row < a.m && at < (uint32_t)a.k;
+          it.v[u][j] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? (uint32_t)row * (uint32_t)a.k + at : kOffNone, 0, 0));
+          it.s[u][j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+              rxs, ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + (at >> 5) : kOffNone, 0, 0);
         }
       }
+    }
   };
 
   v4f acc[MT];
@@ -220,31 +271,45 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   };
-  const uint32_t xrow = STAGED ? (uint32_t)(r < a.m ? r : 0) * (uint32_t)stage_pitch(a.k) + g * 64 : 0;
-  const auto multiply = [&](const MvItem<WT, U>& it, const MvX<XT, MT, U>& xi, int turn) {
-    const int item = kw + (turn << plan.kw_log2);
-    if (item >= items) return;                           // wave-uniform
+  const uint32_t xrow = (STAGED ? (uint32_t)(r < a.m ? r : 0) * (uint32_t)stage_pitch(a.k) : (uint32_t)r * kXPitch) + g * 16;
+  const auto multiply = [&](const MvItem<WT, U, WHOLE>& it, const MvX<XT, MT, U>& xi, int turn) {
+    if (kw + (turn << plan.kw_log2) >= items) return;    // wave-uniform
+    const int item = item_of(turn);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      bf16x8_t x[MT][4], w[4];
+      if constexpr (!STAGED) {                           // this step of x into the wave's room
+        if constexpr (XT == kXBf16) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        if constexpr (STAGED) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            x[i][q] = *reinterpret_cast<const bf16x8_t*>(stage + xrow + (uint32_t)(item * U + u) * 256 + 16 * q);
-        } else if constexpr (XT == kXBf16) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) x[i][q] = __builtin_bit_cast(bf16x8_t, xi.v[i][u][q]);
+          for (int j = 0; j < 4 * MT; ++j)
+            *reinterpret_cast<v4i*>(stage + (4 * j + (lane >> 4)) * kXPitch + (lane & 15) * 16) = xi.v[u][j];
         } else {
-          decode_x16(xi.v[i][u][0], xi.s[i][u], x[i][0], x[i][1]);
-          decode_x16(xi.v[i][u][1], xi.s[i][u], x[i][2], x[i][3]);
+#pragma unroll
+          for (int j = 0; j < 2 * MT; ++j) {
+            bf16x8_t lo, hi;
+            decode_x16(xi.v[u][j], xi.s[u][j], lo, hi);
+            bf16x8_t* const p = reinterpret_cast<bf16x8_t*>(stage + (8 * j + (lane >> 3)) * kXPitch + (lane & 7) * 32);
+            p[0] = lo;
+            p[1] = hi;
+          }
         }
       }
-      uint32_t sc = it.s[u];
-      if constexpr (WHOLE && WT == kMx) sc = (sc >> (8 * g)) & 0xFFu;
-      if constexpr (WHOLE && WT == kNv) sc = ((g & 2) ? it.s[2 * u + 1] : it.s[2 * u]) >> (16 * (g & 1));
-      decode32<WT>(it.c[u], sc, w);
+      bf16x8_t x[MT][4], w[4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          x[i][q] = *reinterpret_cast<const bf16x8_t*>(
+              stage + xrow + (STAGED ? (uint32_t)(item * U + u) * 256 : (uint32_t)i * 16 * kXPitch) + 64 * q);
+      uint32_t c[4] = {(uint32_t)it.c[u][0], (uint32_t)it.c[u][1], (uint32_t)it.c[u][2], (uint32_t)it.c[u][3]};
+      to_operand(c, lane);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t sc;                                     // the scale byte of product q's values
+        if constexpr (!WHOLE) sc = it.s[q];
+        else if constexpr (WT == kMx) sc = it.s[u] >> (8 * q);
+        else sc = it.s[2 * u + (q >> 1)] >> (16 * (q & 1) + 8 * (g >> 1));
+        w[q] = decode8<WT>(c[q], sc & 0xFFu);
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -252,7 +317,7 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     }
   };
   // lane l of a partial tile holds rows 4 (l >> 4) .. + 3 of W against row l & 15 of x
-  const float* const rf = reinterpret_cast<const float*>(red);
+  const float* const rf = reinterpret_cast<const float*>(lds);
   const auto finish = [&](int64_t group, int slots) {     // group: the first one since the last meeting
     lds_barrier();
     const int count = slots * RT * MT * (16 * ROWS);
@@ -266,9 +331,9 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
       const int64_t row = ((group + (int64_t)slot * gridDim.x) * RT + t) * ROWS + nl;
       if (mr >= a.m || row >= a.n) continue;
       const auto total = [&](int wr) {
-        const float* p = rf + ((slot * NW + (t << plan.kw_log2)) * MT + i) * 256 + ((wr >> 2) * 16 + ml) * 4 + (wr & 3);
+        const float* p = rf + (slot * NW + (t << plan.kw_log2)) * kWaveFloats + i * 256 + ((wr >> 2) * 16 + ml) * 4 + (wr & 3);
         float v = 0.0f;
-        for (int w = 0; w < 1 << plan.kw_log2; ++w) v = __fadd_rn(v, p[w * (MT * 256)]);
+        for (int w = 0; w < 1 << plan.kw_log2; ++w) v = __fadd_rn(v, p[w * kWaveFloats]);
         return v;
       };
       if constexpr (GATE) {
@@ -287,7 +352,7 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     lds_barrier();                                       // the partial sums' room is free again
   };
 
-  MvItem<WT, U> w0, w1;
+  MvItem<WT, U, WHOLE> w0, w1;
   MvX<XT, MT, U> x0, x1;
   const int64_t first = blockIdx.x;
   load_w(w0, first, 0);
@@ -325,12 +390,13 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     if (++tn == per) { tn = 0; gr += gridDim.x; }
   };
   // the products of an item; at a tile's end its sums go to LDS, and every `batch` tiles and at the end they meet
-  const auto use = [&](const MvItem<WT, U>& w, const MvX<XT, MT, U>& x) {
+  const auto use = [&](const MvItem<WT, U, WHOLE>& w, const MvX<XT, MT, U>& x) {
     multiply(w, x, turn);
     --left;
     if (turn + 1 == per) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) red[slots * kSlot + (wave * MT + i) * 64 + lane] = acc[i];
+      for (int i = 0; i < MT; ++i)
+        reinterpret_cast<v4f*>(lds)[(slots * NW + wave) * (kWaveFloats / 4) + i * 64 + lane] = acc[i];
       clear();
       if (++slots == plan.batch || left == 0) {
         finish(met, slots);
@@ -340,29 +406,22 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     }
     advance(group, turn);
   };
-  const auto ahead = [&](MvItem<WT, U>& w, MvX<XT, MT, U>& x) {   // loads of the item after the current one
+  const auto ahead = [&](MvItem<WT, U, WHOLE>& w, MvX<XT, MT, U>& x) {   // loads of the item after the current one
     int64_t gr = group;
     int tn = turn;
     advance(gr, tn);
     load_w(w, gr, tn);
     if constexpr (AHEAD) load_x(x, tn);
   };
-  const auto now = [&](MvX<XT, MT, U>& x) {
-    if constexpr (!STAGED && !AHEAD) load_x(x, turn);
-  };
   while (left > 2) {
-    now(x0);
     ahead(w1, x1);
     use(w0, x0);
-    now(x1);
     ahead(w0, x0);
     use(w1, x1);
   }
-  now(x0);
   if (left == 2) {
     ahead(w1, x1);
     use(w0, x0);
-    now(x1);
     use(w1, x1);
   } else {
     use(w0, x0);
@@ -391,7 +450,7 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   constexpr int ROWS = GATE ? 8 : 16;
   const int64_t tiles = (a.n + ROWS - 1) / ROWS, steps = (a.k + 127) / 128;
   const bool staged = a.m <= 16 && a.m * stage_pitch(a.k) <= kStageBytes;
-  const int mt = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4, nw = mt == 4 ? 8 : 16;
+  const int mt = (a.m + 15) / 16, nw = mt > 2 ? 8 : 16;
   // Waves per tile and steps per item: the pair whose longest workgroup has
   // the fewest steps to walk; longer items and more waves a tile where equal.
   const bool al16 = aligned16(a.scales);
@@ -408,8 +467,7 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   // U = 1 has whole steps too, with a row's word of scales (two for NVFP4) aligned
   const bool whole = u > 1 || (a.k % 128 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0);
   const int64_t groups = (tiles + (nw >> kw) - 1) / (nw >> kw), slot = (int64_t)nw * mt * 1024;
-  const int64_t room = (kLds - (staged ? a.m * stage_pitch(a.k) : 0)) / slot;
-  const MvPlan plan{kw, (int)std::min<int64_t>(room, 4)};
+  const MvPlan plan{kw, staged ? (int)std::min<int64_t>((kLds - a.m * stage_pitch(a.k)) / slot, 4) : 1};
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(groups, kMatvecGrid)), dim3(nw * 64), 0, stream, a, plan);
   };
@@ -425,6 +483,9 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   } else if (mt == 2) {
     if (whole) go(matvec_kernel<XT, WT, 2, 16, 1, GATE, false, true>);
     else go(matvec_kernel<XT, WT, 2, 16, 1, GATE, false, false>);
+  } else if (mt == 3) {
+    if (whole) go(matvec_kernel<XT, WT, 3, 8, 1, GATE, false, true>);
+    else go(matvec_kernel<XT, WT, 3, 8, 1, GATE, false, false>);
   } else {
     if (whole) go(matvec_kernel<XT, WT, 4, 8, 1, GATE, false, true>);
     else go(matvec_kernel<XT, WT, 4, 8, 1, GATE, false, false>);
