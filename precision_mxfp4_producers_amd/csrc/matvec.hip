@@ -121,7 +121,7 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
   b = bf16x8_t{p[4][0], p[4][1], p[5][0], p[5][1], p[6][0], p[6][1], p[7][0], p[7][1]};
 }
 
-// NW waves form a workgroup: sixteen, or eight for three or four tiles of x
+// NW waves form a workgroup: sixteen, or eight for more than one tile of x
 // rows, whose operands take the registers of two waves.  A tile is 16 rows of W (gated: 8
 // of W1 and the same 8 of W3); KW waves share one and split K, the workgroup
 // works on NW / KW tiles at a time and walks groups of them blockIdx.x,
@@ -140,7 +140,7 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
 // WHOLE: K is a multiple of U steps and the scales are aligned, so that an
 // item's scale bytes of a row come with one load.
 constexpr int kLds = 160 * 1024;
-constexpr int kStageBytes = 144 * 1024;                  // most of x in LDS; the rest is the partial sums'
+constexpr int kStageBytes = 143 * 1024;                  // most of x in LDS; the rest is the partial sums'
 constexpr int kXPitch = 256 + 16;                        // of a wave's own step of x
 // A wave's own room: 16 MT rows of a step; its partial sums take the same place.
 __host__ __device__ constexpr int room_bytes(int mt) { return 16 * mt * kXPitch; }
@@ -179,13 +179,12 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
   static_assert(WHOLE || U == 1, "a partial step is an item of its own");
   constexpr int ROWS = GATE ? 8 : 16;                    // output columns of a tile
   constexpr bool AHEAD = !STAGED;                        // x of the next item too
-  constexpr int kSlot = NW * MT * 64;                    // partial sums of one group of tiles, in v4f
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
-  constexpr int kWaveFloats = STAGED ? MT * 256 : room_bytes(MT) / 4;   // between two waves' partial sums
+  constexpr int kWaveFloats = STAGED ? MT * 256 + 4 : room_bytes(MT) / 4;   // between two waves' partial sums
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   // the staged x behind the partial sums; or this wave's room
-  uint8_t* const stage = lds + (STAGED ? (uint32_t)plan.batch * (kSlot * 16) : (uint32_t)wave * room_bytes(MT));
+  uint8_t* const stage = lds + (STAGED ? (uint32_t)plan.batch * (NW * kWaveFloats * 4) : (uint32_t)wave * room_bytes(MT));
   const int kw = wave & ((1 << plan.kw_log2) - 1), rt = wave >> plan.kw_log2, RT = NW >> plan.kw_log2;
   const int64_t kc = a.k >> 1, ks = a.k >> (WT == kMx ? 5 : 4);   // bytes of a row's codes and scales
   const int steps = (int)((a.k + 127) >> 7), items = (steps + U - 1) / U;
@@ -267,10 +266,6 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
   };
 
   v4f acc[MT];
-  const auto clear = [&] {
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  };
   const uint32_t xrow = (STAGED ? (uint32_t)(r < a.m ? r : 0) * (uint32_t)stage_pitch(a.k) : (uint32_t)r * kXPitch) + g * 16;
   const auto multiply = [&](const MvItem<WT, U, WHOLE>& it, const MvX<XT, MT, U>& xi, int turn) {
     if (kw + (turn << plan.kw_log2) >= items) return;    // wave-uniform
@@ -316,116 +311,162 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
         for (int i = 0; i < MT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[q], x[i][q], acc[i], 0, 0, 0);
     }
   };
-  // lane l of a partial tile holds rows 4 (l >> 4) .. + 3 of W against row l & 15 of x
+  // Lane l of a partial tile holds rows 4 (l >> 4) .. + 3 of W against row l &
+  // 15 of x.  Four partial sums a thread, then the threads of one sum (KW / 4
+  // neighbouring lanes, in lane order); gated: the sums of a and b lie in
+  // neighbouring groups of lanes.
   const float* const rf = reinterpret_cast<const float*>(lds);
   const auto finish = [&](int64_t group, int slots) {     // group: the first one since the last meeting
     lds_barrier();
-    const int count = slots * RT * MT * (16 * ROWS);
-    for (int e = threadIdx.x; e < count; e += NW * 64) {
-      const int nl = e & (ROWS - 1), ml = (e / ROWS) & 15;
-      int rest = e / (16 * ROWS);
-      const int i = rest % MT;
-      rest /= MT;
-      const int t = rest & (RT - 1), slot = rest / RT;
-      const int mr = 16 * i + ml;
+    const int split = plan.kw_log2 - 2, sums = 16 * a.m;  // of a tile: 16 rows of W, m rows of x
+    const int count = (slots * RT * sums) << split;
+    for (int e0 = wave * 64; e0 < count; e0 += NW * 64) {
+      const int e = e0 + lane, part = e & ((1 << split) - 1);
+      int q = std::min(e >> split, slots * RT * sums - 1);   // a last wave's spare lanes repeat the last sum
+      const int ab = GATE ? q & 1 : 0;
+      if (GATE) q >>= 1;
+      const int nl = q & (ROWS - 1);
+      q /= ROWS;
+      const int mr = (int)((uint32_t)q % (uint32_t)a.m);
+      q = (int)((uint32_t)q / (uint32_t)a.m);
+      const int t = q & (RT - 1), slot = q / RT, wr = nl + ROWS * ab;
+      const float* const p = rf + (slot * NW + (t << plan.kw_log2) + 4 * part) * kWaveFloats + (mr >> 4) * 256 +
+                             ((wr >> 2) * 16 + (mr & 15)) * 4 + (wr & 3);
+      float v = __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[kWaveFloats]), p[2 * kWaveFloats]), p[3 * kWaveFloats]);
+      for (int s = 1; s < 1 << split; s <<= 1) v = __fadd_rn(v, __shfl_xor(v, s, 64));
       const int64_t row = ((group + (int64_t)slot * gridDim.x) * RT + t) * ROWS + nl;
-      if (mr >= a.m || row >= a.n) continue;
-      const auto total = [&](int wr) {
-        const float* p = rf + (slot * NW + (t << plan.kw_log2)) * kWaveFloats + i * 256 + ((wr >> 2) * 16 + ml) * 4 + (wr & 3);
-        float v = 0.0f;
-        for (int w = 0; w < 1 << plan.kw_log2; ++w) v = __fadd_rn(v, p[w * kWaveFloats]);
-        return v;
-      };
       if constexpr (GATE) {
-        const float av = bf16_bits_to_f32(f32_to_bf16_rne(total(nl)));
-        const float bv = bf16_bits_to_f32(f32_to_bf16_rne(total(nl + ROWS)));
-        float sig, s;
-        sigmoid_silu(av, sig, s);
-        a.h[mr * a.n + row] = (uint16_t)f32_to_bf16_rne(__fmul_rn(s, bv));
-      } else {
-        float v = total(nl);
+        const float other = __shfl_xor(v, 1 << split, 64);
+        const float av = bf16_bits_to_f32(f32_to_bf16_rne(ab ? other : v));
+        const float bv = bf16_bits_to_f32(f32_to_bf16_rne(ab ? v : other));
+        float sig, sl;
+        sigmoid_silu(av, sig, sl);
+        if (e < count && part == 0 && ab == 0 && row < a.n) a.h[mr * a.n + row] = (uint16_t)f32_to_bf16_rne(__fmul_rn(sl, bv));
+      } else if (e < count && part == 0 && row < a.n) {
         if constexpr (WT == kNv) v = __fmul_rn(a.factors[(row >> 8) * a.factor_stride], v);
-        float* p = a.c + mr * a.ldc + row;
-        *p = a.accumulate ? __fadd_rn(*p, v) : v;
+        float* const c = a.c + mr * a.ldc + row;
+        *c = a.accumulate ? __fadd_rn(*c, v) : v;
       }
     }
     lds_barrier();                                       // the partial sums' room is free again
   };
 
-  MvItem<WT, U, WHOLE> w0, w1;
-  MvX<XT, MT, U> x0, x1;
+  // The workgroup's items in order: (group, turn), the same count for every
+  // wave, so that all reach the barriers.
   const int64_t first = blockIdx.x;
-  load_w(w0, first, 0);
-  if constexpr (AHEAD) load_x(x0, 0);
-  if constexpr (STAGED) {
-    const int chunks = steps * 16;                       // of eight values, zero past k
-    const uint32_t pitch = (uint32_t)stage_pitch(a.k);
-    for (int row = 0; row < a.m; ++row)
-      for (int c = threadIdx.x; c < chunks; c += NW * 64) {
-        v4i o;
-        const bool ok = c * 8 < a.k;
-        if constexpr (XT == kXBf16) {
-          o = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
-                                          rx, ok ? ((uint32_t)row * (uint32_t)a.ldx + c * 8) * 2 : kOffNone, 0, 0));
-        } else {
-          typedef int v2i __attribute__((ext_vector_type(2)));
-          const v2i v = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(
-                                                    rx, ok ? (uint32_t)row * (uint32_t)a.k + c * 8 : kOffNone, 0, 0));
-          const uint32_t sc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-              rxs, ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + (c >> 2) : kOffNone, 0, 0);
-          bf16x8_t lo, unused;
-          decode_x16(v4i{v.x, v.y, 0, 0}, sc, lo, unused);
-          o = __builtin_bit_cast(v4i, lo);
-        }
-        *reinterpret_cast<v4i*>(stage + row * pitch + c * 16) = o;
-      }
-    lds_barrier();
-  }
-  clear();
-  // the workgroup's items in order: (group, turn), the same count for every wave, so that all reach the barriers
   int64_t left = (groups - first + gridDim.x - 1) / gridDim.x * per;
-  int64_t group = first, met = first;
+  int64_t group = first;                                 // of the current item
   int turn = 0, slots = 0;
-  const auto advance = [&](int64_t& gr, int& tn) {
+  const auto step = [&](int64_t& gr, int& tn) {
     if (++tn == per) { tn = 0; gr += gridDim.x; }
   };
-  // the products of an item; at a tile's end its sums go to LDS, and every `batch` tiles and at the end they meet
-  const auto use = [&](const MvItem<WT, U, WHOLE>& w, const MvX<XT, MT, U>& x) {
-    multiply(w, x, turn);
-    --left;
-    if (turn + 1 == per) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        reinterpret_cast<v4f*>(lds)[(slots * NW + wave) * (kWaveFloats / 4) + i * 64 + lane] = acc[i];
-      clear();
-      if (++slots == plan.batch || left == 0) {
-        finish(met, slots);
-        slots = 0;
-        met = group + gridDim.x;
-      }
-    }
-    advance(group, turn);
-  };
-  const auto ahead = [&](MvItem<WT, U, WHOLE>& w, MvX<XT, MT, U>& x) {   // loads of the item after the current one
+  using W = MvItem<WT, U, WHOLE>;
+  using X = MvX<XT, MT, U>;
+  const auto ahead = [&](W& w, X& x) {                   // loads of the item after the current one
     int64_t gr = group;
     int tn = turn;
-    advance(gr, tn);
+    step(gr, tn);
     load_w(w, gr, tn);
-    if constexpr (AHEAD) load_x(x, tn);
+    if constexpr (!STAGED) load_x(x, tn);
   };
-  while (left > 2) {
-    ahead(w1, x1);
-    use(w0, x0);
-    ahead(w0, x0);
-    use(w1, x1);
-  }
-  if (left == 2) {
-    ahead(w1, x1);
-    use(w0, x0);
-    use(w1, x1);
-  } else {
-    use(w0, x0);
-  }
+  const auto use = [&](const W& w, const X& x) {         // the products of an item; at a tile's end its sums go to LDS
+    multiply(w, x, turn);
+    if (turn + 1 == per) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        reinterpret_cast<v4f*>(lds)[(slots * NW + wave) * (kWaveFloats / 4) + i * 64 + lane] = acc[i];
+        acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      ++slots;
+    }
+    step(group, turn);
+  };
+  // Stages x in chunks of eight values, zero past k: a thread takes every (64
+  // NW)-th, B loads in flight.  W's first loads go out behind the first B, so
+  // that waiting for those does not wait for these.
+  const auto stage_x = [&](auto b, auto&& behind) {
+    constexpr int B = b();
+    const int chunks = steps * 16, drow = NW * 64 / chunks, dc = NW * 64 - drow * chunks;
+    const uint32_t pitch = (uint32_t)stage_pitch(a.k);
+    int row = (int)threadIdx.x / chunks, c = (int)threadIdx.x - row * chunks;
+    const int passes = (a.m * chunks + NW * 64 * B - 1) / (NW * 64 * B);
+    const auto pass = [&](auto&& then) {
+      v4i v[B];
+      uint32_t sc[B], at[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const bool ok = row < a.m && c * 8 < a.k;
+        at[j] = row < a.m ? (uint32_t)row * pitch + c * 16 : 0xFFFFFFFFu;
+        if constexpr (XT == kXBf16) {
+          v[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rx, ok ? ((uint32_t)row * (uint32_t)a.ldx + c * 8) * 2 : kOffNone, 0, 0));
+        } else {
+          typedef int v2i __attribute__((ext_vector_type(2)));
+          const v2i y = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(
+                                                    rx, ok ? (uint32_t)row * (uint32_t)a.k + c * 8 : kOffNone, 0, 0));
+          v[j] = v4i{y.x, y.y, 0, 0};
+          sc[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+              rxs, ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + (c >> 2) : kOffNone, 0, 0);
+        }
+        c += dc;
+        row += drow;
+        if (c >= chunks) c -= chunks, ++row;
+      }
+      then();
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        if constexpr (XT == kXE4m3) {
+          bf16x8_t lo, unused;
+          decode_x16(v[j], sc[j], lo, unused);
+          v[j] = __builtin_bit_cast(v4i, lo);
+        }
+        if (at[j] != 0xFFFFFFFFu) *reinterpret_cast<v4i*>(stage + at[j]) = v[j];
+      }
+    };
+    pass(behind);
+    for (int p = 1; p < passes; ++p) pass([] {});
+    lds_barrier();
+  };
+  const auto begin = [&](auto&& loads) {
+    if constexpr (STAGED) {
+      if (a.m * steps * 16 <= NW * 64) stage_x(std::integral_constant<int, 1>{}, loads);
+      else stage_x(std::integral_constant<int, 8>{}, loads);
+    } else {
+      loads();
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  W w0, w1;
+  X x0, x1;
+  begin([&] {
+    load_w(w0, first, 0);
+    if constexpr (!STAGED) load_x(x0, 0);
+  });
+  // One stretch of items up to a meeting of the sums, its first in p, in pairs
+  // so that each item has registers of its own; true where it was odd: the next
+  // item is in q then.  Loads past the last item go to the last row, unused.
+  const int64_t stretch = (int64_t)plan.batch * per;
+  const auto run = [&](W& p, X& xp, W& q, X& xq) {
+    int64_t n = std::min(left, stretch);
+    const int64_t met = group;
+    left -= n;
+    for (; n >= 2; n -= 2) {
+      ahead(q, xq);
+      use(p, xp);
+      ahead(p, xp);
+      use(q, xq);
+    }
+    if (n) {
+      ahead(q, xq);
+      use(p, xp);
+    }
+    finish(met, slots);
+    slots = 0;
+    return n != 0;
+  };
+  while (left > 0)
+    if (run(w0, x0, w1, x1) && left > 0) run(w1, x1, w0, x0);
 }
 
 // C (+)= 0 for an empty reduction.
@@ -450,13 +491,14 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   constexpr int ROWS = GATE ? 8 : 16;
   const int64_t tiles = (a.n + ROWS - 1) / ROWS, steps = (a.k + 127) / 128;
   const bool staged = a.m <= 16 && a.m * stage_pitch(a.k) <= kStageBytes;
-  const int mt = (a.m + 15) / 16, nw = mt > 2 ? 8 : 16;
+  const int mt = (a.m + 15) / 16, nw = mt > 1 ? 8 : 16;
   // Waves per tile and steps per item: the pair whose longest workgroup has
   // the fewest steps to walk; longer items and more waves a tile where equal.
   const bool al16 = aligned16(a.scales);
   int u = 1, kw = 4;
   int64_t best = INT64_MAX;
-  for (int uu = mt > 1 ? 1 : staged ? 4 : 2; uu >= 1; uu >>= 1) {
+  constexpr int kMaxU = WT == kMx ? 4 : 2, kMaxUDirect = XT == kXE4m3 ? 2 : 1;   // what the registers hold
+  for (int uu = staged ? kMaxU : mt == 1 ? kMaxUDirect : 1; uu >= 1; uu >>= 1) {
     if (uu > 1 && (a.k % (128 * uu) != 0 || !al16)) continue;
     for (int log2 = nw == 16 ? 4 : 3; log2 >= 2; --log2) {
       const int64_t rounds = ((tiles + (nw >> log2) - 1) / (nw >> log2) + kMatvecGrid - 1) / kMatvecGrid;
@@ -466,23 +508,26 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   }
   // U = 1 has whole steps too, with a row's word of scales (two for NVFP4) aligned
   const bool whole = u > 1 || (a.k % 128 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0);
-  const int64_t groups = (tiles + (nw >> kw) - 1) / (nw >> kw), slot = (int64_t)nw * mt * 1024;
+  const int64_t groups = (tiles + (nw >> kw) - 1) / (nw >> kw), slot = (int64_t)nw * (mt * 256 + 4) * 4;
+  // groups of tiles between two meetings of the sums: what LDS holds beside x
   const MvPlan plan{kw, staged ? (int)std::min<int64_t>((kLds - a.m * stage_pitch(a.k)) / slot, 4) : 1};
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(groups, kMatvecGrid)), dim3(nw * 64), 0, stream, a, plan);
   };
   if (staged) {
-    if (u == 4) go(matvec_kernel<XT, WT, 1, 16, 4, GATE, true, true>);
-    else if (u == 2) go(matvec_kernel<XT, WT, 1, 16, 2, GATE, true, true>);
-    else if (whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, true, true>);
-    else go(matvec_kernel<XT, WT, 1, 16, 1, GATE, true, false>);
+    if (u == 2) go(matvec_kernel<XT, WT, 1, 16, 2, GATE, true, true>);
+    else if (u == 1 && whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, true, true>);
+    else if (u == 1) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, true, false>);
+    if constexpr (kMaxU == 4)
+      if (u == 4) go(matvec_kernel<XT, WT, 1, 16, 4, GATE, true, true>);
   } else if (mt == 1) {
-    if (u == 2) go(matvec_kernel<XT, WT, 1, 16, 2, GATE, false, true>);
-    else if (whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, true>);
-    else go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, false>);
+    if (u == 1 && whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, true>);
+    else if (u == 1) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, false>);
+    if constexpr (kMaxUDirect == 2)
+      if (u == 2) go(matvec_kernel<XT, WT, 1, 16, 2, GATE, false, true>);
   } else if (mt == 2) {
-    if (whole) go(matvec_kernel<XT, WT, 2, 16, 1, GATE, false, true>);
-    else go(matvec_kernel<XT, WT, 2, 16, 1, GATE, false, false>);
+    if (whole) go(matvec_kernel<XT, WT, 2, 8, 1, GATE, false, true>);
+    else go(matvec_kernel<XT, WT, 2, 8, 1, GATE, false, false>);
   } else if (mt == 3) {
     if (whole) go(matvec_kernel<XT, WT, 3, 8, 1, GATE, false, true>);
     else go(matvec_kernel<XT, WT, 3, 8, 1, GATE, false, false>);
