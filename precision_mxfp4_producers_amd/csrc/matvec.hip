@@ -42,21 +42,19 @@ struct MatvecArgs {
   uint16_t* h;                                           // gated: [m][n]
 };
 
-// Eight E2M1 codes -> eight bf16 values times their group scale (an E8M0 or
-// E4M3 byte), exact: E2M1 has 2 significant bits, with an E4M3 scale the
+// Eight E2M1 codes -> eight bf16 values times their group scale (MXFP4: a power
+// of two, of which the converter reads the exponent field; NVFP4: the value of
+// an E4M3 byte), exact: E2M1 has 2 significant bits, with an E4M3 scale the
 // product has 6.
 template <int WT>
-__device__ __forceinline__ bf16x8_t decode8(uint32_t w, uint32_t sc) {
+__device__ __forceinline__ bf16x8_t decode8(uint32_t w, float s) {
   bf16x2_t p[4];
   if constexpr (WT == kMx) {
-    const float s = __uint_as_float(sc << 23);           // the converter reads the exponent field: 2^(byte - 127)
     p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
     p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
     p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
     p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
   } else {
-    const f32x2_t d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(sc, 1.0f, false);
-    const float d = d2[0];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f32x2_t v;
@@ -64,7 +62,7 @@ __device__ __forceinline__ bf16x8_t decode8(uint32_t w, uint32_t sc) {
       else if (j == 1) v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
       else if (j == 2) v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
       else v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-      p[j] = bf16x2_t{(__bf16)__fmul_rn(v[0], d), (__bf16)__fmul_rn(v[1], d)};
+      p[j] = bf16x2_t{(__bf16)__fmul_rn(v[0], s), (__bf16)__fmul_rn(v[1], s)};
     }
   }
   return bf16x8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
@@ -81,13 +79,46 @@ __device__ __forceinline__ void exchange_bit4(uint32_t& a, uint32_t& b) {
   const auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
   a = v[0]; b = v[1];
 }
-template <int BIT>                                       // 0 or 1: the partner is in the quad
-__device__ __forceinline__ void exchange_quad(uint32_t& a, uint32_t& b, bool set) {
-  constexpr int kPerm = BIT == 0 ? 0xB1 : 0x4E;          // quad_perm [1,0,3,2], [2,3,0,1]
-  const uint32_t pa = (uint32_t)__builtin_amdgcn_mov_dpp((int)a, kPerm, 0xF, 0xF, false);
-  const uint32_t pb = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, kPerm, 0xF, 0xF, false);
-  a = set ? pb : a;
-  b = set ? b : pa;
+// Two such exchanges with bit BIT (0 or 1: the partner is in the quad): one
+// conditional move a result, its other operand read across the quad, which the
+// compiler makes two of.  low: the lanes whose bit is 0.  The nop covers the
+// two cycles that a lane-crossing read needs behind a write of its source.
+template <int BIT>
+__device__ __forceinline__ void exchange_quad(uint32_t& a0, uint32_t& b0, uint32_t& a1, uint32_t& b1) {
+  constexpr uint64_t low = BIT == 0 ? 0x5555555555555555ull : 0x3333333333333333ull;
+  uint32_t oa0, ob0, oa1, ob1;
+#define MX_QUAD(PERM)                                                                  \
+  asm("s_nop 1\n\t"                                                                    \
+      "s_mov_b64 vcc, %8\n\t"                                                          \
+      "v_cndmask_b32_dpp %0, %5, %4, vcc quad_perm:" PERM " row_mask:0xf bank_mask:0xf\n\t" \
+      "v_cndmask_b32_dpp %2, %7, %6, vcc quad_perm:" PERM " row_mask:0xf bank_mask:0xf\n\t" \
+      "s_not_b64 vcc, vcc\n\t"                                                         \
+      "v_cndmask_b32_dpp %1, %4, %5, vcc quad_perm:" PERM " row_mask:0xf bank_mask:0xf\n\t" \
+      "v_cndmask_b32_dpp %3, %6, %7, vcc quad_perm:" PERM " row_mask:0xf bank_mask:0xf"     \
+      : "=&v"(oa0), "=&v"(ob0), "=&v"(oa1), "=&v"(ob1)                                 \
+      : "v"(a0), "v"(b0), "v"(a1), "v"(b1), "s"(low)                                   \
+      : "vcc", "scc")
+  if constexpr (BIT == 0) MX_QUAD("[1,0,3,2]");
+  else MX_QUAD("[2,3,0,1]");
+#undef MX_QUAD
+  a0 = oa0; b0 = ob0; a1 = oa1; b1 = ob1;
+}
+
+// Byte Q of a word as an E8M0 scale: its bits at the exponent's place.
+template <int Q>
+__device__ __forceinline__ float e8m0_byte(uint32_t w) {
+  uint32_t o;
+  const uint32_t sh = 23;
+#define MX_BYTE(SEL)                                                                                      \
+  asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:" SEL \
+      : "=v"(o)                                                                                           \
+      : "v"(sh), "v"(w))
+  if constexpr (Q == 0) MX_BYTE("BYTE_0");
+  else if constexpr (Q == 1) MX_BYTE("BYTE_1");
+  else if constexpr (Q == 2) MX_BYTE("BYTE_2");
+  else MX_BYTE("BYTE_3");
+#undef MX_BYTE
+  return __uint_as_float(o);
 }
 
 // The codes of a step as loaded, lane 4 rho + c holding 16-byte piece c of a
@@ -96,16 +127,13 @@ __device__ __forceinline__ void exchange_quad(uint32_t& a, uint32_t& b, bool set
 // 64 consecutive bytes: the address unit takes four neighbouring lanes at a
 // time, and loads laid out as the operand (neighbouring lanes: different rows)
 // took four times as long even from the L1.
-__device__ __forceinline__ void to_operand(uint32_t (&c)[4], int lane) {
+__device__ __forceinline__ void to_operand(uint32_t (&c)[4]) {
   exchange_bit5(c[0], c[2]);
   exchange_bit5(c[1], c[3]);
   exchange_bit4(c[0], c[1]);
   exchange_bit4(c[2], c[3]);
-  const bool b1 = lane & 2, b0 = lane & 1;
-  exchange_quad<1>(c[0], c[2], b1);
-  exchange_quad<1>(c[1], c[3], b1);
-  exchange_quad<0>(c[0], c[1], b0);
-  exchange_quad<0>(c[2], c[3], b0);
+  exchange_quad<1>(c[0], c[2], c[1], c[3]);
+  exchange_quad<0>(c[0], c[1], c[2], c[3]);
 }
 
 // Sixteen E4M3 codes with one E8M0 scale -> two fragments of eight bf16 values.
@@ -137,17 +165,19 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
 // x goes through LDS as bf16: all of it once per workgroup where it fits
 // (STAGED), else each wave brings its own steps, with the item, into a room of
 // its own (no barrier: one wave's LDS accesses keep their order).
-// WHOLE: K is a multiple of U steps and the scales are aligned, so that an
-// item's scale bytes of a row come with one load.
+// WHOLE: K is a multiple of U steps and the scales are aligned to words, so
+// that the scale bytes of an item come with one load, spread like the codes,
+// and reach the other lanes of a row by permutes.
 constexpr int kLds = 160 * 1024;
 constexpr int kStageBytes = 143 * 1024;                  // most of x in LDS; the rest is the partial sums'
-constexpr int kXPitch = 256 + 16;                        // of a wave's own step of x
+constexpr int kXPitch = 256 + 64;                        // of a wave's own step of x
 // A wave's own room: 16 MT rows of a step; its partial sums take the same place.
 __host__ __device__ constexpr int room_bytes(int mt) { return 16 * mt * kXPitch; }
 
-// Bytes between staged rows of x: 16 past the rounded row, so that equal
-// columns of neighbouring rows fall into different banks.
-__host__ __device__ constexpr int64_t stage_pitch(int64_t k) { return (k + 127) / 128 * 256 + 16; }
+// Bytes between staged rows of x: 64 past the rounded row.  An operand's four
+// lane groups read 64 consecutive bytes of a row, so that four rows fill the 64
+// banks (16 bytes more a row left 4 of 9 LDS cycles to bank conflicts).
+__host__ __device__ constexpr int64_t stage_pitch(int64_t k) { return (k + 127) / 128 * 256 + 64; }
 
 // How a launch splits the work (host side).
 struct MvPlan {
@@ -155,19 +185,23 @@ struct MvPlan {
   int batch;                                             // groups of tiles between two meetings of the partial sums
 };
 
-// One item of W: a row's scale bytes of the U steps (MXFP4 4 U, NVFP4 8 U), or
-// of a partial step the four that this lane's products take.
+// Words of a row's scale bytes in an item of U steps.
+template <int WT, int U>
+constexpr int kScaleWords = WT == kMx ? U : 2 * U;
+
+// One item of W as loaded: pieces of codes, and one word of a row's scale
+// bytes; of a partial step the four bytes that this lane's products take.
 template <int WT, int U, bool WHOLE>
 struct MvItem {
   v4i c[U];
-  uint32_t s[!WHOLE ? 4 : WT == kMx ? U : 2 * U];
+  uint32_t s[WHOLE ? 1 : 4];
 };
 
-// One item of x, as loaded: sixteen bytes a lane, 16 (bf16) or 8 (E4M3) lanes a row.
-template <int XT, int MT, int U>
+// One step of x, as loaded: sixteen bytes a lane, 16 (bf16) or 8 (E4M3) lanes a row.
+template <int XT, int MT>
 struct MvX {
-  v4i v[U][XT == kXBf16 ? 4 * MT : 2 * MT];
-  uint32_t s[U][2 * MT];
+  v4i v[XT == kXBf16 ? 4 * MT : 2 * MT];
+  uint32_t s[2 * MT];
 };
 
 // Waits for this wave's LDS accesses and meets the workgroup's other waves;
@@ -176,9 +210,8 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 
 template <int XT, int WT, int MT, int NW, int U, bool GATE, bool STAGED, bool WHOLE>
 __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan plan) {
-  static_assert(WHOLE || U == 1, "a partial step is an item of its own");
+  static_assert((WHOLE && STAGED) || U == 1, "a partial step, and one that brings its x, is an item of its own");
   constexpr int ROWS = GATE ? 8 : 16;                    // output columns of a tile
-  constexpr bool AHEAD = !STAGED;                        // x of the next item too
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   constexpr int kWaveFloats = STAGED ? MT * 256 + 4 : room_bytes(MT) / 4;   // between two waves' partial sums
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -209,25 +242,16 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
   };
   const auto load_w = [&](MvItem<WT, U, WHOLE>& it, int64_t group, int turn) {
     const int item = item_of(turn), piece = lane & 3;
-    const uint8_t* const c = a.codes + row_of(group, 4 * ((lane >> 2) & 3) + (lane >> 4)) * kc;
-    const uint8_t* const s = a.scales + row_of(group, r) * ks;
+    const int64_t row = row_of(group, 4 * ((lane >> 2) & 3) + (lane >> 4));
+    const uint8_t* const c = a.codes + row * kc;
     if constexpr (WHOLE) {
 #pragma unroll
       for (int u = 0; u < U; ++u) it.c[u] = *reinterpret_cast<const v4i*>(c + (item * U + u) * 64 + piece * 16);
-      constexpr int kBytes = (WT == kMx ? 4 : 8) * U;
-      const uint8_t* const p = s + item * kBytes;
-      if constexpr (kBytes % 16 == 0) {
-#pragma unroll
-        for (int b = 0; b < kBytes / 16; ++b) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * b);
-          it.s[4 * b] = v.x; it.s[4 * b + 1] = v.y; it.s[4 * b + 2] = v.z; it.s[4 * b + 3] = v.w;
-        }
-      } else {
-#pragma unroll
-        for (int b = 0; b < kBytes / 4; ++b) it.s[b] = reinterpret_cast<const uint32_t*>(p)[b];
-      }
+      constexpr int D = kScaleWords<WT, U>;
+      it.s[0] = reinterpret_cast<const uint32_t*>(a.scales + row * ks)[item * D + (piece & (D - 1))];
     } else {
       const int blocks = (int)(a.k >> 5), kb = item * 4;  // a block of 32 values is whole or absent
+      const uint8_t* const s = a.scales + row_of(group, r) * ks;
       const v4i v = *reinterpret_cast<const v4i*>(c + std::min(kb + piece, blocks - 1) * 16);
       it.c[0] = kb + piece < blocks ? v : v4i{0, 0, 0, 0};
 #pragma unroll
@@ -237,78 +261,88 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
       }
     }
   };
-  const auto load_x = [&](MvX<XT, MT, U>& it, int turn) {
-    const int item = item_of(turn);
+  const auto load_x = [&](MvX<XT, MT>& it, int turn) {
+    if constexpr (XT == kXBf16) {
+      const uint32_t at = (uint32_t)item_of(turn) * 128 + 8 * (lane & 15);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t k0 = (uint32_t)(item * U + u) * 128;
-      if constexpr (XT == kXBf16) {
-        const uint32_t at = k0 + 8 * (lane & 15);
+      for (int j = 0; j < 4 * MT; ++j) {
+        const int row = 4 * j + (lane >> 4);
+        const uint32_t off = row < a.m && at < (uint32_t)a.k ? ((uint32_t)row * (uint32_t)a.ldx + at) * 2 : kOffNone;
+        it.v[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off, 0, 0));
+      }
+    } else {
+      const uint32_t at = (uint32_t)item_of(turn) * 128 + 16 * (lane & 7);
 #pragma unroll
-        for (int j = 0; j < 4 * MT; ++j) {
-          const int row = 4 * j + (lane >> 4);
-          const uint32_t off = row < a.m && at < (uint32_t)a.k ? ((uint32_t)row * (uint32_t)a.ldx + at) * 2 : kOffNone;
-          it.v[u][j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off, 0, 0));
-        }
-      } else {
-        const uint32_t at = k0 + 16 * (lane & 7);
+      for (int j = 0; j < 2 * MT; ++j) {
+        const int row = 8 * j + (lane >> 3);
+        const bool ok = row < a.m && at < (uint32_t)a.k;
+        it.v[j] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? (uint32_t)row * (uint32_t)a.k + at : kOffNone, 0, 0));
+        it.s[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+            rxs, ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + (at >> 5) : kOffNone, 0, 0);
+      }
+    }
+  };
+  // this step of x into the wave's room
+  const auto put_x = [&](const MvX<XT, MT>& it) {
+    if constexpr (XT == kXBf16) {
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) {
-          const int row = 8 * j + (lane >> 3);
-          const bool ok = row < a.m && at < (uint32_t)a.k;
-          it.v[u][j] = __builtin_bit_cast(
-              v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? (uint32_t)row * (uint32_t)a.k + at : kOffNone, 0, 0));
-          it.s[u][j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-              rxs, ok ? (uint32_t)row * (uint32_t)(a.k >> 5) + (at >> 5) : kOffNone, 0, 0);
-        }
+      for (int j = 0; j < 4 * MT; ++j)
+        *reinterpret_cast<v4i*>(stage + (4 * j + (lane >> 4)) * kXPitch + (lane & 15) * 16) = it.v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2 * MT; ++j) {
+        bf16x8_t lo, hi;
+        decode_x16(it.v[j], it.s[j], lo, hi);
+        bf16x8_t* const p = reinterpret_cast<bf16x8_t*>(stage + (8 * j + (lane >> 3)) * kXPitch + (lane & 7) * 32);
+        p[0] = lo;
+        p[1] = hi;
       }
     }
   };
 
   v4f acc[MT];
   const uint32_t xrow = (STAGED ? (uint32_t)(r < a.m ? r : 0) * (uint32_t)stage_pitch(a.k) : (uint32_t)r * kXPitch) + g * 16;
-  const auto multiply = [&](const MvItem<WT, U, WHOLE>& it, const MvX<XT, MT, U>& xi, int turn) {
+  const auto multiply = [&](const MvItem<WT, U, WHOLE>& it, int turn) {
     if (kw + (turn << plan.kw_log2) >= items) return;    // wave-uniform
     const int item = item_of(turn);
+    // the item's scale words of this lane's row r, from the lanes that loaded the row
+    uint32_t sw[kScaleWords<WT, U>];
+    if constexpr (WHOLE)
+#pragma unroll
+      for (int d = 0; d < kScaleWords<WT, U>; ++d)
+        sw[d] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * (4 * (r & 3) + (r >> 2)) + d), (int)it.s[0]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if constexpr (!STAGED) {                           // this step of x into the wave's room
-        if constexpr (XT == kXBf16) {
+      bf16x8_t w[4];
+      uint32_t c[4] = {(uint32_t)it.c[u][0], (uint32_t)it.c[u][1], (uint32_t)it.c[u][2], (uint32_t)it.c[u][3]};
+      to_operand(c);
+      float sc[4];                                       // the scale of product q's values
+      if constexpr (WT == kMx && WHOLE) {
+        sc[0] = e8m0_byte<0>(sw[u]);
+        sc[1] = e8m0_byte<1>(sw[u]);
+        sc[2] = e8m0_byte<2>(sw[u]);
+        sc[3] = e8m0_byte<3>(sw[u]);
+      } else if constexpr (WT == kMx) {
 #pragma unroll
-          for (int j = 0; j < 4 * MT; ++j)
-            *reinterpret_cast<v4i*>(stage + (4 * j + (lane >> 4)) * kXPitch + (lane & 15) * 16) = xi.v[u][j];
-        } else {
+        for (int q = 0; q < 4; ++q) sc[q] = __uint_as_float(it.s[q] << 23);
+      } else {
 #pragma unroll
-          for (int j = 0; j < 2 * MT; ++j) {
-            bf16x8_t lo, hi;
-            decode_x16(xi.v[u][j], xi.s[u][j], lo, hi);
-            bf16x8_t* const p = reinterpret_cast<bf16x8_t*>(stage + (8 * j + (lane >> 3)) * kXPitch + (lane & 7) * 32);
-            p[0] = lo;
-            p[1] = hi;
-          }
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t b = WHOLE ? (sw[2 * u + (q >> 1)] >> (16 * (q & 1) + 8 * (g >> 1))) & 0xFFu : it.s[q];
+          const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 1.0f, false);
+          sc[q] = d[0];
         }
       }
-      bf16x8_t x[MT][4], w[4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int q = 0; q < 4; ++q) w[q] = decode8<WT>(c[q], sc[q]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint8_t* const x = stage + xrow + (STAGED ? (uint32_t)(item * U + u) * 256 : (uint32_t)i * 16 * kXPitch);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          x[i][q] = *reinterpret_cast<const bf16x8_t*>(
-              stage + xrow + (STAGED ? (uint32_t)(item * U + u) * 256 : (uint32_t)i * 16 * kXPitch) + 64 * q);
-      uint32_t c[4] = {(uint32_t)it.c[u][0], (uint32_t)it.c[u][1], (uint32_t)it.c[u][2], (uint32_t)it.c[u][3]};
-      to_operand(c, lane);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t sc;                                     // the scale byte of product q's values
-        if constexpr (!WHOLE) sc = it.s[q];
-        else if constexpr (WT == kMx) sc = it.s[u] >> (8 * q);
-        else sc = it.s[2 * u + (q >> 1)] >> (16 * (q & 1) + 8 * (g >> 1));
-        w[q] = decode8<WT>(c[q], sc & 0xFFu);
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[q], *reinterpret_cast<const bf16x8_t*>(x + 64 * q), acc[i], 0, 0, 0);
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[q], x[i][q], acc[i], 0, 0, 0);
     }
   };
   // Lane l of a partial tile holds rows 4 (l >> 4) .. + 3 of W against row l &
@@ -361,16 +395,27 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     if (++tn == per) { tn = 0; gr += gridDim.x; }
   };
   using W = MvItem<WT, U, WHOLE>;
-  using X = MvX<XT, MT, U>;
-  const auto ahead = [&](W& w, X& x) {                   // loads of the item after the current one
+  MvX<XT, MT> x;                                         // the next step of x, on its way to the wave's room
+  const auto ahead = [&](W& w) {                         // loads of the item after the current one
     int64_t gr = group;
     int tn = turn;
     step(gr, tn);
     load_w(w, gr, tn);
-    if constexpr (!STAGED) load_x(x, tn);
   };
-  const auto use = [&](const W& w, const X& x) {         // the products of an item; at a tile's end its sums go to LDS
-    multiply(w, x, turn);
+  // The products of an item; at a tile's end its sums go to LDS.
+  const auto use = [&](const W& w) {
+    if constexpr (!STAGED) {
+      int64_t gr = group;
+      int tn = turn;
+      step(gr, tn);
+      put_x(x);
+      load_x(x, tn);
+    }
+    multiply(w, turn);
+    // The waves keep together, so that their loads stay on neighbouring
+    // addresses: left to drift, 57344 x 8192 took 54 us instead of 50, as it
+    // did with more loads in flight.
+    if constexpr (STAGED) __builtin_amdgcn_s_barrier();
     if (turn + 1 == per) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -438,35 +483,39 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   W w0, w1;
-  X x0, x1;
   begin([&] {
     load_w(w0, first, 0);
-    if constexpr (!STAGED) load_x(x0, 0);
+    if constexpr (!STAGED) load_x(x, 0);
   });
+  if (left == 1) {                                       // a small product: one item a wave
+    use(w0);
+    finish(first, slots);
+    return;
+  }
   // One stretch of items up to a meeting of the sums, its first in p, in pairs
   // so that each item has registers of its own; true where it was odd: the next
   // item is in q then.  Loads past the last item go to the last row, unused.
   const int64_t stretch = (int64_t)plan.batch * per;
-  const auto run = [&](W& p, X& xp, W& q, X& xq) {
+  const auto run = [&](W& p, W& q) {
     int64_t n = std::min(left, stretch);
     const int64_t met = group;
     left -= n;
     for (; n >= 2; n -= 2) {
-      ahead(q, xq);
-      use(p, xp);
-      ahead(p, xp);
-      use(q, xq);
+      ahead(q);
+      use(p);
+      ahead(p);
+      use(q);
     }
     if (n) {
-      ahead(q, xq);
-      use(p, xp);
+      ahead(q);
+      use(p);
     }
     finish(met, slots);
     slots = 0;
     return n != 0;
   };
   while (left > 0)
-    if (run(w0, x0, w1, x1) && left > 0) run(w1, x1, w0, x0);
+    if (run(w0, w1) && left > 0) run(w1, w0);
 }
 
 // C (+)= 0 for an empty reduction.
@@ -493,21 +542,20 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   const bool staged = a.m <= 16 && a.m * stage_pitch(a.k) <= kStageBytes;
   const int mt = (a.m + 15) / 16, nw = mt > 1 ? 8 : 16;
   // Waves per tile and steps per item: the pair whose longest workgroup has
-  // the fewest steps to walk; longer items and more waves a tile where equal.
-  const bool al16 = aligned16(a.scales);
+  // the fewest steps to walk; longer items and fewer waves a tile where equal.
+  const bool words = (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0;
   int u = 1, kw = 4;
   int64_t best = INT64_MAX;
-  constexpr int kMaxU = WT == kMx ? 4 : 2, kMaxUDirect = XT == kXE4m3 ? 2 : 1;   // what the registers hold
-  for (int uu = staged ? kMaxU : mt == 1 ? kMaxUDirect : 1; uu >= 1; uu >>= 1) {
-    if (uu > 1 && (a.k % (128 * uu) != 0 || !al16)) continue;
-    for (int log2 = nw == 16 ? 4 : 3; log2 >= 2; --log2) {
+  constexpr int kMaxU = WT == kMx ? 4 : 2;               // what the registers hold
+  for (int uu = staged ? kMaxU : 1; uu >= 1; uu >>= 1) {
+    if (uu > 1 && (a.k % (128 * uu) != 0 || !words)) continue;
+    for (int log2 = 2; log2 <= (nw == 16 ? 4 : 3); ++log2) {
       const int64_t rounds = ((tiles + (nw >> log2) - 1) / (nw >> log2) + kMatvecGrid - 1) / kMatvecGrid;
       const int64_t cost = rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2) * uu;
       if (cost < best) best = cost, u = uu, kw = log2;
     }
   }
-  // U = 1 has whole steps too, with a row's word of scales (two for NVFP4) aligned
-  const bool whole = u > 1 || (a.k % 128 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0);
+  const bool whole = a.k % 128 == 0 && words;
   const int64_t groups = (tiles + (nw >> kw) - 1) / (nw >> kw), slot = (int64_t)nw * (mt * 256 + 4) * 4;
   // groups of tiles between two meetings of the sums: what LDS holds beside x
   const MvPlan plan{kw, staged ? (int)std::min<int64_t>((kLds - a.m * stage_pitch(a.k)) / slot, 4) : 1};
@@ -521,10 +569,8 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
     if constexpr (kMaxU == 4)
       if (u == 4) go(matvec_kernel<XT, WT, 1, 16, 4, GATE, true, true>);
   } else if (mt == 1) {
-    if (u == 1 && whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, true>);
-    else if (u == 1) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, false>);
-    if constexpr (kMaxUDirect == 2)
-      if (u == 2) go(matvec_kernel<XT, WT, 1, 16, 2, GATE, false, true>);
+    if (whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, true>);
+    else go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, false>);
   } else if (mt == 2) {
     if (whole) go(matvec_kernel<XT, WT, 2, 8, 1, GATE, false, true>);
     else go(matvec_kernel<XT, WT, 2, 8, 1, GATE, false, false>);
