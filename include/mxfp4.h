@@ -564,7 +564,7 @@ fp4_status fp4_matvec(int64_t m, int64_t n, int64_t k, const void* x, int64_t ld
  *   C[m][n] (+)= w_factors[(n / 256) * w_factor_stride] * sum_k x[m][k] (delta q)[n][k]
  *   w_codes [n][k/2], w_scales [n][k/16] E4M3
  * Errors as fp4_matvec; FP4_EINVAL also for a negative stride; FP4_EALIGN also
- * for w_scales not 2-byte or w_factors not 4-byte aligned.
+ * for w_factors not 4-byte aligned.
  */
 fp4_status fp4_nv_matvec(int64_t m, int64_t n, int64_t k, const uint16_t* x, int64_t ldx,
                          const uint8_t* w_codes, const uint8_t* w_scales, const float* w_factors,

@@ -440,15 +440,25 @@ def fp4_nv_gemm(a_codes, a_scales, a_factors, b_codes, b_scales, b_factors, c=No
     return c
 
 
+# The calls below also serve single tokens, whose kernels take a few
+# microseconds: their checks read each tensor's properties once, and the
+# current device once a call.
 _BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
+_ROWS32 = _BITS16 + (torch.float32,)
 
 
-def _rows2d(x, name, shape=None, f32=False):
-    """A 2-D tensor of bf16 values (or, with f32, fp32 ones) with unit column
-    stride; returns its leading dimension."""
-    _dev(x, name)
-    if x.dtype not in _BITS16 and not (f32 and x.dtype is torch.float32):
-        raise Fp4Error(f"{name} must hold bf16 values or their 16-bit patterns" + (", or fp32 values" if f32 else ""))
+def _here(t, name, cur):
+    if not isinstance(t, torch.Tensor) or t.get_device() != cur:
+        _dev(t, name)
+
+
+def _rows2d(x, name, cur, shape=None, dtypes=_BITS16):
+    """A 2-D tensor of bf16 values (or, with _ROWS32, fp32 ones) with unit
+    column stride; returns its leading dimension."""
+    _here(x, name, cur)
+    if x.dtype not in dtypes:
+        raise Fp4Error(f"{name} must hold bf16 values or their 16-bit patterns"
+                       + (", or fp32 values" if dtypes is _ROWS32 else ""))
     size, stride = x.shape, x.stride()
     if len(size) != 2 or (stride[1] != 1 and size[1] > 1):
         raise Fp4Error(f"{name} must be 2-D with unit column stride")
@@ -458,24 +468,32 @@ def _rows2d(x, name, shape=None, f32=False):
     return stride[0] if size[0] > 1 else -(-size[1] // 8) * 8
 
 
-def _vec(t, name, n, dtypes):
-    _dev(t, name)
-    if t.dtype not in dtypes or t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+def _vec(t, name, n, dtypes, cur):
+    _here(t, name, cur)
+    if t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous():
         raise Fp4Error(f"{name} must be a contiguous vector of {n} elements of {dtypes[0]}")
-    return t
 
 
 def _out16(t, shape, device, name):
     if t is None:
         return torch.empty(shape, dtype=torch.bfloat16, device=device)
     _dev(t, name)
-    if tuple(t.shape) != tuple(shape) or t.dtype not in _BITS16 or not t.is_contiguous():
+    if t.shape != shape or t.dtype not in _BITS16 or not t.is_contiguous():
         raise Fp4Error(f"{name} must be a contiguous bf16 tensor of shape {tuple(shape)}")
     return t
 
 
-def _dtype(x):
-    return FP4_F32 if x.dtype == torch.float32 else FP4_BF16
+def _bytes2d(t, name, cur, shape):
+    _here(t, name, cur)
+    if t.dtype is not torch.uint8 or not t.is_contiguous() or t.shape != shape:
+        raise Fp4Error(f"{name} must be a contiguous uint8 tensor of shape {tuple(shape)}")
+
+
+def _raw_stream(cur):
+    return torch._C._cuda_getCurrentRawStream(cur)
+
+
+_NONE3, _NONE5 = (None,) * 3, (None,) * 5
 
 
 def fp4_dropout(x, p, seed=0, offset=0, residual=None, out=None):
@@ -483,14 +501,20 @@ def fp4_dropout(x, p, seed=0, offset=0, residual=None, out=None):
     never stored; the same call on the output's gradient (without residual) is
     the backward pass.  Without `out` the result's rows lie at a pitch of a
     multiple of eight elements (what the quantizers read)."""
-    ldx = _rows2d(x, "x", f32=True)
-    rows, cols = x.shape
-    ldr = 0 if residual is None else _rows2d(residual, "residual", x.shape)
+    cur = torch.cuda.current_device()
+    ldx = _rows2d(x, "x", cur, None, _ROWS32)
+    shape = x.shape
+    rows, cols = shape
+    ldr = 0 if residual is None else _rows2d(residual, "residual", cur, shape)
     if out is None:
-        out = torch.empty((rows, -(-cols // 8) * 8), dtype=torch.bfloat16, device=x.device)[:, :cols]
-    ldo = _rows2d(out, "out", x.shape)
-    _check(load().fp4_dropout(rows, cols, _p(x), _dtype(x), ldx, _p(residual), ldr, float(p), int(seed), int(offset),
-                              _p(out), ldo, _stream()))
+        ldo = -(-cols // 8) * 8
+        out = torch.empty((rows, ldo), dtype=torch.bfloat16, device=x.device)
+        if ldo != cols:
+            out = out[:, :cols]
+    else:
+        ldo = _rows2d(out, "out", cur, shape)
+    _check(load().fp4_dropout(rows, cols, x.data_ptr(), 1 if x.dtype is torch.float32 else 0, ldx, _p(residual), ldr,
+                              float(p), int(seed), int(offset), out.data_ptr(), ldo, _raw_stream(cur)))
     return out
 
 
@@ -499,24 +523,26 @@ def fp4_rmsnorm_producer(x, gamma, eps=1e-5, residual=None, p=0.0, seed=0, offse
     """Dropout of x, addition to the residual, RMSNorm and its codes: returns
     (s, rstd, y, codes, scales), None where not emitted.  `out` may hold those
     five buffers (None: allocated)."""
-    ldx = _rows2d(x, "x", f32=True)
-    t, d = x.shape
-    ldr = 0 if residual is None else _rows2d(residual, "residual", x.shape)
-    _vec(gamma, "gamma", d, _BITS16)
-    dev = x.device
+    cur = torch.cuda.current_device()
+    ldx = _rows2d(x, "x", cur, None, _ROWS32)
+    shape = x.shape
+    t, d = shape
+    ldr = 0 if residual is None else _rows2d(residual, "residual", cur, shape)
+    _vec(gamma, "gamma", d, _BITS16, cur)
     if d % 32:
         raise Fp4Error("the row length must be a multiple of 32")
-    out = list(out) if out is not None else [None] * 5
-    s = _out16(out[0], (t, d), dev, "sum") if emit_sum else None
-    rstd = _out(out[1], (t,), torch.float32, dev, "rstd")
-    y = _out16(out[2], (t, d), dev, "y") if emit_y else None
+    dev = x.device
+    o_s, o_rstd, o_y, o_codes, o_scales = _NONE5 if out is None else out
+    s = _out16(o_s, shape, dev, "sum") if emit_sum else None
+    rstd = _out(o_rstd, (t,), torch.float32, dev, "rstd")
+    y = _out16(o_y, shape, dev, "y") if emit_y else None
     codes = scales = None
     if emit_codes:
-        codes = _out(out[3], (t, d // 2 if fmt == FP4_E2M1 else d), torch.uint8, dev, "codes")
-        scales = _out(out[4], (t, d // 32), torch.uint8, dev, "scales")
-    _check(load().fp4_rmsnorm_producer(t, d, _p(x), _dtype(x), ldx, _p(residual), ldr, _p(gamma), float(eps), float(p),
-                                       int(seed), int(offset), _p(s), _p(rstd), _p(y), int(fmt), _p(codes),
-                                       _p(scales), _stream()))
+        codes = _out(o_codes, (t, d // 2 if fmt == FP4_E2M1 else d), torch.uint8, dev, "codes")
+        scales = _out(o_scales, (t, d // 32), torch.uint8, dev, "scales")
+    _check(load().fp4_rmsnorm_producer(t, d, x.data_ptr(), 1 if x.dtype is torch.float32 else 0, ldx, _p(residual), ldr,
+                                       gamma.data_ptr(), float(eps), float(p), int(seed), int(offset), _p(s), rstd.data_ptr(), _p(y), int(fmt),
+                                       _p(codes), _p(scales), _raw_stream(cur)))
     return s, rstd, y, codes, scales
 
 
@@ -524,52 +550,64 @@ def fp4_rmsnorm_backward(dy, s, rstd, gamma, ds=None, p=0.0, seed=0, offset=0, a
     """Gradients of fp4_rmsnorm_producer's boundary: returns (dsum, dx, dgamma);
     dx is dsum where nothing is dropped.  `ds` is the gradient that reaches s
     along the residual stream; `out` may hold the three buffers."""
-    lddy = _rows2d(dy, "dy", f32=True)
-    t, d = dy.shape
-    lds = _rows2d(s, "s", dy.shape)
-    ldds = 0 if ds is None else _rows2d(ds, "ds", dy.shape)
-    _vec(rstd, "rstd", t, (torch.float32,))
-    _vec(gamma, "gamma", d, _BITS16)
+    cur = torch.cuda.current_device()
+    lddy = _rows2d(dy, "dy", cur, None, _ROWS32)
+    shape = dy.shape
+    t, d = shape
+    lds = _rows2d(s, "s", cur, shape)
+    ldds = 0 if ds is None else _rows2d(ds, "ds", cur, shape)
+    _vec(rstd, "rstd", t, (torch.float32,), cur)
+    _vec(gamma, "gamma", d, _BITS16, cur)
     dev = dy.device
-    out = list(out) if out is not None else [None] * 3
-    if accumulate and out[2] is None:
+    o_dsum, o_dx, o_dgamma = _NONE3 if out is None else out
+    if accumulate and o_dgamma is None:
         raise Fp4Error("accumulate needs a dgamma tensor")
-    dsum = _out16(out[0], (t, d), dev, "dsum")
-    dx = _out16(out[1], (t, d), dev, "dx") if int(float(p) * 65536 + 0.5) > 0 else None
-    dgamma = _out(out[2], (d,), torch.float32, dev, "dgamma")
+    dsum = _out16(o_dsum, shape, dev, "dsum")
+    # the call writes dx where p, as the fp32 it receives, rounds above 0, and then only
+    dx = _out16(o_dx, shape, dev, "dx") if ctypes.c_float(p).value * 65536 + 0.5 >= 1 else None
+    dgamma = _out(o_dgamma, (d,), torch.float32, dev, "dgamma")
     lib = load()
     size = lib.fp4_rmsnorm_backward_workspace(t, d)
     ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
-    _check(lib.fp4_rmsnorm_backward(t, d, _p(dy), _dtype(dy), lddy, _p(s), lds, _p(rstd), _p(gamma), _p(ds), ldds,
-                                    float(p), int(seed), int(offset), _p(dsum), _p(dx), _p(dgamma),
-                                    1 if accumulate else 0, _p(ws), size, _stream()))
+    _check(lib.fp4_rmsnorm_backward(t, d, dy.data_ptr(), 1 if dy.dtype is torch.float32 else 0, lddy, s.data_ptr(), lds,
+                                    rstd.data_ptr(), gamma.data_ptr(), _p(ds), ldds, float(p), int(seed), int(offset), dsum.data_ptr(),
+                                    _p(dx), dgamma.data_ptr(), 1 if accumulate else 0, ws.data_ptr(), size,
+                                    _raw_stream(cur)))
     return dsum, dsum if dx is None else dx, dgamma
 
 
-def _few_rows(x, x_scales, w_codes):
-    """Shapes of the few-row products: returns (m, k, ldx)."""
-    _u8_2d(w_codes, "w_codes")
+def _few_rows(x, x_scales, w_codes, cur):
+    """Shapes of the few-row products: returns (m, n, k, ldx)."""
+    _here(w_codes, "w_codes", cur)
+    if w_codes.dtype is not torch.uint8 or w_codes.dim() != 2 or not w_codes.is_contiguous():
+        raise Fp4Error("w_codes must be a contiguous 2-D uint8 tensor")
+    n, k = w_codes.shape
+    k *= 2
     if x_scales is None:
-        ldx = _rows2d(x, "x")
+        ldx = _rows2d(x, "x", cur)
+        m, kx = x.shape
     else:
-        _u8_2d(x, "x")
-        _u8_2d(x_scales, "x_scales", (x.shape[0], x.shape[1] // 32))
-        ldx = x.shape[1]
-    m, k = x.shape
-    if 2 * w_codes.shape[1] != k:
-        raise Fp4Error(f"w_codes has {2 * w_codes.shape[1]} values per row, x {k}")
-    return m, k, ldx
+        _here(x, "x", cur)
+        if x.dim() != 2:
+            raise Fp4Error("x must be 2-D")
+        m, kx = x.shape
+        _bytes2d(x, "x", cur, (m, kx))
+        _bytes2d(x_scales, "x_scales", cur, (m, kx // 32))
+        ldx = kx
+    if kx != k:
+        raise Fp4Error(f"w_codes has {k} values per row, x {kx}")
+    return m, n, k, ldx
 
 
 def fp4_matvec(x, w_codes, w_scales, x_scales=None, c=None, accumulate=False):
     """C (+)= x dec(W)^T for up to 64 rows of x, bf16 or E4M3 codes with
     x_scales, and MXFP4 weights in the row layout."""
-    m, k, ldx = _few_rows(x, x_scales, w_codes)
-    n = w_codes.shape[0]
-    _u8_2d(w_scales, "w_scales", (n, k // 32))
+    cur = torch.cuda.current_device()
+    m, n, k, ldx = _few_rows(x, x_scales, w_codes, cur)
+    _bytes2d(w_scales, "w_scales", cur, (n, k // 32))
     c = _gemm_out(c, m, n, accumulate, x.device)
-    _check(load().fp4_matvec(m, n, k, _p(x), ldx, _p(x_scales), _p(w_codes), _p(w_scales), _p(c), _ldc(c),
-                             1 if accumulate else 0, _stream()))
+    _check(load().fp4_matvec(m, n, k, x.data_ptr(), ldx, _p(x_scales), w_codes.data_ptr(), w_scales.data_ptr(),
+                             c.data_ptr(), _ldc(c), 1 if accumulate else 0, _raw_stream(cur)))
     return c
 
 
@@ -577,30 +615,32 @@ def fp4_nv_matvec(x, w_codes, w_scales, w_factors, c=None, accumulate=False):
     """C (+)= x dec(W)^T for up to 64 rows of bf16 x and CTA-local NVFP4
     weights in the row layout; a factor vector of one element is shared by all
     rows of W, otherwise it holds one per 256-row panel."""
-    m, k, ldx = _few_rows(x, None, w_codes)
-    n = w_codes.shape[0]
-    _u8_2d(w_scales, "w_scales", (n, k // 16))
+    cur = torch.cuda.current_device()
+    m, n, k, ldx = _few_rows(x, None, w_codes, cur)
+    _bytes2d(w_scales, "w_scales", cur, (n, k // 16))
     panels = (n + 255) // 256
-    _dev(w_factors, "w_factors")
-    if (w_factors.dtype != torch.float32 or w_factors.dim() != 1 or not w_factors.is_contiguous()
-            or w_factors.numel() not in (1, panels)):
+    _here(w_factors, "w_factors", cur)
+    if w_factors.dtype is not torch.float32 or w_factors.shape not in ((1,), (panels,)) or not w_factors.is_contiguous():
         raise Fp4Error(f"w_factors must be a contiguous fp32 vector of 1 or {panels} elements")
     c = _gemm_out(c, m, n, accumulate, x.device)
-    _check(load().fp4_nv_matvec(m, n, k, _p(x), ldx, _p(w_codes), _p(w_scales), _p(w_factors),
-                                0 if w_factors.numel() == 1 else 1, _p(c), _ldc(c), 1 if accumulate else 0, _stream()))
+    _check(load().fp4_nv_matvec(m, n, k, x.data_ptr(), ldx, w_codes.data_ptr(), w_scales.data_ptr(),
+                                w_factors.data_ptr(), 0 if w_factors.shape[0] == 1 else 1, c.data_ptr(), _ldc(c),
+                                1 if accumulate else 0, _raw_stream(cur)))
     return c
 
 
 def fp4_swiglu_matvec(x, w13_codes, w13_scales, x_scales=None, h=None):
     """h = bf16(SiLU(a) b) with a = bf16(x W1^T), b = bf16(x W3^T) for up to 64
     rows of x (as fp4_matvec) and the stacked MXFP4 rows of W1 and W3."""
-    m, d, ldx = _few_rows(x, x_scales, w13_codes)
-    if w13_codes.shape[0] % 2:
+    cur = torch.cuda.current_device()
+    m, f2, d, ldx = _few_rows(x, x_scales, w13_codes, cur)
+    if f2 % 2:
         raise Fp4Error("w13_codes must stack W1 and W3: an even number of rows")
-    f = w13_codes.shape[0] // 2
-    _u8_2d(w13_scales, "w13_scales", (2 * f, d // 32))
+    _bytes2d(w13_scales, "w13_scales", cur, (f2, d // 32))
+    f = f2 // 2
     h = _out16(h, (m, f), x.device, "h")
-    _check(load().fp4_swiglu_matvec(m, f, d, _p(x), ldx, _p(x_scales), _p(w13_codes), _p(w13_scales), _p(h), _stream()))
+    _check(load().fp4_swiglu_matvec(m, f, d, x.data_ptr(), ldx, _p(x_scales), w13_codes.data_ptr(),
+                                    w13_scales.data_ptr(), h.data_ptr(), _raw_stream(cur)))
     return h
 
 

@@ -382,7 +382,8 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
         *c = a.accumulate ? __fadd_rn(*c, v) : v;
       }
     }
-    lds_barrier();                                       // the partial sums' room is free again
+    // the partial sums' room is free again once all have read (STAGED: the next item's barrier says so)
+    if constexpr (!STAGED) lds_barrier();
   };
 
   // The workgroup's items in order: (group, turn), the same count for every
@@ -587,8 +588,7 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
 // Checks shared by the three calls; n counts output columns, `stack` the rows
 // of codes per output column.
 static fp4_status matvec_check(int64_t m, int64_t n, int64_t k, const void* x, int64_t ldx, const uint8_t* x_scales,
-                               bool e4m3, const uint8_t* codes, const uint8_t* scales, int64_t scale_align,
-                               const void* out) {
+                               bool e4m3, const uint8_t* codes, const uint8_t* scales, const void* out) {
   if (m < 0 || m > kMatvecMaxM || n < 0 || !mult32z(k) || k >= ((int64_t)1 << 24) || ldx < k ||
       ldx >= ((int64_t)1 << 24))
     return FP4_ESHAPE;
@@ -596,9 +596,7 @@ static fp4_status matvec_check(int64_t m, int64_t n, int64_t k, const void* x, i
   if (n > ((int64_t)1 << 34)) return FP4_ESHAPE;
   if (!out) return FP4_EINVAL;
   if (k > 0 && (!x || !codes || !scales || (e4m3 && !x_scales))) return FP4_EINVAL;
-  if (k > 0 && (!aligned16(x) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & (scale_align - 1)) ||
-                (!e4m3 && ldx % 8 != 0)))
-    return FP4_EALIGN;
+  if (k > 0 && (!aligned16(x) || !aligned16(codes) || (!e4m3 && ldx % 8 != 0))) return FP4_EALIGN;
   return FP4_OK;
 }
 
@@ -614,7 +612,7 @@ fp4_status fp4_matvec(int64_t m, int64_t n, int64_t k, const void* x, int64_t ld
   if (accumulate != 0 && accumulate != 1) return FP4_EINVAL;
   const bool e4m3 = x_scales != nullptr;
   if (ldc < n || (e4m3 && ldx != k)) return FP4_ESHAPE;
-  const fp4_status st = matvec_check(m, n, k, x, ldx, x_scales, e4m3, w_codes, w_scales, 1, c);
+  const fp4_status st = matvec_check(m, n, k, x, ldx, x_scales, e4m3, w_codes, w_scales, c);
   if (st != FP4_OK || m == 0 || n == 0) return st;
   if (reinterpret_cast<uintptr_t>(c) & 3) return FP4_EALIGN;
   const MatvecArgs a{(int)m, n, k, x, ldx, x_scales, w_codes, w_scales, nullptr, 0, c, ldc, accumulate, nullptr};
@@ -627,7 +625,7 @@ fp4_status fp4_nv_matvec(int64_t m, int64_t n, int64_t k, const uint16_t* x, int
                          int64_t ldc, int accumulate, hipStream_t stream) {
   if ((accumulate != 0 && accumulate != 1) || w_factor_stride < 0) return FP4_EINVAL;
   if (ldc < n) return FP4_ESHAPE;
-  const fp4_status st = matvec_check(m, n, k, x, ldx, nullptr, false, w_codes, w_scales, 2, c);
+  const fp4_status st = matvec_check(m, n, k, x, ldx, nullptr, false, w_codes, w_scales, c);
   if (st != FP4_OK || m == 0 || n == 0) return st;
   if (k > 0 && !w_factors) return FP4_EINVAL;
   if ((reinterpret_cast<uintptr_t>(c) & 3) || (reinterpret_cast<uintptr_t>(w_factors) & 3)) return FP4_EALIGN;
@@ -640,7 +638,7 @@ fp4_status fp4_swiglu_matvec(int64_t m, int64_t f, int64_t d, const void* x, int
                              const uint8_t* w13_codes, const uint8_t* w13_scales, uint16_t* h, hipStream_t stream) {
   const bool e4m3 = x_scales != nullptr;
   if (e4m3 && ldx != d) return FP4_ESHAPE;
-  const fp4_status st = matvec_check(m, f, d, x, ldx, x_scales, e4m3, w13_codes, w13_scales, 1, h);
+  const fp4_status st = matvec_check(m, f, d, x, ldx, x_scales, e4m3, w13_codes, w13_scales, h);
   if (st != FP4_OK || m == 0 || f == 0) return st;
   if (reinterpret_cast<uintptr_t>(h) & 1) return FP4_EALIGN;
   const MatvecArgs a{(int)m, f, d, x, ldx, x_scales, w13_codes, w13_scales, nullptr, 0, nullptr, 0, 0, h};

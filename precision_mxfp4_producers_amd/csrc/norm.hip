@@ -140,60 +140,67 @@ struct NormOut {
 // G threads hold one row, thread i the groups of eight columns i, i + G, ...:
 // the row stays in registers between the statistics and the output, x and the
 // residual are read once.  Four neighbouring lanes hold one 32-value block.
-template <int G, int V, bool F32>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, int d, const void* x, int64_t ldx,
-                                                                    const uint16_t* residual, int64_t ldr,
-                                                                    const uint16_t* gamma, float eps, Dropout drop,
-                                                                    NormOut o) {
+//
+// No branch surrounds a load (a row or column past the end reads the last
+// one), and all of a thread's loads go out before its first use: with the
+// loads of each group behind the stores of the one before, 8192 x 4096 with
+// dropout took 89 us.
+template <int G, int V, bool F32, bool RES>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, int d, const void* __restrict__ x,
+                                                                    int64_t ldx, const uint16_t* __restrict__ residual,
+                                                                    int64_t ldr, const uint16_t* __restrict__ gamma,
+                                                                    float eps, Dropout drop, NormOut o) {
   constexpr int kRows = G < 256 ? 256 / G : 1;
   __shared__ float lds[16];
   const int i = threadIdx.x & (G - 1);
   const int64_t r = (int64_t)blockIdx.x * kRows + (G < 256 ? threadIdx.x / G : 0);
-  const bool live = r < t;                               // whole rows of threads; all threads reach the exchanges
-  uint4 s[V];
+  const int64_t rr = std::min(r, t - 1);
+  uint4 s[V], g[V];
+  float v[V][8], base[V][8];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = std::min((k * G + i) * 8, d - 8);
+    load8<F32>(x, rr * ldx + c, v[k]);
+    if constexpr (RES) unpack8(load_once_u4(residual + rr * ldr + c), base[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) g[k] = *reinterpret_cast<const uint4*>(gamma + std::min((k * G + i) * 8, d - 8));
   float sq = 0.0f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = (k * G + i) * 8;
-    s[k] = make_uint4(0, 0, 0, 0);
-    if (live && c < d) {
-      float v[8], base[8];
-      load8<F32>(x, r * ldx + c, v);
-      if (residual) unpack8(load_once_u4(residual + r * ldr + c), base);
-      if (drop.thr) {
-        dropout8(v, residual ? base : nullptr, (uint64_t)r * (uint32_t)(d >> 3) + (uint32_t)(c >> 3), drop);
-      } else if (residual) {
+    const bool live = r < t && c < d;                    // whole rows of threads, and whole groups of four lanes
+    if (drop.thr) {
+      dropout8(v[k], RES ? base[k] : nullptr, (uint64_t)rr * (uint32_t)(d >> 3) + (uint32_t)(c >> 3), drop);
+    } else if constexpr (RES) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], base[j]);
-      }
-      s[k] = pack8(v);
-      if (o.sum) *reinterpret_cast<uint4*>(o.sum + r * d + c) = s[k];
+      for (int j = 0; j < 8; ++j) v[k][j] = __fadd_rn(v[k][j], base[k][j]);
     }
-    float v[8];
-    unpack8(s[k], v);
+    s[k] = pack8(v[k]);
+    if (!live) s[k] = make_uint4(0, 0, 0, 0);
+    if (o.sum && live) *reinterpret_cast<uint4*>(o.sum + r * d + c) = s[k];
+    unpack8(s[k], v[k]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[j], v[j], sq);
+    for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[k][j], v[k][j], sq);
   }
   sq = row_sum<G>(sq, lds);
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sq, (float)d), eps)));
-  if (live && i == 0) o.rstd[r] = rstd;
+  if (r < t && i == 0) o.rstd[r] = rstd;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = (k * G + i) * 8;
-    uint4 y = make_uint4(0, 0, 0, 0);
-    if (live && c < d) {
-      float v[8], g[8];
-      unpack8(s[k], v);
-      unpack8(*reinterpret_cast<const uint4*>(gamma + c), g);
+    const bool live = r < t && c < d;
+    float w[8], gm[8];
+    unpack8(s[k], w);
+    unpack8(g[k], gm);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(v[j], rstd), g[j]);
-      y = pack8(v);
-      if (o.y) *reinterpret_cast<uint4*>(o.y + r * d + c) = y;
-    }
+    for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(__fmul_rn(w[j], rstd), gm[j]);
+    const uint4 y = pack8(w);
+    if (o.y && live) *reinterpret_cast<uint4*>(o.y + r * d + c) = y;
     if (o.codes) {
       const uint32_t am = max_quad(bf16_absmax8(y.x, y.y, y.z, y.w)) << 16;
       const int e = o.e4m3 ? upward_exp_e4m3(am) : upward_exp(am);
-      if (live && c < d) {
+      if (live) {
         if (o.e4m3)
           *reinterpret_cast<uint2*>(o.codes + r * d + c) = e4m3_8(y, pow2_scale(e));
         else
@@ -208,61 +215,82 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, i
 // With xh = s rstd and g = dy gamma,
 //   ds' = rstd (g - xh mean(g xh)) [+ ds],  dsum = bf16(ds'),
 //   dx = bf16(dropout(ds')),  dgamma = sum over rows of dy xh.
-// G threads hold a row, as in the forward; each group of G threads walks rows
-// group, group + groups, ... and keeps its columns' share of dgamma in
-// registers, which it writes once, as row `group` of the workspace.
-template <int G, int V, bool F32>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_bwd_kernel(int64_t t, int d, const void* dy, int64_t lddy,
-                                                                        const uint16_t* s, int64_t lds_s,
-                                                                        const float* rstd, const uint16_t* gamma,
-                                                                        const uint16_t* ds, int64_t ldds, Dropout drop,
-                                                                        uint16_t* dsum, uint16_t* dx, float* parts,
-                                                                        int64_t groups) {
+// G threads hold a row, as in the forward.  A workgroup walks rows in steps of
+// the whole grid, loads the next row's tensors before it works on the current
+// one, keeps its columns' share of dgamma in registers and writes it once, as
+// one row of the workspace.
+template <int V, bool F32, bool DS>
+struct BwdRow {
+  float dy[V][8];
+  uint4 s[V], ds[V];
+  float rstd;
+};
+
+template <int G, int V, bool F32, bool DS>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_bwd_kernel(
+    int64_t t, int d, const void* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ s, int64_t lds_s,
+    const float* __restrict__ rstd, const uint16_t* __restrict__ gamma, const uint16_t* __restrict__ ds, int64_t ldds,
+    Dropout drop, uint16_t* __restrict__ dsum, uint16_t* __restrict__ dx, float* __restrict__ parts) {
   constexpr int kRows = G < 256 ? 256 / G : 1;
-  __shared__ float lds[16];
+  constexpr bool NEXT = G < 512;                         // the next row's registers beside this one's
+  __shared__ float lds[G < 256 ? 4 * 64 * V * 8 : 16];
   const int i = threadIdx.x & (G - 1);
-  const int64_t group = (int64_t)blockIdx.x * kRows + (G < 256 ? threadIdx.x / G : 0);
+  const int64_t first = (int64_t)blockIdx.x * kRows + (G < 256 ? threadIdx.x / G : 0), sweep = (int64_t)gridDim.x * kRows;
+  const int64_t turns = (t - (int64_t)blockIdx.x * kRows + sweep - 1) / sweep;   // the same for a whole workgroup
   float dg[V][8];
+  uint4 gm[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k)
+  for (int k = 0; k < V; ++k) {
+    gm[k] = *reinterpret_cast<const uint4*>(gamma + std::min((k * G + i) * 8, d - 8));
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[k][j] = 0.0f;
-  const int64_t turns = (t + groups - 1) / groups;       // the same for every thread: all reach the exchanges
-  for (int64_t turn = 0; turn < turns; ++turn) {
-    const int64_t r = turn * groups + group;
-    const bool live = group < groups && r < t;
-    const float rs = live ? rstd[r] : 0.0f;
-    float g[V][8], xh[V][8], dot = 0.0f;
+  }
+  const auto load = [&](BwdRow<V, F32, DS>& row, int64_t turn) {
+    const int64_t r = std::min(first + turn * sweep, t - 1);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = (k * G + i) * 8;
+      const int c = std::min((k * G + i) * 8, d - 8);
+      load8<F32>(dy, r * lddy + c, row.dy[k]);
+      row.s[k] = load_once_u4(s + r * lds_s + c);
+      if constexpr (DS) row.ds[k] = load_once_u4(ds + r * ldds + c);
+    }
+    row.rstd = rstd[r];
+  };
+  BwdRow<V, F32, DS> cur, next;
+  load(cur, 0);
+  for (int64_t turn = 0; turn < turns; ++turn) {
+    const int64_t r = first + turn * sweep;
+    if constexpr (NEXT) load(next, turn + 1);
+    float dot = 0.0f;
+    const float rs = cur.rstd;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[k][j] = xh[k][j] = 0.0f;
-      if (live && c < d) {
-        float gm[8];
-        load8<F32>(dy, r * lddy + c, g[k]);
-        unpack8(load_once_u4(s + r * lds_s + c), xh[k]);
-        unpack8(*reinterpret_cast<const uint4*>(gamma + c), gm);
+    for (int k = 0; k < V; ++k) {
+      const bool live = r < t && (k * G + i) * 8 < d;
+      float xh[8], g[8];
+      unpack8(cur.s[k], xh);
+      unpack8(gm[k], g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          xh[k][j] = __fmul_rn(xh[k][j], rs);
-          dg[k][j] = __builtin_fmaf(g[k][j], xh[k][j], dg[k][j]);
-          g[k][j] = __fmul_rn(g[k][j], gm[j]);
-          dot = __builtin_fmaf(g[k][j], xh[k][j], dot);
-        }
+      for (int j = 0; j < 8; ++j) {
+        if (!live) cur.dy[k][j] = 0.0f;
+        xh[j] = __fmul_rn(xh[j], rs);
+        // a dead lane adds 0 times a finite s of the last row or group
+        dg[k][j] = live ? __builtin_fmaf(cur.dy[k][j], xh[j], dg[k][j]) : dg[k][j];
+        dot = live ? __builtin_fmaf(__fmul_rn(cur.dy[k][j], g[j]), xh[j], dot) : dot;
       }
     }
     const float mean = __fdiv_rn(row_sum<G>(dot, lds), (float)d);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int c = (k * G + i) * 8;
-      if (live && c < d) {
-        float v[8], b[8];
-        if (ds) unpack8(load_once_u4(ds + r * ldds + c), b);
+      if (r < t && c < d) {
+        float v[8], xh[8], g[8], b[8];
+        unpack8(cur.s[k], xh);
+        unpack8(gm[k], g);
+        if constexpr (DS) unpack8(cur.ds[k], b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          v[j] = __builtin_fmaf(-xh[k][j], mean, g[k][j]);
-          v[j] = ds ? __builtin_fmaf(rs, v[j], b[j]) : __fmul_rn(rs, v[j]);
+          v[j] = __builtin_fmaf(-__fmul_rn(xh[j], rs), mean, __fmul_rn(cur.dy[k][j], g[j]));
+          v[j] = DS ? __builtin_fmaf(rs, v[j], b[j]) : __fmul_rn(rs, v[j]);
         }
         *reinterpret_cast<uint4*>(dsum + r * d + c) = pack8(v);
         if (drop.thr) {
@@ -271,13 +299,35 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_bwd_kernel(int64_t 
         }
       }
     }
+    if constexpr (NEXT) cur = next;
+    else if (turn + 1 < turns) load(cur, turn + 1);
   }
-  if (group < groups) {
+  float* const out = parts + (int64_t)blockIdx.x * d;
+  if constexpr (G < 256) {
+    // lanes that hold the same columns of other rows, then the four waves
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int st = G; st < 64; st <<= 1) dg[k][j] = __fadd_rn(dg[k][j], __shfl_xor(dg[k][j], st, 64));
+        lds[(((threadIdx.x >> 6) * V + k) * 8 + j) * 64 + (threadIdx.x & 63)] = dg[k][j];
+      }
+    __syncthreads();
+    for (int e = threadIdx.x; e < V * G * 8; e += 256) {
+      const int l = e & (G - 1), j = (e / G) & 7, k = e / (G * 8), c = (k * G + l) * 8 + j;
+      if (c >= d) continue;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v = __fadd_rn(v, lds[((w * V + k) * 8 + j) * 64 + l]);
+      out[c] = v;
+    }
+  } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int c = (k * G + i) * 8;
       if (c < d) {
-        float4* p = reinterpret_cast<float4*>(parts + group * d + c);
+        float4* const p = reinterpret_cast<float4*>(out + c);
         p[0] = make_float4(dg[k][0], dg[k][1], dg[k][2], dg[k][3]);
         p[1] = make_float4(dg[k][4], dg[k][5], dg[k][6], dg[k][7]);
       }
@@ -285,30 +335,33 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_bwd_kernel(int64_t 
   }
 }
 
-// dgamma[c] (+)= sum over the workspace's rows, in a fixed order: 16 slices of
-// rows per column, added by slice.
-__global__ __launch_bounds__(512) void dgamma_kernel(int64_t groups, int d, const float* parts, float* dgamma,
-                                                     int accumulate) {
-  __shared__ float lds[16][33];
-  const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5, c = blockIdx.x * 32 + cl;   // d is a multiple of 32
-  float v = 0.0f;
-  for (int64_t q = sl; q < groups; q += 16) v = __fadd_rn(v, parts[q * d + c]);
+// dgamma[c] (+)= sum over the workspace's rows, in a fixed order: 32 slices of
+// rows per column, added by slice.  32 columns (one 128-byte line a row) a
+// workgroup, four a thread, so that a thread's loads are wide and few.
+__global__ __launch_bounds__(256) void dgamma_kernel(int64_t rows, int d, const float* __restrict__ parts,
+                                                     float* __restrict__ dgamma, int accumulate) {
+  __shared__ float4 lds[32][9];
+  const int cl = threadIdx.x & 7, sl = threadIdx.x >> 3, c = blockIdx.x * 32 + cl * 4;   // d is a multiple of 32
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int64_t q = sl; q < rows; q += 32) {
+    const float4 p = *reinterpret_cast<const float4*>(parts + q * d + c);
+    v = make_float4(__fadd_rn(v.x, p.x), __fadd_rn(v.y, p.y), __fadd_rn(v.z, p.z), __fadd_rn(v.w, p.w));
+  }
   lds[sl][cl] = v;
   __syncthreads();
-  if (sl == 0) {
-    float sum = accumulate ? dgamma[c] : 0.0f;
+  if (threadIdx.x < 32) {
+    const int col = blockIdx.x * 32 + threadIdx.x;
+    const float* const f = reinterpret_cast<const float*>(lds);
+    float sum = accumulate ? dgamma[col] : 0.0f;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) sum = __fadd_rn(sum, lds[q][cl]);
-    dgamma[c] = sum;
+    for (int q = 0; q < 32; ++q) sum = __fadd_rn(sum, f[q * 36 + threadIdx.x]);
+    dgamma[col] = sum;
   }
 }
 
 // ---------------------------------------------------------------- host side
 constexpr int64_t kNormMaxD = 32768;                     // a row in the registers of 1024 threads, 32 values each
-constexpr int64_t kNormMaxGroups = 512;                  // rows of the backward's workspace
-
-static int64_t norm_groups(int64_t t) { return std::min(t, kNormMaxGroups); }
-
 // Calls f with the variant that holds a row of d columns: threads a row, groups of eight columns a thread.
 template <typename F>
 static void norm_variant(int64_t d, F&& f) {
@@ -317,12 +370,22 @@ static void norm_variant(int64_t d, F&& f) {
   if (d <= 128) MX_NORM(16, 1);
   else if (d <= 512) MX_NORM(64, 1);
   else if (d <= 1024) MX_NORM(64, 2);
-  else if (d <= 2048) MX_NORM(256, 1);
+  else if (d <= 1536) MX_NORM(64, 3);
+  else if (d <= 2048) MX_NORM(64, 4);
   else if (d <= 4096) MX_NORM(256, 2);
+  else if (d <= 6144) MX_NORM(256, 3);
   else if (d <= 8192) MX_NORM(256, 4);
-  else if (d <= 16384) MX_NORM(1024, 2);
+  else if (d <= 16384) MX_NORM(512, 4);
   else MX_NORM(1024, 4);
 #undef MX_NORM
+}
+
+// Workgroups of the backward pass, each of which leaves one row of partial
+// sums: two a CU where that gives each several rows, else one a CU at most (a
+// row of sums costs as much to write and read back as two rows of inputs).
+static int64_t norm_parts(int64_t t, int64_t d) {
+  const int64_t rows = d <= 128 ? 16 : d <= 2048 ? 4 : 1, groups = (t + rows - 1) / rows;
+  return groups >= 2048 ? 512 : std::min<int64_t>(groups, 256);
 }
 
 static bool dtype_ok(fp4_dtype t) { return t == FP4_BF16 || t == FP4_F32; }
@@ -384,14 +447,15 @@ fp4_status fp4_rmsnorm_producer(int64_t t, int64_t d, const void* x, fp4_dtype x
       hipLaunchKernelGGL(kernel, dim3((unsigned)((t + kRows - 1) / kRows)), dim3(G < 256 ? 256 : G), 0,
                          as_stream(stream), t, (int)d, x, ldx, residual, ldr, gamma, eps, drop, o);
     };
-    x_type == FP4_F32 ? go(rmsnorm_kernel<G, V, true>) : go(rmsnorm_kernel<G, V, false>);
+    if (residual) x_type == FP4_F32 ? go(rmsnorm_kernel<G, V, true, true>) : go(rmsnorm_kernel<G, V, false, true>);
+    else x_type == FP4_F32 ? go(rmsnorm_kernel<G, V, true, false>) : go(rmsnorm_kernel<G, V, false, false>);
   });
   return launch_status();
 }
 
 int64_t fp4_rmsnorm_backward_workspace(int64_t t, int64_t d) {
   if (t < 0 || !mult32z(d) || d > kNormMaxD) return -1;
-  return norm_groups(t) * d * (int64_t)sizeof(float);
+  return norm_parts(t, d) * d * (int64_t)sizeof(float);
 }
 
 fp4_status fp4_rmsnorm_backward(int64_t t, int64_t d, const void* dy, fp4_dtype dy_type, int64_t lddy,
@@ -411,19 +475,19 @@ fp4_status fp4_rmsnorm_backward(int64_t t, int64_t d, const void* dy, fp4_dtype 
       !aligned16(workspace) || (reinterpret_cast<uintptr_t>(rstd) & 3) || (reinterpret_cast<uintptr_t>(dgamma) & 3) ||
       !pitch_ok(dy_type, lddy) || lds % 8 != 0 || (ds && ldds % 8 != 0))
     return FP4_EALIGN;
-  const int64_t groups = norm_groups(t);
+  const int64_t rows = norm_parts(t, d);
   float* parts = static_cast<float*>(workspace);
   if (t > 0)
     norm_variant(d, [&](auto g, auto v) {
-      constexpr int G = g(), V = v(), kRows = G < 256 ? 256 / G : 1;
+      constexpr int G = g(), V = v();
       const auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)((groups + kRows - 1) / kRows)), dim3(G < 256 ? 256 : G), 0,
-                           as_stream(stream), t, (int)d, dy, lddy, s, lds, rstd, gamma, ds, ldds, drop, dsum, dx,
-                           parts, groups);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)rows), dim3(G < 256 ? 256 : G), 0, as_stream(stream), t, (int)d, dy,
+                           lddy, s, lds, rstd, gamma, ds, ldds, drop, dsum, dx, parts);
       };
-      dy_type == FP4_F32 ? go(rmsnorm_bwd_kernel<G, V, true>) : go(rmsnorm_bwd_kernel<G, V, false>);
+      if (ds) dy_type == FP4_F32 ? go(rmsnorm_bwd_kernel<G, V, true, true>) : go(rmsnorm_bwd_kernel<G, V, false, true>);
+      else dy_type == FP4_F32 ? go(rmsnorm_bwd_kernel<G, V, true, false>) : go(rmsnorm_bwd_kernel<G, V, false, false>);
     });
-  hipLaunchKernelGGL(dgamma_kernel, dim3((unsigned)(d / 32)), dim3(512), 0, as_stream(stream), groups, (int)d, parts,
+  hipLaunchKernelGGL(dgamma_kernel, dim3((unsigned)(d / 32)), dim3(256), 0, as_stream(stream), rows, (int)d, parts,
                      dgamma, accumulate);
   return launch_status();
 }

@@ -57,7 +57,8 @@ def check(got, x, w, prev=None):
 
 SHAPES = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (1, 5, 160), (3, 33, 128), (5, 64, 544), (16, 100, 1024), (17, 48, 2080),
           (31, 31, 256), (32, 257, 4096), (33, 19, 1056), (48, 16, 512), (64, 130, 640), (1, 1000, 8192), (64, 32, 14336),
-          (7, 4096, 288), (2, 515, 4128)]
+          (7, 4096, 288), (2, 515, 4128), (1, 9000, 512), (4, 20000, 256), (16, 8200, 4096), (3, 12289, 1536), (9, 6000, 6144),
+          (50, 5000, 1280), (20, 4200, 384)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -144,6 +145,21 @@ def test_strided_operands_leave_padding(gpu_lib):
     check(c, F.bf16_bits_to_f64(xb)[:, 8:8 + k], F.decode(codes, scales))
     o = host(buf)
     assert (o[m] == -3).all() and (o[:, :2] == -3).all() and (o[:, 2 + n:] == -3).all()
+
+
+@pytest.mark.parametrize("m,k", [(1, 512), (3, 1024), (5, 160), (20, 512), (40, 256)])
+@pytest.mark.parametrize("by", [1, 2, 4])
+def test_scales_at_any_address(gpu_lib, m, k, by):
+    """Scale rows that start off a word boundary (a slice of a larger buffer)."""
+    mx, n = gpu_lib, 50
+    x64, x, _ = activations(m, k, 20, "bf16")
+    codes, scales = weights(n, k, 21)
+    at = lambda a: torch.cat([torch.zeros(by, dtype=torch.uint8, device="cuda"), dev(a).flatten()])[by:].view(a.shape)  # noqa: E731
+    check(mx.fp4_matvec(x, dev(codes), at(scales)), x64, F.decode(codes, scales))
+    s4 = np.random.default_rng(22).integers(0, 0x7F, (n, k // 16), dtype=np.uint8)
+    check(mx.fp4_nv_matvec(x, dev(codes), at(s4), torch.ones(1, device="cuda")), x64, NV.decode(codes, s4))
+    xe, xc, xs = activations(m, k, 23, "e4m3")
+    check(mx.fp4_matvec(xc, dev(codes), at(scales), at(host(xs))), xe, F.decode(codes, scales))
 
 
 def test_empty_reduction_and_empty_outputs(gpu_lib):
