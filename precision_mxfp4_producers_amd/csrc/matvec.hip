@@ -191,10 +191,10 @@ constexpr int kScaleWords = WT == kMx ? U : 2 * U;
 
 // One item of W as loaded: pieces of codes, and one word of a row's scale
 // bytes; of a partial step the four bytes that this lane's products take.
-template <int WT, int U, bool WHOLE>
+template <int WT, int NT, int U, bool WHOLE>
 struct MvItem {
-  v4i c[U];
-  uint32_t s[WHOLE ? 1 : 4];
+  v4i c[NT][U];
+  uint32_t s[NT][WHOLE ? 1 : 4];
 };
 
 // One step of x, as loaded: sixteen bytes a lane, 16 (bf16) or 8 (E4M3) lanes a row.
@@ -208,12 +208,13 @@ struct MvX {
 // global loads stay in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int XT, int WT, int MT, int NW, int U, bool GATE, bool STAGED, bool WHOLE>
+template <int XT, int WT, int MT, int NT, int NW, int U, bool GATE, bool STAGED, bool WHOLE>
 __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan plan) {
+  static_assert(!STAGED || (MT == 1 && NT == 1), "sixteen rows of x and one tile at a time");
   static_assert((WHOLE && STAGED) || U == 1, "a partial step, and one that brings its x, is an item of its own");
   constexpr int ROWS = GATE ? 8 : 16;                    // output columns of a tile
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
-  constexpr int kWaveFloats = STAGED ? MT * 256 + 4 : room_bytes(MT) / 4;   // between two waves' partial sums
+  constexpr int kWaveFloats = STAGED ? 260 : room_bytes(MT) / 4;   // between two waves' partial sums
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   // the staged x behind the partial sums; or this wave's room
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
   const int64_t kc = a.k >> 1, ks = a.k >> (WT == kMx ? 5 : 4);   // bytes of a row's codes and scales
   const int steps = (int)((a.k + 127) >> 7), items = (steps + U - 1) / U;
   const int per = (items + (1 << plan.kw_log2) - 1) >> plan.kw_log2;   // turns of a wave per tile
-  const int64_t tiles = (a.n + ROWS - 1) / ROWS, groups = (tiles + RT - 1) / RT;
+  const int64_t groups = (a.n + ROWS * NT * RT - 1) / (ROWS * NT * RT);
   const __amdgpu_buffer_rsrc_t rx =
       buffer_rsrc(a.x, XT == kXBf16 ? ((a.m - 1) * a.ldx + a.k) * 2 : (int64_t)a.m * a.k);
   const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(a.x_scales, XT == kXBf16 ? 0 : (int64_t)a.m * (a.k >> 5));
@@ -237,27 +238,30 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     return it < items ? it : it - items;
   };
   // A row past the end reads the last one (its sums are not stored).
-  const auto row_of = [&](int64_t group, int r) {
-    return std::min((group * RT + rt) * ROWS + (r & (ROWS - 1)), a.n - 1) + (GATE && r >= ROWS ? a.n : 0);
+  const auto row_of = [&](int64_t group, int j, int r) {
+    return std::min(((group * RT + rt) * NT + j) * ROWS + (r & (ROWS - 1)), a.n - 1) + (GATE && r >= ROWS ? a.n : 0);
   };
-  const auto load_w = [&](MvItem<WT, U, WHOLE>& it, int64_t group, int turn) {
+  const auto load_w = [&](MvItem<WT, NT, U, WHOLE>& it, int64_t group, int turn) {
     const int item = item_of(turn), piece = lane & 3;
-    const int64_t row = row_of(group, 4 * ((lane >> 2) & 3) + (lane >> 4));
-    const uint8_t* const c = a.codes + row * kc;
-    if constexpr (WHOLE) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) it.c[u] = *reinterpret_cast<const v4i*>(c + (item * U + u) * 64 + piece * 16);
-      constexpr int D = kScaleWords<WT, U>;
-      it.s[0] = reinterpret_cast<const uint32_t*>(a.scales + row * ks)[item * D + (piece & (D - 1))];
-    } else {
-      const int blocks = (int)(a.k >> 5), kb = item * 4;  // a block of 32 values is whole or absent
-      const uint8_t* const s = a.scales + row_of(group, r) * ks;
-      const v4i v = *reinterpret_cast<const v4i*>(c + std::min(kb + piece, blocks - 1) * 16);
-      it.c[0] = kb + piece < blocks ? v : v4i{0, 0, 0, 0};
+    for (int j = 0; j < NT; ++j) {
+      const int64_t row = row_of(group, j, 4 * ((lane >> 2) & 3) + (lane >> 4));
+      const uint8_t* const c = a.codes + row * kc;
+      if constexpr (WHOLE) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = std::min(kb + q, blocks - 1);
-        it.s[q] = WT == kMx ? s[at] : s[2 * at + (g >> 1)];
+        for (int u = 0; u < U; ++u) it.c[j][u] = *reinterpret_cast<const v4i*>(c + (item * U + u) * 64 + piece * 16);
+        constexpr int D = kScaleWords<WT, U>;
+        it.s[j][0] = reinterpret_cast<const uint32_t*>(a.scales + row * ks)[item * D + (piece & (D - 1))];
+      } else {
+        const int blocks = (int)(a.k >> 5), kb = item * 4;   // a block of 32 values is whole or absent
+        const uint8_t* const s = a.scales + row_of(group, j, r) * ks;
+        const v4i v = *reinterpret_cast<const v4i*>(c + std::min(kb + piece, blocks - 1) * 16);
+        it.c[j][0] = kb + piece < blocks ? v : v4i{0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int at = std::min(kb + q, blocks - 1);
+          it.s[j][q] = WT == kMx ? s[at] : s[2 * at + (g >> 1)];
+        }
       }
     }
   };
@@ -301,47 +305,56 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     }
   };
 
-  v4f acc[MT];
+  v4f acc[MT][NT];
   const uint32_t xrow = (STAGED ? (uint32_t)(r < a.m ? r : 0) * (uint32_t)stage_pitch(a.k) : (uint32_t)r * kXPitch) + g * 16;
-  const auto multiply = [&](const MvItem<WT, U, WHOLE>& it, int turn) {
+  const auto multiply = [&](const MvItem<WT, NT, U, WHOLE>& it, int turn) {
     if (kw + (turn << plan.kw_log2) >= items) return;    // wave-uniform
     const int item = item_of(turn);
     // the item's scale words of this lane's row r, from the lanes that loaded the row
-    uint32_t sw[kScaleWords<WT, U>];
+    uint32_t sw[NT][kScaleWords<WT, U>];
     if constexpr (WHOLE)
 #pragma unroll
-      for (int d = 0; d < kScaleWords<WT, U>; ++d)
-        sw[d] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * (4 * (r & 3) + (r >> 2)) + d), (int)it.s[0]);
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int d = 0; d < kScaleWords<WT, U>; ++d)
+          sw[j][d] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * (4 * (r & 3) + (r >> 2)) + d), (int)it.s[j][0]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      bf16x8_t w[4];
-      uint32_t c[4] = {(uint32_t)it.c[u][0], (uint32_t)it.c[u][1], (uint32_t)it.c[u][2], (uint32_t)it.c[u][3]};
-      to_operand(c);
-      float sc[4];                                       // the scale of product q's values
-      if constexpr (WT == kMx && WHOLE) {
-        sc[0] = e8m0_byte<0>(sw[u]);
-        sc[1] = e8m0_byte<1>(sw[u]);
-        sc[2] = e8m0_byte<2>(sw[u]);
-        sc[3] = e8m0_byte<3>(sw[u]);
-      } else if constexpr (WT == kMx) {
+      bf16x8_t w[NT][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sc[q] = __uint_as_float(it.s[q] << 23);
-      } else {
+      for (int j = 0; j < NT; ++j) {
+        const v4i cw = it.c[j][u];
+        uint32_t c[4] = {(uint32_t)cw[0], (uint32_t)cw[1], (uint32_t)cw[2], (uint32_t)cw[3]};
+        to_operand(c);
+        float sc[4];                                     // the scale of product q's values
+        if constexpr (WT == kMx && WHOLE) {
+          sc[0] = e8m0_byte<0>(sw[j][u]);
+          sc[1] = e8m0_byte<1>(sw[j][u]);
+          sc[2] = e8m0_byte<2>(sw[j][u]);
+          sc[3] = e8m0_byte<3>(sw[j][u]);
+        } else if constexpr (WT == kMx) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t b = WHOLE ? (sw[2 * u + (q >> 1)] >> (16 * (q & 1) + 8 * (g >> 1))) & 0xFFu : it.s[q];
-          const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 1.0f, false);
-          sc[q] = d[0];
+          for (int q = 0; q < 4; ++q) sc[q] = __uint_as_float(it.s[j][q] << 23);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t b = WHOLE ? (sw[j][2 * u + (q >> 1)] >> (16 * (q & 1) + 8 * (g >> 1))) & 0xFFu : it.s[j][q];
+            const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 1.0f, false);
+            sc[q] = d[0];
+          }
         }
-      }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) w[q] = decode8<WT>(c[q], sc[q]);
+        for (int q = 0; q < 4; ++q) w[j][q] = decode8<WT>(c[q], sc[q]);
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const uint8_t* const x = stage + xrow + (STAGED ? (uint32_t)(item * U + u) * 256 : (uint32_t)i * 16 * kXPitch);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[q], *reinterpret_cast<const bf16x8_t*>(x + 64 * q), acc[i], 0, 0, 0);
+        for (int q = 0; q < 4; ++q) {
+          const bf16x8_t xq = *reinterpret_cast<const bf16x8_t*>(x + 64 * q);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][q], xq, acc[i][j], 0, 0, 0);
+        }
       }
     }
   };
@@ -352,7 +365,7 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
   const float* const rf = reinterpret_cast<const float*>(lds);
   const auto finish = [&](int64_t group, int slots) {     // group: the first one since the last meeting
     lds_barrier();
-    const int split = plan.kw_log2 - 2, sums = 16 * a.m;  // of a tile: 16 rows of W, m rows of x
+    const int split = plan.kw_log2 - 2, sums = 16 * NT * a.m;   // of a wave's tiles: 16 NT rows of W, m rows of x
     const int count = (slots * RT * sums) << split;
     for (int e0 = wave * 64; e0 < count; e0 += NW * 64) {
       const int e = e0 + lane, part = e & ((1 << split) - 1);
@@ -361,14 +374,16 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
       if (GATE) q >>= 1;
       const int nl = q & (ROWS - 1);
       q /= ROWS;
+      const int j = q & (NT - 1);
+      q /= NT;
       const int mr = (int)((uint32_t)q % (uint32_t)a.m);
       q = (int)((uint32_t)q / (uint32_t)a.m);
       const int t = q & (RT - 1), slot = q / RT, wr = nl + ROWS * ab;
-      const float* const p = rf + (slot * NW + (t << plan.kw_log2) + 4 * part) * kWaveFloats + (mr >> 4) * 256 +
+      const float* const p = rf + (slot * NW + (t << plan.kw_log2) + 4 * part) * kWaveFloats + ((mr >> 4) * NT + j) * 256 +
                              ((wr >> 2) * 16 + (mr & 15)) * 4 + (wr & 3);
       float v = __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[kWaveFloats]), p[2 * kWaveFloats]), p[3 * kWaveFloats]);
       for (int s = 1; s < 1 << split; s <<= 1) v = __fadd_rn(v, __shfl_xor(v, s, 64));
-      const int64_t row = ((group + (int64_t)slot * gridDim.x) * RT + t) * ROWS + nl;
+      const int64_t row = (((group + (int64_t)slot * gridDim.x) * RT + t) * NT + j) * ROWS + nl;
       if constexpr (GATE) {
         const float other = __shfl_xor(v, 1 << split, 64);
         const float av = bf16_bits_to_f32(f32_to_bf16_rne(ab ? other : v));
@@ -395,7 +410,7 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
   const auto step = [&](int64_t& gr, int& tn) {
     if (++tn == per) { tn = 0; gr += gridDim.x; }
   };
-  using W = MvItem<WT, U, WHOLE>;
+  using W = MvItem<WT, NT, U, WHOLE>;
   MvX<XT, MT> x;                                         // the next step of x, on its way to the wave's room
   const auto ahead = [&](W& w) {                         // loads of the item after the current one
     int64_t gr = group;
@@ -419,10 +434,12 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     if constexpr (STAGED) __builtin_amdgcn_s_barrier();
     if (turn + 1 == per) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        reinterpret_cast<v4f*>(lds)[(slots * NW + wave) * (kWaveFloats / 4) + i * 64 + lane] = acc[i];
-        acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      }
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          reinterpret_cast<v4f*>(lds)[(slots * NW + wave) * (kWaveFloats / 4) + (i * NT + j) * 64 + lane] = acc[i][j];
+          acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        }
       ++slots;
     }
     step(group, turn);
@@ -482,7 +499,9 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     }
   };
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   W w0, w1;
   begin([&] {
     load_w(w0, first, 0);
@@ -542,46 +561,50 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   const int64_t tiles = (a.n + ROWS - 1) / ROWS, steps = (a.k + 127) / 128;
   const bool staged = a.m <= 16 && a.m * stage_pitch(a.k) <= kStageBytes;
   const int mt = (a.m + 15) / 16, nw = mt > 1 ? 8 : 16;
+  // Where x is not staged its way through LDS bounds the kernel (110 cycles a
+  // step and 16 rows): two tiles of W a wave share it, if there are as many for
+  // every CU (33 rows on 8192 x 14336: 37 to 25 us, NVFP4 38 to 29; with up to
+  // 16 rows MXFP4 18 to 15.6, NVFP4 20.3 to 21.5, which keeps one).
+  const bool words = (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0, whole = a.k % 128 == 0 && words;
+  const int nt = !staged && whole && tiles >= 2 * kMatvecGrid && (WT == kMx || mt > 1) ? 2 : 1;
   // Waves per tile and steps per item: the pair whose longest workgroup has
   // the fewest steps to walk; longer items and fewer waves a tile where equal.
-  const bool words = (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0;
   int u = 1, kw = 4;
   int64_t best = INT64_MAX;
+  const auto groups_of = [&](int log2) { return (tiles + nt * (nw >> log2) - 1) / (nt * (nw >> log2)); };
   constexpr int kMaxU = WT == kMx ? 4 : 2;               // what the registers hold
   for (int uu = staged ? kMaxU : 1; uu >= 1; uu >>= 1) {
     if (uu > 1 && (a.k % (128 * uu) != 0 || !words)) continue;
     for (int log2 = 2; log2 <= (nw == 16 ? 4 : 3); ++log2) {
-      const int64_t rounds = ((tiles + (nw >> log2) - 1) / (nw >> log2) + kMatvecGrid - 1) / kMatvecGrid;
+      const int64_t rounds = (groups_of(log2) + kMatvecGrid - 1) / kMatvecGrid;
       const int64_t cost = rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2) * uu;
       if (cost < best) best = cost, u = uu, kw = log2;
     }
   }
-  const bool whole = a.k % 128 == 0 && words;
-  const int64_t groups = (tiles + (nw >> kw) - 1) / (nw >> kw), slot = (int64_t)nw * (mt * 256 + 4) * 4;
   // groups of tiles between two meetings of the sums: what LDS holds beside x
+  const int64_t slot = 16 * 260 * 4;
   const MvPlan plan{kw, staged ? (int)std::min<int64_t>((kLds - a.m * stage_pitch(a.k)) / slot, 4) : 1};
-  const auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(groups, kMatvecGrid)), dim3(nw * 64), 0, stream, a, plan);
-  };
+  const unsigned grid = (unsigned)std::min(groups_of(kw), kMatvecGrid);
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(nw * 64), 0, stream, a, plan); };
   if (staged) {
-    if (u == 2) go(matvec_kernel<XT, WT, 1, 16, 2, GATE, true, true>);
-    else if (u == 1 && whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, true, true>);
-    else if (u == 1) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, true, false>);
+    if (u == 2) go(matvec_kernel<XT, WT, 1, 1, 16, 2, GATE, true, true>);
+    else if (u == 1 && whole) go(matvec_kernel<XT, WT, 1, 1, 16, 1, GATE, true, true>);
+    else if (u == 1) go(matvec_kernel<XT, WT, 1, 1, 16, 1, GATE, true, false>);
     if constexpr (kMaxU == 4)
-      if (u == 4) go(matvec_kernel<XT, WT, 1, 16, 4, GATE, true, true>);
-  } else if (mt == 1) {
-    if (whole) go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, true>);
-    else go(matvec_kernel<XT, WT, 1, 16, 1, GATE, false, false>);
-  } else if (mt == 2) {
-    if (whole) go(matvec_kernel<XT, WT, 2, 8, 1, GATE, false, true>);
-    else go(matvec_kernel<XT, WT, 2, 8, 1, GATE, false, false>);
-  } else if (mt == 3) {
-    if (whole) go(matvec_kernel<XT, WT, 3, 8, 1, GATE, false, true>);
-    else go(matvec_kernel<XT, WT, 3, 8, 1, GATE, false, false>);
-  } else {
-    if (whole) go(matvec_kernel<XT, WT, 4, 8, 1, GATE, false, true>);
-    else go(matvec_kernel<XT, WT, 4, 8, 1, GATE, false, false>);
+      if (u == 4) go(matvec_kernel<XT, WT, 1, 1, 16, 4, GATE, true, true>);
+    return launch_status();
   }
+  const auto own = [&](auto mtc) {                       // each wave brings its own steps of x
+    constexpr int MT = mtc(), NW = MT > 1 ? 8 : 16;
+    if constexpr (WT == kMx || MT > 1)
+      if (nt == 2) return go(matvec_kernel<XT, WT, MT, 2, NW, 1, GATE, false, true>);
+    whole ? go(matvec_kernel<XT, WT, MT, 1, NW, 1, GATE, false, true>)
+          : go(matvec_kernel<XT, WT, MT, 1, NW, 1, GATE, false, false>);
+  };
+  if (mt == 1) own(std::integral_constant<int, 1>{});
+  else if (mt == 2) own(std::integral_constant<int, 2>{});
+  else if (mt == 3) own(std::integral_constant<int, 3>{});
+  else own(std::integral_constant<int, 4>{});
   return launch_status();
 }
 
