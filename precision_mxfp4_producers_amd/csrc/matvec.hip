@@ -6,6 +6,17 @@
 // the activations stay in bf16 or come as the E4M3 codes of
 // fp4_rmsnorm_producer.
 //
+// The decoded weights are exact in bf16, so that the products run on the bf16
+// matrix cores with fp32 sums, 4e-8 from float64 in the 2-norm (the scaled
+// 8-bit by 4-bit products were 4e-6 from it after 32 steps).
+//
+// Bound by HBM for few rows: 57344 x 8192 MXFP4 with five E4M3 rows, 250 MB,
+// 49 us (5.1 TB/s; a bare loop of the same loads takes 41, contiguous loads
+// 34); gate/up 14336 x 4096 with one row, 62 MB, 13.6 us; 4096 x 4096 with one
+// row, 9 MB, 4.8 us (a bare loop 3.8).  With more rows x's way through LDS
+// takes over: gate/up 14336 x 4096 with 16 rows 20.8 us, 4096 x 14336 NVFP4
+// with 33 rows 22 us.
+//
 // Method: "Format-Aware Fusion for Fast FP4 Pretraining", §2.2 (Eq. 1) decode,
 // §2.4 row layouts, §3.2 gated FFN.
 #include <hip/hip_runtime.h>

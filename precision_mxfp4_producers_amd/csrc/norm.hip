@@ -48,6 +48,8 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
 
 // ---------------------------------------------------------------- dropout
 // out = bf16(dropout(x) [+ residual]); one thread per group of eight columns.
+// Bound by HBM: bf16 8192 x 14336, 470 MB, takes 80 us (5.9 TB/s; a 1 GiB copy
+// moves 5.2); the generator is some 400 of a wave's cycles per 3 KB.
 // VEC: every row of every tensor starts on a 16-byte boundary; a group that
 // runs past the row's end, and every group otherwise, goes element by element
 // (a view's last row may end with its last element).
@@ -142,9 +144,10 @@ struct NormOut {
 // residual are read once.  Four neighbouring lanes hold one 32-value block.
 //
 // No branch surrounds a load (a row or column past the end reads the last
-// one), and all of a thread's loads go out before its first use: with the
-// loads of each group behind the stores of the one before, 8192 x 4096 with
-// dropout took 89 us.
+// one), and all of a thread's loads go out before its first use: 8192 x 4096,
+// fp32 x with dropout and residual to s and E4M3, 302 MB, takes 51 us (5.9
+// TB/s), and took 89 with the loads of each group of columns behind the stores
+// of the one before.  Bound by HBM; one token by its launch (2.8 us).
 template <int G, int V, bool F32, bool RES>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, int d, const void* __restrict__ x,
                                                                     int64_t ldx, const uint16_t* __restrict__ residual,
@@ -218,7 +221,9 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, i
 // G threads hold a row, as in the forward.  A workgroup walks rows in steps of
 // the whole grid, loads the next row's tensors before it works on the current
 // one, keeps its columns' share of dgamma in registers and writes it once, as
-// one row of the workspace.
+// one row of the workspace.  Bound by HBM: fp32 dy 8192 x 4096 with ds and
+// dropout, 402 MB, takes 68 us and 5 for the sums of dgamma (88 and 10 without
+// the next row's loads and with one column a thread in the sums).
 template <int V, bool F32, bool DS>
 struct BwdRow {
   float dy[V][8];
@@ -384,7 +389,7 @@ static void norm_variant(int64_t d, F&& f) {
 // sums: two a CU where that gives each several rows, else one a CU at most (a
 // row of sums costs as much to write and read back as two rows of inputs).
 static int64_t norm_parts(int64_t t, int64_t d) {
-  const int64_t rows = d <= 128 ? 16 : d <= 2048 ? 4 : 1, groups = (t + rows - 1) / rows;
+  const int64_t rows = d <= 128 ? 16 : d <= 2048 ? 4 : 1, groups = t / rows + (t % rows != 0);
   return groups >= 2048 ? 512 : std::min<int64_t>(groups, 256);
 }
 
