@@ -58,7 +58,8 @@ def check(got, x, w, prev=None):
 SHAPES = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (1, 5, 160), (3, 33, 128), (5, 64, 544), (16, 100, 1024), (17, 48, 2080),
           (31, 31, 256), (32, 257, 4096), (33, 19, 1056), (48, 16, 512), (64, 130, 640), (1, 1000, 8192), (64, 32, 14336),
           (7, 4096, 288), (2, 515, 4128), (1, 9000, 512), (4, 20000, 256), (16, 8200, 4096), (3, 12289, 1536), (9, 6000, 6144),
-          (50, 5000, 1280), (20, 4200, 384)]
+          (50, 5000, 1280), (20, 4200, 384), (16, 40, 4544), (16, 40, 4576), (12, 8300, 8192), (33, 8192, 256),
+          (64, 8209, 128)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -118,20 +119,21 @@ def test_matvec_every_code_and_scale(gpu_lib):
         assert np.array_equal(got, want), byte
 
 
-def test_non_finite_rows_stay_apart(gpu_lib):
+@pytest.mark.parametrize("m,n,k", [(4, 20, 96), (20, 20, 96), (40, 20, 256), (60, 8200, 128), (16, 20, 4640)])
+def test_non_finite_rows_stay_apart(gpu_lib, m, n, k):
     """An infinity or NaN in one row of x does not reach the other rows, nor do
     values in the row's padding."""
-    k = 96
-    codes, scales = weights(20, k, 7)
-    xb = synthetic.tensor((4, 128), seed=8)
+    codes, scales = weights(n, k, 7)
+    xb = synthetic.tensor((m, k + 32), seed=8)
     xd = dev16(xb).clone()
     xd[1, 3] = float("inf")
-    xd[2, 90] = float("nan")
+    xd[2, k - 6] = float("nan")
     xd[:, k:] = float("nan")
     got = host(gpu_lib.fp4_matvec(xd[:, :k], dev(codes), dev(scales)))
     x64 = F.bf16_bits_to_f64(xb)[:, :k]
     ref, e = x64 @ F.decode(codes, scales).T, np.abs(x64) @ np.abs(F.decode(codes, scales)).T
-    assert G.within_bound(got[[0, 3]], ref[[0, 3]], e[[0, 3]], k=k).all()
+    rest = [0, *range(3, m)]
+    assert G.within_bound(got[rest], ref[rest], e[rest], k=k).all()
     assert np.isnan(got[2]).all() and not np.isfinite(got[1]).any()
 
 
@@ -277,3 +279,26 @@ def test_refusals_of_the_binding(gpu_lib):
         with pytest.raises(mx.Fp4Error):
             f()
             pytest.fail(f"call {k} was not refused")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(gpu_lib, seed):
+    """Shapes drawn over the whole range (logarithmic), each call once."""
+    mx, rng = gpu_lib, np.random.default_rng(1000 + seed)
+    log = lambda lo, hi: int(round(np.exp(rng.uniform(np.log(lo), np.log(hi)))))  # noqa: E731
+    m, n, k = log(1, 64), log(1, 3000), 32 * log(1, 300)
+    kind = ("bf16", "e4m3")[seed % 2]
+    x64, x, xs = activations(m, k, 2000 + seed, kind)
+    codes, scales = weights(n, k, 3000 + seed)
+    check(mx.fp4_matvec(x, dev(codes), dev(scales), xs), x64, F.decode(codes, scales))
+    if kind == "bf16":
+        s4 = rng.integers(0, 0x7F, (n, k // 16), dtype=np.uint8)
+        check(mx.fp4_nv_matvec(x, dev(codes), dev(s4), torch.ones(1, device="cuda")), x64, NV.decode(codes, s4))
+    if n % 2 == 0:
+        # the gate, in the 2-norm: two rounded factors and the result
+        lo = (scales - 4 - int(np.log2(k) / 2)).astype(np.uint8)
+        ab = x64 @ F.decode(codes, lo).T
+        a, b = ab[:, :n // 2], ab[:, n // 2:]
+        h = host(mx.fp4_swiglu_matvec(x, dev(codes), dev(lo), xs).float()).astype(np.float64)
+        want = a / (1 + np.exp(-a)) * b
+        assert np.linalg.norm(h - want) <= 3 * H * np.linalg.norm(want) + 1e-30

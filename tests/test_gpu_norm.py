@@ -277,3 +277,33 @@ def test_refusals_of_the_binding(gpu_lib):
         with pytest.raises(mx.Fp4Error):
             f()
             pytest.fail(f"call {k} was not refused")
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_shapes(gpu_lib, seed):
+    """Shapes drawn over the whole range: the sum and the codes exactly, y and
+    the gradients in the 2-norm (their roundings, and 2^-16 for the fp32 sums)."""
+    mx, rng = gpu_lib, np.random.default_rng(500 + seed)
+    log = lambda lo, hi: int(round(np.exp(rng.uniform(np.log(lo), np.log(hi)))))  # noqa: E731
+    t, d, p, f32 = log(1, 1500), 32 * log(1, 512), (0.0, 0.1, 0.6)[seed % 3], seed % 2 == 1
+    t = max(1, min(t, (1 << 21) // d))
+    x, xd = inputs((t, d), 600 + seed, f32)
+    rb = synthetic.tensor((t, d), std=1.0, seed=700 + seed) if seed % 4 else None
+    gb = synthetic.bf16_bits((1 + 0.2 * rng.standard_normal(d)).astype(np.float32))
+    sb = N.dropout_bits(x, p, seed, seed, rb)
+    s, rstd, y, codes, scales = mx.fp4_rmsnorm_producer(xd, dev16(gb), 1e-5, None if rb is None else dev16(rb), p, seed,
+                                                        seed, emit_y=True)
+    assert np.array_equal(bits(s), sb)
+    want = N.encode_e4m3(bits(y))
+    assert np.array_equal(host(codes), want[0]) and np.array_equal(host(scales), want[1])
+    s64, g64 = F.bf16_bits_to_f64(sb), F.bf16_bits_to_f64(gb)
+    near = lambda got, ref, tol: np.linalg.norm(got - ref) <= tol * np.linalg.norm(ref)  # noqa: E731
+    r64, y64 = N.rmsnorm(s64, g64, 1e-5)
+    assert near(host(rstd), r64, 2.0 ** -18) and near(val(y), y64, H)
+    db = None if rb is None else dev16(rb)
+    dsum, dx, dgamma = mx.fp4_rmsnorm_backward(xd, s, rstd, dev16(gb), db, p, seed, seed)
+    ds, dg = N.rmsnorm_backward(x.astype(np.float64), s64, host(rstd).astype(np.float64), g64,
+                                None if rb is None else F.bf16_bits_to_f64(rb))
+    assert near(val(dsum), ds, H + 2.0 ** -16) and near(host(dgamma), dg, 2.0 ** -16)
+    keep, sc = N.keep_mask(t, d, p, seed, seed), float(N.keep_scale(p))
+    assert near(val(dx), np.where(keep, ds * sc, 0.0), H + 2.0 ** -16)
