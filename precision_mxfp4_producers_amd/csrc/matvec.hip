@@ -14,7 +14,7 @@
 // 49 us (5.1 TB/s; a bare loop of the same loads takes 41, contiguous loads
 // 34); gate/up 14336 x 4096 with one row, 62 MB, 13.6 us; 4096 x 4096 with one
 // row, 9 MB, 4.8 us (a bare loop 3.8).  With more rows x's way through LDS
-// takes over: gate/up 14336 x 4096 with 16 rows 20.8 us, 4096 x 14336 NVFP4
+// takes over: gate/up 14336 x 4096 with 16 rows 16.6 us, 4096 x 14336 NVFP4
 // with 33 rows 22 us.
 //
 // Method: "Format-Aware Fusion for Fast FP4 Pretraining", §2.2 (Eq. 1) decode,
@@ -397,11 +397,12 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
       const int64_t row = (((group + (int64_t)slot * gridDim.x) * RT + t) * NT + j) * ROWS + nl;
       if constexpr (GATE) {
         const float other = __shfl_xor(v, 1 << split, 64);
-        const float av = bf16_bits_to_f32(f32_to_bf16_rne(ab ? other : v));
-        const float bv = bf16_bits_to_f32(f32_to_bf16_rne(ab ? v : other));
-        float sig, sl;
-        sigmoid_silu(av, sig, sl);
-        if (e < count && part == 0 && ab == 0 && row < a.n) a.h[mr * a.n + row] = (uint16_t)f32_to_bf16_rne(__fmul_rn(sl, bv));
+        const uint32_t both = ab ? bf16_pack2_rne(other, v) : bf16_pack2_rne(v, other);   // a low, b high
+        const float av[1] = {__uint_as_float(both << 16)};
+        float sig[1], sl[1];
+        sigmoid_silu_n(av, sig, sl);
+        if (e < count && part == 0 && ab == 0 && row < a.n)
+          a.h[mr * a.n + row] = (uint16_t)bf16_pack2_rne(__fmul_rn(sl[0], __uint_as_float(both & 0xFFFF0000u)), 0.0f);
       } else if (e < count && part == 0 && row < a.n) {
         if constexpr (WT == kNv) v = __fmul_rn(a.factors[(row >> 8) * a.factor_stride], v);
         float* const c = a.c + mr * a.ldc + row;
@@ -578,8 +579,14 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   // 16 rows MXFP4 18 to 15.6, NVFP4 20.3 to 21.5, which keeps one).
   const bool words = (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0, whole = a.k % 128 == 0 && words;
   const int nt = !staged && whole && tiles >= 2 * kMatvecGrid && (WT == kMx || mt > 1) ? 2 : 1;
+  // groups of tiles between two meetings of the sums: what LDS holds beside x
+  const int64_t slot = 16 * 260 * 4;
+  const int batch = staged ? (int)std::min<int64_t>((kLds - a.m * stage_pitch(a.k)) / slot, 4) : 1;
   // Waves per tile and steps per item: the pair whose longest workgroup has
-  // the fewest steps to walk; longer items and fewer waves a tile where equal.
+  // the fewest steps to walk, a meeting of the sums counted as one (both take
+  // some 0.8 us; 16 rows on gate/up 14336 x 4096, whose x leaves room for one
+  // group's sums: 20.7 us without counting them, 16.6 with); longer items
+  // and fewer waves a tile where equal.
   int u = 1, kw = 4;
   int64_t best = INT64_MAX;
   const auto groups_of = [&](int log2) { return (tiles + nt * (nw >> log2) - 1) / (nt * (nw >> log2)); };
@@ -588,13 +595,12 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
     if (uu > 1 && (a.k % (128 * uu) != 0 || !words)) continue;
     for (int log2 = 2; log2 <= (nw == 16 ? 4 : 3); ++log2) {
       const int64_t rounds = (groups_of(log2) + kMatvecGrid - 1) / kMatvecGrid;
-      const int64_t cost = rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2) * uu;
+      const int64_t cost =
+          rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2) * uu + (rounds + batch - 1) / batch;
       if (cost < best) best = cost, u = uu, kw = log2;
     }
   }
-  // groups of tiles between two meetings of the sums: what LDS holds beside x
-  const int64_t slot = 16 * 260 * 4;
-  const MvPlan plan{kw, staged ? (int)std::min<int64_t>((kLds - a.m * stage_pitch(a.k)) / slot, 4) : 1};
+  const MvPlan plan{kw, batch};
   const unsigned grid = (unsigned)std::min(groups_of(kw), kMatvecGrid);
   const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(nw * 64), 0, stream, a, plan); };
   if (staged) {
