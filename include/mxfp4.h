@@ -474,8 +474,10 @@ fp4_status fp4_dropout(int64_t rows, int64_t cols, const void* x, fp4_dtype x_ty
  * codes its consumer reads).
  *   s    = dropout(x) + residual as fp4_dropout (p = 0: x + residual; no
  *          residual: x), rounded to bf16
- *   rstd = 1 / sqrt(mean(s^2) + eps)             fp32, of the rounded s
- *   y    = bf16((s * rstd) * gamma)              fp32, single roundings
+ *   rstd = 1 / sqrt(mean(s^2) + eps)             of the rounded s; squares summed
+ *          in fp32 within a thread (at most 32) and in 64 bits beyond, then fp32
+ *   y    = bf16(s * rstd * gamma)                with the 64-bit rstd, one fp32
+ *          rounding before bf16's
  * and the codes of y in blocks of 32 along d:
  *   FP4_E2M1: the bytes of fp4_quantize_rows(y, FP4_RTN) (input of fp4_gemm
  *             and fp4_swiglu_producer);
@@ -489,7 +491,7 @@ fp4_status fp4_dropout(int64_t rows, int64_t cols, const void* x, fp4_dtype x_ty
  *   y         [t][d] bf16 or NULL (e.g. for fp4_quantize_cols)
  *   codes     [t][d/2] (E2M1) or [t][d] (E4M3), scales [t][d/32]; both or
  *             neither NULL
- * |s| must stay below 2^63 / sqrt(d) (the squares are summed in fp32).
+ * |s| must stay below 2^60 (the squares are summed in fp32).
  * Errors: FP4_EINVAL bad x_type or format, p outside [0, 1], eps not a
  * positive finite number, exactly one of codes, scales NULL, or another null
  * pointer; FP4_ESHAPE t negative or above 2^31 - 1, d not a non-negative

@@ -90,17 +90,17 @@ __global__ __launch_bounds__(256) void dropout_kernel(int64_t groups, uint32_t p
 // Sum over the G threads of a row (G a power of two, 16 <= G <= 1024): lanes
 // of a wave by exchanges, waves of a workgroup through LDS in wave order.  The
 // same value in every thread of the row.
-template <int G>
-__device__ __forceinline__ float row_sum(float v, float* lds) {
+template <int G, typename T>
+__device__ __forceinline__ T row_sum(T v, T* lds) {
 #pragma unroll
-  for (int s = 1; s < (G < 64 ? G : 64); s <<= 1) v = __fadd_rn(v, __shfl_xor(v, s, 64));
+  for (int s = 1; s < (G < 64 ? G : 64); s <<= 1) v = v + __shfl_xor(v, s, 64);
   if constexpr (G > 64) {
     __syncthreads();                                     // the previous use of lds is over
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.0f;
+    v = 0;
 #pragma unroll
-    for (int w = 0; w < G / 64; ++w) v = __fadd_rn(v, lds[w]);
+    for (int w = 0; w < G / 64; ++w) v = v + lds[w];
   }
   return v;
 }
@@ -152,9 +152,9 @@ template <int G, int V, bool F32, bool RES>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, int d, const void* __restrict__ x,
                                                                     int64_t ldx, const uint16_t* __restrict__ residual,
                                                                     int64_t ldr, const uint16_t* __restrict__ gamma,
-                                                                    float eps, Dropout drop, NormOut o) {
+                                                                    float eps, double inv_d, Dropout drop, NormOut o) {
   constexpr int kRows = G < 256 ? 256 / G : 1;
-  __shared__ float lds[16];
+  __shared__ double lds[16];
   const int i = threadIdx.x & (G - 1);
   const int64_t r = (int64_t)blockIdx.x * kRows + (G < 256 ? threadIdx.x / G : 0);
   const int64_t rr = std::min(r, t - 1);
@@ -186,8 +186,12 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, i
 #pragma unroll
     for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[k][j], v[k][j], sq);
   }
-  sq = row_sum<G>(sq, lds);
-  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sq, (float)d), eps)));
+  // The statistic in 64 bits from the threads' sums on: one Newton step from
+  // the fp32 root, then as a pair rstd + low.
+  const double mean = __builtin_fma(row_sum<G>((double)sq, lds), inv_d, (double)eps);
+  double r64 = (double)__fdiv_rn(1.0f, __fsqrt_rn((float)mean));
+  r64 = r64 * __builtin_fma(-0.5 * mean * r64, r64, 1.5);
+  const float rstd = (float)r64, low = (float)(r64 - (double)rstd);
   if (r < t && i == 0) o.rstd[r] = rstd;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
@@ -197,7 +201,14 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, i
     unpack8(s[k], w);
     unpack8(g[k], gm);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(__fmul_rn(w[j], rstd), gm[j]);
+    for (int j = 0; j < 8; ++j) {
+      // s (rstd + low) gamma with the products' remainders: what bf16 and the
+      // codes round is off by one fp32 rounding, not by that of three steps
+      const float a = __fmul_rn(w[j], rstd), ar = __builtin_fmaf(w[j], low, __builtin_fmaf(w[j], rstd, -a));
+      const float b = __fmul_rn(a, gm[j]);
+      const float sum = __fadd_rn(b, __builtin_fmaf(ar, gm[j], __builtin_fmaf(a, gm[j], -b)));
+      w[j] = b == 0.0f ? b : sum;                        // a zero keeps its sign
+    }
     const uint4 y = pack8(w);
     if (o.y && live) *reinterpret_cast<uint4*>(o.y + r * d + c) = y;
     if (o.codes) {
@@ -450,7 +461,7 @@ fp4_status fp4_rmsnorm_producer(int64_t t, int64_t d, const void* x, fp4_dtype x
     constexpr int G = g(), V = v(), kRows = G < 256 ? 256 / G : 1;
     const auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)((t + kRows - 1) / kRows)), dim3(G < 256 ? 256 : G), 0,
-                         as_stream(stream), t, (int)d, x, ldx, residual, ldr, gamma, eps, drop, o);
+                         as_stream(stream), t, (int)d, x, ldx, residual, ldr, gamma, eps, 1.0 / (double)d, drop, o);
     };
     if (residual) x_type == FP4_F32 ? go(rmsnorm_kernel<G, V, true, true>) : go(rmsnorm_kernel<G, V, false, true>);
     else x_type == FP4_F32 ? go(rmsnorm_kernel<G, V, true, false>) : go(rmsnorm_kernel<G, V, false, false>);
