@@ -218,6 +218,8 @@ struct MvX {
 // Waits for this wave's LDS accesses and meets the workgroup's other waves;
 // global loads stay in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// The same without the wait; the compiler moves no access across it.
+__device__ __forceinline__ void wave_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 template <int XT, int WT, int MT, int NT, int NW, int U, bool GATE, bool STAGED, bool WHOLE>
 __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan plan) {
@@ -442,8 +444,9 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     multiply(w, turn);
     // The waves keep together, so that their loads stay on neighbouring
     // addresses: left to drift, 57344 x 8192 took 54 us instead of 50, as it
-    // did with more loads in flight.
-    if constexpr (STAGED) __builtin_amdgcn_s_barrier();
+    // did with more loads in flight.  Behind it all waves have read the sums of
+    // the meeting before, whose place the ones below take.
+    if constexpr (STAGED) wave_barrier();
     if (turn + 1 == per) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)

@@ -307,3 +307,55 @@ def test_random_shapes(gpu_lib, seed):
     assert near(val(dsum), ds, H + 2.0 ** -16) and near(host(dgamma), dg, 2.0 ** -16)
     keep, sc = N.keep_mask(t, d, p, seed, seed), float(N.keep_scale(p))
     assert near(val(dx), np.where(keep, ds * sc, 0.0), H + 2.0 ** -16)
+
+
+def test_everything_dropped(gpu_lib):
+    """p = 1: s is the residual (or zero), nothing flows back to x."""
+    mx, t, d = gpu_lib, 6, 96
+    x, xd = inputs((t, d), 31, True)
+    rb = synthetic.tensor((t, d), seed=32)
+    g = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    s, rstd, *_ = mx.fp4_rmsnorm_producer(xd, g, 1e-5, dev16(rb), 1.0, 3, 4)
+    assert torch.equal(s, dev16(rb))
+    dsum, dx, _ = mx.fp4_rmsnorm_backward(xd, s, rstd, g, p=1.0, seed=3, offset=4)
+    assert (val(dx) == 0).all() and (val(dsum) != 0).any()
+    s, rstd, y, codes, scales = mx.fp4_rmsnorm_producer(xd, g, 1e-5, None, 1.0, 3, 4, emit_y=True)
+    assert (val(s) == 0).all() and (val(y) == 0).all() and (host(codes) == 0).all() and (host(scales) == 0).all()
+
+
+def test_a_probability_below_the_resolution_drops_nothing(gpu_lib):
+    mx = gpu_lib
+    x, xd = inputs((4, 64), 33, False)
+    g = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for p in (0.0, 1e-6, 7.62939453125e-06 * 0.999):
+        assert torch.equal(mx.fp4_dropout(xd, p, 1, 2), xd)
+        s, rstd, *_ = mx.fp4_rmsnorm_producer(xd, g, p=p, seed=1, offset=2)
+        assert torch.equal(s, xd)
+        dsum, dx, _ = mx.fp4_rmsnorm_backward(xd, s, rstd, g, p=p, seed=1, offset=2)
+        assert dx is dsum
+    # 2^-17 rounds up to one part in 65536
+    dsum, dx, _ = mx.fp4_rmsnorm_backward(xd, s, rstd, g, p=2.0 ** -17, seed=1, offset=2)
+    assert dx is not dsum
+
+
+def test_bit_patterns_flags_and_given_gradients(gpu_lib):
+    """16-bit integer tensors hold the same values; every output can be left
+    out or given; the outputs that are made do not depend on which."""
+    mx, t, d = gpu_lib, 7, 160
+    x, xd = inputs((t, d), 34, False)
+    gb = synthetic.bf16_bits(np.linspace(0.5, 1.5, d, dtype=np.float32))
+    i16 = lambda v: v.view(torch.int16)  # noqa: E731
+    full = mx.fp4_rmsnorm_producer(xd, dev16(gb), 1e-5, xd, emit_y=True)
+    same = mx.fp4_rmsnorm_producer(i16(xd), i16(dev16(gb)), 1e-5, i16(xd), emit_y=True)
+    assert all(torch.equal(a, b) for a, b in zip(full, same))
+    for es in (False, True):
+        for ey in (False, True):
+            for ec in (False, True):
+                got = mx.fp4_rmsnorm_producer(xd, dev16(gb), 1e-5, xd, emit_sum=es, emit_y=ey, emit_codes=ec)
+                assert [v is not None for v in got] == [es, True, ey, ec, ec]
+                assert all(v is None or torch.equal(v, w) for v, w in zip(got, full))
+    want = mx.fp4_rmsnorm_backward(xd, full[0], full[1], dev16(gb), xd, 0.3, 5, 6)
+    bufs = (torch.empty((t, d), dtype=torch.int16, device="cuda"), torch.empty_like(xd), torch.empty(d, device="cuda"))
+    got = mx.fp4_rmsnorm_backward(i16(xd), full[0], full[1], dev16(gb), xd, 0.3, 5, 6, out=bufs)
+    assert all(a is b for a, b in zip(got, bufs))
+    assert torch.equal(got[0].view(torch.bfloat16), want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])

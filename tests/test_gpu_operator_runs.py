@@ -170,3 +170,25 @@ def test_calls_on_two_streams(gpu_lib):
     torch.cuda.synchronize()
     for out in got:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_documented_usage(gpu_lib):
+    """The README's boundary and decoded token, in small."""
+    mx, T, D = gpu_lib, 96, 256
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = (0.02 * torch.randn(D, D, device="cuda", generator=g)).bfloat16()
+    wr, wrs, wc, wcs = mx.fp4_quantize_w2d32(w, 0.87)
+    y = torch.randn(T, D, device="cuda", generator=g)
+    dx = torch.randn(T, D, device="cuda", generator=g)
+    gamma, res = torch.ones(D, device="cuda").bfloat16(), torch.zeros(T, D, device="cuda").bfloat16()
+    s, rstd, yn, yc, ys = mx.fp4_rmsnorm_producer(y, gamma, 1e-5, residual=res, p=0.1, seed=7, offset=0, fmt=mx.FP4_E2M1,
+                                                  emit_y=True)
+    dres, dbranch, dgamma = mx.fp4_rmsnorm_backward(dx, s, rstd, gamma, p=0.1, seed=7, offset=0)
+    assert dres.shape == dbranch.shape == (T, D) and dgamma.shape == (D,)
+    out = mx.fp4_gemm(yc, ys, wr, wrs)
+    ref, e = G.gemm_ref(host(yc), host(ys), host(wr), host(wrs))
+    assert G.within_bound(host(out), ref, e).all()
+    s1, r1, _, c8, s8 = mx.fp4_rmsnorm_producer(y[:1], gamma, residual=res[:1])
+    one = mx.fp4_matvec(c8, wr, wrs, x_scales=s8)
+    x64, w64 = N.decode_e4m3(host(c8), host(s8)), F.decode(host(wr), host(wrs))
+    assert G.within_bound(host(one), x64 @ w64.T, np.abs(x64) @ np.abs(w64).T).all()
