@@ -457,6 +457,8 @@ typedef enum { FP4_E2M1 = 0, FP4_E4M3 = 1 } fp4_format;
  *   x         [rows][ldx] bf16 or fp32 (x_type; fp32: a GEMM's C)
  *   residual  [rows][ldr] bf16, or NULL
  *   out       [rows][ldo] bf16; columns cols .. ldo - 1 are left as they were
+ * out may be x (bf16, ldo = ldx) or the residual (ldo = ldr), and overlaps
+ * neither otherwise.
  * Any cols and any ld >= cols; rows that all start on 16-byte boundaries (ldx,
  * ldr, ldo multiples of 8) go by wide loads, others element by element.
  * Errors: FP4_EINVAL bad x_type, p outside [0, 1] or null pointer; FP4_ESHAPE
@@ -491,6 +493,8 @@ fp4_status fp4_dropout(int64_t rows, int64_t cols, const void* x, fp4_dtype x_ty
  *   y         [t][d] bf16 or NULL (e.g. for fp4_quantize_cols)
  *   codes     [t][d/2] (E2M1) or [t][d] (E4M3), scales [t][d/32]; both or
  *             neither NULL
+ * sum may be the residual (ldr = d); outputs overlap no input otherwise.  t = 0
+ * or d = 0 writes nothing.
  * |s| must stay below 2^60 (the squares are summed in fp32).
  * Errors: FP4_EINVAL bad x_type or format, p outside [0, 1], eps not a
  * positive finite number, exactly one of codes, scales NULL, or another null
@@ -522,7 +526,8 @@ fp4_status fp4_rmsnorm_producer(int64_t t, int64_t d, const void* x, fp4_dtype x
  *   ds [t][ldds] bf16 or NULL; dsum, dx [t][d] bf16
  *   workspace  fp4_rmsnorm_backward_workspace(t, d) bytes, 16-byte aligned,
  *              in use until the call's work on the stream is done
- * t = 0 sets dgamma to 0 (leaves it unchanged when accumulating).
+ * t = 0 sets dgamma to 0 (leaves it unchanged when accumulating).  Outputs
+ * overlap no input.
  * Errors: FP4_EINVAL bad dy_type, p outside [0, 1], accumulate not 0 or 1, or
  * null pointer; FP4_ESHAPE as the producer, or a workspace below that size;
  * FP4_EALIGN a tensor or the workspace not 16-byte aligned (rstd and dgamma: 4), lddy

@@ -541,8 +541,8 @@ def fp4_rmsnorm_producer(x, gamma, eps=1e-5, residual=None, p=0.0, seed=0, offse
         codes = _out(o_codes, (t, d // 2 if fmt == FP4_E2M1 else d), torch.uint8, dev, "codes")
         scales = _out(o_scales, (t, d // 32), torch.uint8, dev, "scales")
     _check(load().fp4_rmsnorm_producer(t, d, x.data_ptr(), 1 if x.dtype is torch.float32 else 0, ldx, _p(residual), ldr,
-                                       gamma.data_ptr(), float(eps), float(p), int(seed), int(offset), _p(s), rstd.data_ptr(), _p(y), int(fmt),
-                                       _p(codes), _p(scales), _raw_stream(cur)))
+                                       gamma.data_ptr(), float(eps), float(p), int(seed), int(offset), _p(s),
+                                       rstd.data_ptr(), _p(y), int(fmt), _p(codes), _p(scales), _raw_stream(cur)))
     return s, rstd, y, codes, scales
 
 
@@ -570,8 +570,8 @@ def fp4_rmsnorm_backward(dy, s, rstd, gamma, ds=None, p=0.0, seed=0, offset=0, a
     size = lib.fp4_rmsnorm_backward_workspace(t, d)
     ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
     _check(lib.fp4_rmsnorm_backward(t, d, dy.data_ptr(), 1 if dy.dtype is torch.float32 else 0, lddy, s.data_ptr(), lds,
-                                    rstd.data_ptr(), gamma.data_ptr(), _p(ds), ldds, float(p), int(seed), int(offset), dsum.data_ptr(),
-                                    _p(dx), dgamma.data_ptr(), 1 if accumulate else 0, ws.data_ptr(), size,
+                                    rstd.data_ptr(), gamma.data_ptr(), _p(ds), ldds, float(p), int(seed), int(offset),
+                                    dsum.data_ptr(), _p(dx), dgamma.data_ptr(), 1 if accumulate else 0, ws.data_ptr(), size,
                                     _raw_stream(cur)))
     return dsum, dsum if dx is None else dx, dgamma
 

@@ -164,9 +164,11 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
 // rows, whose operands take the registers of two waves.  A tile is 16 rows of
 // W (gated: 8 of W1 and the same 8 of W3).  KW waves share NT tiles (one, or
 // two) and split K; the workgroup works on NW / KW such sets at a time and
-// walks groups of them blockIdx.x, blockIdx.x + gridDim.x, ...  A step is 128 values of K; product q = 0 .. 3 of
-// its four 16x16x32 bf16 products takes values 32 q + 8 g .. + 7 in lane (r =
-// lane & 15, g = lane >> 4), row r of W and of x.  An item is U consecutive
+// walks groups of them blockIdx.x, blockIdx.x + gridDim.x, ...
+//
+// A step is 128 values of K; product q = 0 .. 3 of its four 16x16x32 bf16
+// products takes values 32 q + 8 g .. + 7 in lane (r = lane & 15, g = lane >>
+// 4), row r of W and of x.  An item is U consecutive
 // steps; wave kw takes items kw, kw + KW, ... of a tile, and the loads of its
 // next item, across the end of a tile too, are in flight during the products
 // of the current one.  No branch surrounds a load: the compiler could not

@@ -143,14 +143,17 @@ struct NormOut {
 // the row stays in registers between the statistics and the output, x and the
 // residual are read once.  Four neighbouring lanes hold one 32-value block.
 //
+// The sum may take the residual's place: a thread that stores it has read those
+// elements, and uses no others (what it reads past the end is dropped).
+//
 // No branch surrounds a load (a row or column past the end reads the last
 // one), and all of a thread's loads go out before its first use: 8192 x 4096,
-// fp32 x with dropout and residual to s and E4M3, 302 MB, takes 51 us (5.9
+// fp32 x with dropout and residual to s and E4M3, 302 MB, takes 52 us (5.8
 // TB/s), and took 89 with the loads of each group of columns behind the stores
 // of the one before.  Bound by HBM; one token by its launch (2.8 us).
 template <int G, int V, bool F32, bool RES>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, int d, const void* __restrict__ x,
-                                                                    int64_t ldx, const uint16_t* __restrict__ residual,
+                                                                    int64_t ldx, const uint16_t* residual,
                                                                     int64_t ldr, const uint16_t* __restrict__ gamma,
                                                                     float eps, double inv_d, Dropout drop, NormOut o) {
   constexpr int kRows = G < 256 ? 256 / G : 1;
@@ -289,7 +292,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_bwd_kernel(
       for (int j = 0; j < 8; ++j) {
         if (!live) cur.dy[k][j] = 0.0f;
         xh[j] = __fmul_rn(xh[j], rs);
-        // a dead lane adds 0 times a finite s of the last row or group
+        // selected, not multiplied by 0: a dead lane holds the last row's s, which may be an infinity
         dg[k][j] = live ? __builtin_fmaf(cur.dy[k][j], xh[j], dg[k][j]) : dg[k][j];
         dot = live ? __builtin_fmaf(__fmul_rn(cur.dy[k][j], g[j]), xh[j], dot) : dot;
       }

@@ -359,3 +359,30 @@ def test_bit_patterns_flags_and_given_gradients(gpu_lib):
     got = mx.fp4_rmsnorm_backward(i16(xd), full[0], full[1], dev16(gb), xd, 0.3, 5, 6, out=bufs)
     assert all(a is b for a, b in zip(got, bufs))
     assert torch.equal(got[0].view(torch.bfloat16), want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("rows,cols,pitch", [(5, 64, 64), (3, 33, 40), (2, 4099, 4099), (1030, 40, 48)])
+def test_dropout_in_place(gpu_lib, rows, cols, pitch):
+    """out may be x or the residual; the columns behind stay."""
+    mx = gpu_lib
+    xb, rb = synthetic.tensor((rows, pitch), seed=41), synthetic.tensor((rows, pitch), seed=42)
+    x, r = dev16(xb), dev16(rb)
+    want = mx.fp4_dropout(x[:, :cols], 0.25, 7, 8, residual=r[:, :cols])
+    for place in (0, 1):
+        bufs = [dev16(xb), dev16(rb)]
+        mx.fp4_dropout(bufs[0][:, :cols], 0.25, 7, 8, residual=bufs[1][:, :cols], out=bufs[place][:, :cols])
+        assert torch.equal(bufs[place][:, :cols], want)
+        assert torch.equal(bufs[place][:, cols:], (x, r)[place][:, cols:])
+
+
+@pytest.mark.parametrize("t,d", [(1, 32), (17, 96), (5, 544), (300, 4096), (3, 8224), (2, 32768)])
+def test_the_sum_takes_the_residuals_place(gpu_lib, t, d):
+    mx = gpu_lib
+    x, xd = inputs((t, d), 43, True)
+    rb = synthetic.tensor((t, d), seed=44)
+    g = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    for p in (0.0, 0.2):
+        want = mx.fp4_rmsnorm_producer(xd, g, 1e-5, dev16(rb), p, 3, 4, emit_y=True)
+        res = dev16(rb)
+        got = mx.fp4_rmsnorm_producer(xd, g, 1e-5, res, p, 3, 4, emit_y=True, out=(res, None, None, None, None))
+        assert got[0] is res and all(torch.equal(a, b) for a, b in zip(got, want))

@@ -173,7 +173,7 @@ def test_calls_on_two_streams(gpu_lib):
 
 
 def test_documented_usage(gpu_lib):
-    """The README's boundary and decoded token, in small."""
+    """The documented usage, in small: a boundary with its backward pass and a decoded token."""
     mx, T, D = gpu_lib, 96, 256
     g = torch.Generator(device="cuda").manual_seed(1)
     w = (0.02 * torch.randn(D, D, device="cuda", generator=g)).bfloat16()
