@@ -177,7 +177,8 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
 //
 // x goes through LDS as bf16: all of it once per workgroup where it fits
 // (STAGED), else each wave brings its own steps, with the item, into a room of
-// its own (no barrier: one wave's LDS accesses keep their order).
+// its own (no barrier between waves; wave_lds_order between its writes and
+// its reads).
 // WHOLE: K is a multiple of U steps and the scales are aligned to words, so
 // that the scale bytes of an item come with one load, spread like the codes,
 // and reach the other lanes of a row by permutes.
@@ -222,6 +223,14 @@ struct MvX {
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 // The same without the wait; the compiler moves no access across it.
 __device__ __forceinline__ void wave_barrier() { asm volatile("s_barrier" ::: "memory"); }
+// Between LDS accesses of one wave whose lanes read what others wrote: the
+// hardware keeps a wave's LDS accesses in order, and this the compiler, which
+// sees a thread's own addresses only and may take them for distinct.  It makes
+// no instruction.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
 
 template <int XT, int WT, int MT, int NT, int NW, int U, bool GATE, bool STAGED, bool WHOLE>
 __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan plan) {
@@ -440,8 +449,10 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
       int64_t gr = group;
       int tn = turn;
       step(gr, tn);
+      wave_lds_order();                                  // the room: the last step's reads are before
       put_x(x);
       load_x(x, tn);
+      wave_lds_order();                                  // its values: other lanes read them below
     }
     multiply(w, turn);
     // The waves keep together, so that their loads stay on neighbouring
@@ -450,6 +461,7 @@ __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan pl
     // the meeting before, whose place the ones below take.
     if constexpr (STAGED) wave_barrier();
     if (turn + 1 == per) {
+      if constexpr (!STAGED) wave_lds_order();           // the sums take the room of the step just read
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
