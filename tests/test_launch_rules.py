@@ -57,3 +57,23 @@ def test_every_product_variant_has_a_test_shape(program):
     built = {re.sub(r"\s", "", v) for v in re.findall(r"__device_stub__(matvec_kernel<[^>]*>)", symbols)}
     compiled = {name.split("::")[-1] for name in reached}
     assert len(built) > 70 and compiled == built, sorted(built - compiled)
+
+
+# t at and around 2^32 threads for each number of rows a workgroup holds, and the largest that the call takes
+@pytest.mark.parametrize("d", [32, 128, 160, 2048, 2080, 8192, 16384, 32768])
+@pytest.mark.parametrize("t", [1, 8192, (1 << 22) - 1, 1 << 22, (1 << 23) + 5, (1 << 24) - 1, 1 << 24, (1 << 26) + 3, 1 << 28,
+                               (1 << 28) + 17, (1 << 31) - 1])
+def test_norm_launches_stay_below_the_thread_limit(program, t, d):
+    """A dimension of a launch holds less than 2^32 threads; every row has its workgroup."""
+    for op in ("norm", "bwd"):
+        for st, made in launches(program, [f"{op} {t} {d} {f32} {extra}" for f32 in (0, 1) for extra in (0, 1)]):
+            assert st == 0
+            for name, (x, y, z), threads in made:
+                assert x * threads < 1 << 32 and y < 1 << 16 and z == 1, name
+            name, (x, y, z), _ = made[0]
+            lanes = int(re.search(r"<(\d+),", name)[1])
+            rows = max(256 // lanes, 1)
+            if op == "norm":
+                assert x * y * rows >= t and x * (y - 1) * rows < t
+            else:
+                assert x <= 512 and y == 1
