@@ -125,10 +125,12 @@ __device__ __forceinline__ uint2 e4m3_8(const uint4 w, float scale) {
   return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
 }
 
-// A launch's dimension holds less than 2^32 threads, fewer than the calls take
-// rows of (17 GB of bf16 at 32 columns): workgroups past 2^20 go to a second
-// dimension.
-constexpr int kNormGridX = 20;                           // log2
+// A launch's dimension holds less than 2^32 threads (a larger one wraps, with
+// no error), fewer than the calls take rows of (17 GB of bf16 at 32 columns):
+// workgroups past 2^20 go to a second dimension, in equal shares.  A return of
+// the few past the last row, in place of their clamped loads, cost every launch
+// of 1536 to 2048 columns 2-3%.
+constexpr int64_t kNormGridX = 1 << 20;
 
 struct NormOut {
   uint16_t* sum;                                         // any of these may be null
@@ -164,9 +166,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, i
   constexpr int kRows = G < 256 ? 256 / G : 1;
   __shared__ double lds[16];
   const int i = threadIdx.x & (G - 1);
-  const int64_t top = (((int64_t)blockIdx.y << kNormGridX) + blockIdx.x) * kRows;
-  const int64_t r = top + (G < 256 ? threadIdx.x / G : 0);
-  if (top >= t) return;                                  // the second dimension's last turn may end early
+  const int64_t r = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRows + (G < 256 ? threadIdx.x / G : 0);
   const int64_t rr = std::min(r, t - 1);
   uint4 s[V], g[V];
   float v[V][8], base[V][8];
@@ -469,8 +469,8 @@ fp4_status fp4_rmsnorm_producer(int64_t t, int64_t d, const void* x, fp4_dtype x
   const NormOut o{sum, y, rstd, codes, scales, format == FP4_E4M3};
   norm_variant(d, [&](auto g, auto v) {
     constexpr int G = g(), V = v(), kRows = G < 256 ? 256 / G : 1;
-    const int64_t groups = (t + kRows - 1) / kRows, most = (int64_t)1 << kNormGridX;
-    const dim3 grid((unsigned)std::min(groups, most), (unsigned)((groups + most - 1) >> kNormGridX));
+    const int64_t groups = (t + kRows - 1) / kRows, shares = (groups + kNormGridX - 1) / kNormGridX;
+    const dim3 grid((unsigned)((groups + shares - 1) / shares), (unsigned)shares);
     const auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, dim3(G < 256 ? 256 : G), 0, as_stream(stream), t, (int)d, x, ldx,
                          residual, ldr, gamma, eps, 1.0 / (double)d, drop, o);
