@@ -125,6 +125,8 @@ __device__ __forceinline__ uint2 e4m3_8(const uint4 w, float scale) {
   return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
 }
 
+constexpr int kNoRemainder = 0x267;                      // the classes of both zeros, both infinities and NaN
+
 // A launch's dimension holds less than 2^32 threads (a larger one wraps, with
 // no error), fewer than the calls take rows of (17 GB of bf16 at 32 columns):
 // workgroups past 2^20 go to a second dimension, in equal shares.  A return of
@@ -213,11 +215,13 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, i
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       // s (rstd + low) gamma with the products' remainders: what bf16 and the
-      // codes round is off by one fp32 rounding, not by that of three steps
+      // codes round is off by one fp32 rounding, not by that of three steps.
+      // A zero keeps its sign, and a product past fp32 its infinity, of which
+      // the remainder would make a NaN.
       const float a = __fmul_rn(w[j], rstd), ar = __builtin_fmaf(w[j], low, __builtin_fmaf(w[j], rstd, -a));
       const float b = __fmul_rn(a, gm[j]);
       const float sum = __fadd_rn(b, __builtin_fmaf(ar, gm[j], __builtin_fmaf(a, gm[j], -b)));
-      w[j] = b == 0.0f ? b : sum;                        // a zero keeps its sign
+      w[j] = __builtin_amdgcn_classf(b, kNoRemainder) ? b : sum;
     }
     const uint4 y = pack8(w);
     if (o.y && live) *reinterpret_cast<uint4*>(o.y + r * d + c) = y;

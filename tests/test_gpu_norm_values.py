@@ -1,0 +1,71 @@
+"""The norm producer's values at the ends of their ranges."""
+
+import numpy as np
+import pytest
+import torch
+
+import synthetic
+from oracle import formats as F
+from oracle import norm as N
+
+pytestmark = pytest.mark.gpu
+
+
+def dev16(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.cpu().numpy()
+
+
+def val(t):
+    return F.bf16_bits_to_f64(host(t.contiguous().view(torch.int16)).view(np.uint16))
+
+
+SHAPES = [(3, 96), (2, 544), (2, 2080), (1, 8224), (1, 32768)]
+
+
+def check_past_the_range(mx, s_bits, g):
+    """y against float64 rounded once: from 2^128 - 2^119 on (half a bf16 step
+    past the largest bf16 value) an infinity with the product's sign."""
+    s, g_bits = F.bf16_bits_to_f64(s_bits), synthetic.bf16_bits(g)
+    y = val(mx.fp4_rmsnorm_producer(dev16(s_bits), dev16(g_bits), emit_y=True)[2])
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = N.rmsnorm(s, F.bf16_bits_to_f64(g_bits), 1e-5)[1]
+        top = 2.0 ** 128 - 2.0 ** 119
+        # one fp32 rounding on either side of the border may go either way
+        sure = ~(np.abs(np.abs(want) - top) <= 2.0 ** 104)
+        want = np.where(np.abs(want) >= top, np.copysign(np.inf, want), want)
+    assert sure.mean() > 0.99 and np.array_equal(np.isnan(y), np.isnan(want))
+    inf = np.isinf(want) & sure
+    assert np.array_equal(y[inf], want[inf])
+    fin = np.isfinite(want) & sure
+    # a bf16 rounding, and one of fp32 before it
+    assert (np.abs(y[fin] - want[fin]) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(want[fin]) + 2.0 ** -133).all()
+    return want, inf
+
+
+@pytest.mark.parametrize("t,d", SHAPES)
+def test_infinite_and_nan_gamma_stay_in_their_columns(gpu_lib, t, d):
+    s_bits = synthetic.tensor((t, d), seed=51)
+    s_bits[:, 5] = 0
+    g = np.ones(d, np.float32)
+    g[0:4] = [2.0 ** 127, -2.0 ** 127, 2.0 ** 126, 1.5 * 2.0 ** 127]
+    g[4:9] = [np.inf, np.inf, -np.inf, np.nan, 2.0 ** -126]
+    g[16:32] = 2.0 ** np.arange(112, 128)
+    s_bits[np.abs(F.bf16_bits_to_f64(s_bits)) < 2.0 ** -6] = 0x3F80   # away from zero, but for column 5
+    s_bits[:, 5] = 0
+    want, inf = check_past_the_range(gpu_lib, s_bits, g)
+    # 0 times an infinity is NaN
+    assert inf[:, [4, 6]].all() and np.isnan(want[:, [5, 7]]).all()
+
+
+@pytest.mark.parametrize("t,d", SHAPES)
+def test_products_past_the_range_are_infinities(gpu_lib, t, d):
+    s_bits = synthetic.tensor((t, d), std=1.0, seed=52, outlier_rate=0.002, outlier_scale=20.0)
+    rng = np.random.default_rng(53)
+    g = (rng.choice([-1.0, 1.0], d) * rng.uniform(1, 1.99, d) * 2.0 ** rng.integers(124, 128, d)).astype(np.float32)
+    want, inf = check_past_the_range(gpu_lib, s_bits, g)
+    assert 0.01 < inf.mean() < 0.5 and (want[inf] > 0).any() and (want[inf] < 0).any()
