@@ -447,6 +447,14 @@ _BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
 _ROWS32 = _BITS16 + (torch.float32,)
 
 
+def _current(t, name):
+    """The current device; a host tensor is refused before torch is asked for
+    one, which raises its own error where no GPU is visible."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _dev(t, name)
+    return torch.cuda.current_device()
+
+
 def _here(t, name, cur):
     if not isinstance(t, torch.Tensor) or t.get_device() != cur:
         _dev(t, name)
@@ -514,7 +522,7 @@ def fp4_dropout(x, p, seed=0, offset=0, residual=None, out=None):
     never stored; the same call on the output's gradient (without residual) is
     the backward pass.  Without `out` the result's rows lie at a pitch of a
     multiple of eight elements (what the quantizers read)."""
-    cur = torch.cuda.current_device()
+    cur = _current(x, "x")
     ldx = _rows2d(x, "x", cur, None, _ROWS32)
     shape = x.shape
     rows, cols = shape
@@ -536,7 +544,7 @@ def fp4_rmsnorm_producer(x, gamma, eps=1e-5, residual=None, p=0.0, seed=0, offse
     """Dropout of x, addition to the residual, RMSNorm and its codes: returns
     (s, rstd, y, codes, scales), None where not emitted.  `out` may hold those
     five buffers (None: allocated)."""
-    cur = torch.cuda.current_device()
+    cur = _current(x, "x")
     ldx = _rows2d(x, "x", cur, None, _ROWS32)
     shape = x.shape
     t, d = shape
@@ -563,7 +571,7 @@ def fp4_rmsnorm_backward(dy, s, rstd, gamma, ds=None, p=0.0, seed=0, offset=0, a
     """Gradients of fp4_rmsnorm_producer's boundary: returns (dsum, dx, dgamma);
     dx is dsum where nothing is dropped.  `ds` is the gradient that reaches s
     along the residual stream; `out` may hold the three buffers."""
-    cur = torch.cuda.current_device()
+    cur = _current(dy, "dy")
     lddy = _rows2d(dy, "dy", cur, None, _ROWS32)
     shape = dy.shape
     t, d = shape
@@ -615,7 +623,7 @@ def _few_rows(x, x_scales, w_codes, cur):
 def fp4_matvec(x, w_codes, w_scales, x_scales=None, c=None, accumulate=False):
     """C (+)= x dec(W)^T for up to 64 rows of x, bf16 or E4M3 codes with
     x_scales, and MXFP4 weights in the row layout."""
-    cur = torch.cuda.current_device()
+    cur = _current(x, "x")
     m, n, k, ldx = _few_rows(x, x_scales, w_codes, cur)
     _bytes2d(w_scales, "w_scales", cur, (n, k // 32))
     c = _gemm_out(c, m, n, accumulate, x.device)
@@ -628,7 +636,7 @@ def fp4_nv_matvec(x, w_codes, w_scales, w_factors, c=None, accumulate=False):
     """C (+)= x dec(W)^T for up to 64 rows of bf16 x and CTA-local NVFP4
     weights in the row layout; a factor vector of one element is shared by all
     rows of W, otherwise it holds one per 256-row panel."""
-    cur = torch.cuda.current_device()
+    cur = _current(x, "x")
     m, n, k, ldx = _few_rows(x, None, w_codes, cur)
     _bytes2d(w_scales, "w_scales", cur, (n, k // 16))
     panels = (n + 255) // 256
@@ -645,7 +653,7 @@ def fp4_nv_matvec(x, w_codes, w_scales, w_factors, c=None, accumulate=False):
 def fp4_swiglu_matvec(x, w13_codes, w13_scales, x_scales=None, h=None):
     """h = bf16(SiLU(a) b) with a = bf16(x W1^T), b = bf16(x W3^T) for up to 64
     rows of x (as fp4_matvec) and the stacked MXFP4 rows of W1 and W3."""
-    cur = torch.cuda.current_device()
+    cur = _current(x, "x")
     m, f2, d, ldx = _few_rows(x, x_scales, w13_codes, cur)
     if f2 % 2:
         raise Fp4Error("w13_codes must stack W1 and W3: an even number of rows")
