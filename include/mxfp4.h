@@ -495,7 +495,9 @@ fp4_status fp4_dropout(int64_t rows, int64_t cols, const void* x, fp4_dtype x_ty
  *             neither NULL
  * sum may be the residual (ldr = d); outputs overlap no input otherwise.  t = 0
  * or d = 0 writes nothing.
- * |s| must stay below 2^60 (the squares are summed in fp32).
+ * The squares are summed in fp32: |s| must stay below 2^60, and where eps is
+ * below 2^-126 too, rows of |s| below 2^-63 lose bits of rstd.  A row with an
+ * infinity or NaN in s becomes NaN; other rows are not touched by it.
  * Errors: FP4_EINVAL bad x_type or format, p outside [0, 1], eps not a
  * positive finite number, exactly one of codes, scales NULL, or another null
  * pointer; FP4_ESHAPE t negative or above 2^31 - 1, d not a non-negative
@@ -547,13 +549,16 @@ int64_t fp4_rmsnorm_backward_workspace(int64_t t, int64_t d);
  * fp4_gemm: C[m][n] (+)= sum_k x[m][k] * dec(W)[n][k] in fp32, m <= 64.
  * W is the row layout of fp4_quantize_w2d32 (or fp4_quantize_rows).  x stays
  * in bf16, or is E4M3 codes with E8M0 scales as fp4_rmsnorm_producer emits
- * (x_scales not NULL).  Every decoded value is exact in bf16, the products run
- * on the bf16 matrix cores with fp32 sums.  Deterministic.
+ * (x_scales not NULL).  The products run on the bf16 matrix cores with fp32
+ * sums.  Deterministic.  Decoded weights and the producer's codes are exact in
+ * bf16; other E4M3 codes under scale bytes 0 to 2 may not be, and take the
+ * nearest multiple of 2^-133 (ties to even).
  *   x        bf16 [m][ldx], or E4M3 [m][k] (ldx = k) with x_scales [m][k/32]
  *   w_codes  [n][k/2], w_scales [n][k/32]
  *   c        [m][ldc] fp32, any ldc >= n
- * Any n; an empty reduction (k = 0) writes 0.  Decoded weights must be below
- * 2^128 in magnitude (scale byte 253 with codes 4 and 6 is not).
+ * Any n; an empty reduction (k = 0) writes 0.  Decoded values must be below
+ * 2^128 in magnitude: weights under scale byte 253 with codes 4 and 6 are not,
+ * nor are E4M3 codes of 256 and more under byte 247 (they become infinities).
  * Errors: FP4_EINVAL accumulate not 0 or 1, or null pointer; FP4_ESHAPE m
  * outside [0, 64], n negative or above 2^34, k not a non-negative multiple of
  * 32 or >= 2^24, ldx < k, ldx >= 2^24 (32-bit offsets within x), ldx != k with

@@ -69,3 +69,30 @@ def test_products_past_the_range_are_infinities(gpu_lib, t, d):
     g = (rng.choice([-1.0, 1.0], d) * rng.uniform(1, 1.99, d) * 2.0 ** rng.integers(124, 128, d)).astype(np.float32)
     want, inf = check_past_the_range(gpu_lib, s_bits, g)
     assert 0.01 < inf.mean() < 0.5 and (want[inf] > 0).any() and (want[inf] < 0).any()
+
+
+@pytest.mark.parametrize("t,d", [(40, 32), (9, 160), (7, 2048), (3, 4096), (3, 32768)])
+def test_non_finite_rows_stay_apart(gpu_lib, t, d):
+    """A row with an infinity or NaN becomes NaN, rows beside it (of the same
+    wave too) keep their bytes, forwards and backwards."""
+    mx = gpu_lib
+    s = dev16(synthetic.tensor((t, d), std=1.0, seed=54))
+    dy = dev16(synthetic.tensor((t, d), std=1.0, seed=55))
+    g = torch.linspace(0.5, 1.5, d, device="cuda").bfloat16()
+    clean = mx.fp4_rmsnorm_producer(s, g, emit_y=True)
+    grad = mx.fp4_rmsnorm_backward(dy, s, clean[1], g, ds=dy)
+    bad, bad_dy = s.clone(), dy.clone()
+    rows = [1] if t == 3 else [1, 4, t - 1]
+    for r, v in zip(rows, (float("inf"), float("nan"), -float("inf"))):
+        bad[r, (7 * r) % d] = v
+        bad_dy[r, (5 * r + 1) % d] = v
+    rest = [r for r in range(t) if r not in rows]
+    got = mx.fp4_rmsnorm_producer(bad, g, emit_y=True)
+    for k, (a, b) in enumerate(zip(got, clean)):
+        assert torch.equal(a[rest], b[rest]), k
+    assert got[1][rows].isnan().all() and got[2][rows].isnan().all()
+    for first, second, rstd in ((dy, bad, got[1]), (bad_dy, s, clean[1])):
+        dsum, _, dgamma = mx.fp4_rmsnorm_backward(first, second, rstd, g, ds=dy)
+        assert torch.equal(dsum[rest], grad[0][rest]) and not dsum[rows].isfinite().all(1).any()
+        # every column of a row whose rstd is NaN, else only the columns of the infinities and NaN
+        assert dgamma.isnan().all() if second is bad else (~dgamma.isfinite()).sum() == len(rows)
