@@ -5,11 +5,9 @@ import numpy as np
 import pytest
 import torch
 
-import synthetic
 from oracle import formats as F
 from oracle import norm as N
 from oracle import philox as P
-from oracle import quant as Q
 
 pytestmark = pytest.mark.gpu
 U, H = 2.0 ** -24, 2.0 ** -8                             # half an fp32 step, half a bf16 step
@@ -66,3 +64,51 @@ def test_more_rows_than_a_launch_dimension_holds(gpu_lib, room, t, d):
         want = N.f32_to_bf16_rne(np.where(row_mask(r, d, p, seed, offset), val(x[r:r + 1])[0].astype(np.float32)
                                           * N.keep_scale(p), np.float32(0)))
         assert np.array_equal(bits(s[r:r + 1])[0], want), r
+
+
+# several turns of a workgroup over its rows, with full and ragged last ones, for
+# every number of threads a row and of columns a thread, below and from the
+# number of rows on that takes two workgroups a CU
+WALKS = [(33000, 32), (40000, 128), (9001, 160), (9001, 544), (5000, 1056), (2500, 1568), (8200, 2048), (2500, 2080),
+         (2047, 4096), (2048, 4096), (2100, 4096), (700, 6144), (600, 8192), (520, 8224), (1030, 16384), (515, 32768)]
+
+
+@pytest.mark.parametrize("t,d", WALKS)
+@pytest.mark.parametrize("f32,with_ds,p", [(True, True, 0.1), (False, False, 0.0), (True, False, 0.5), (False, True, 0.0)])
+def test_backward_walks_its_rows(gpu_lib, t, d, f32, with_ds, p):
+    """With u = 2^-24 and h = 2^-8 (half a bf16 step): dsum as the mean's
+    products and its at most 54 sums on mean |g xh| and five more operations,
+    then h; dgamma two product roundings and a thread's turns (at most t / 512
+    and 8), lanes, waves, at most 16 partial sums a slice and 32 slices on sum
+    |dy xh|."""
+    mx, g = gpu_lib, torch.Generator("cuda").manual_seed(t + d)
+    rand = lambda *n, k=1.0: k * torch.randn(n, device="cuda", generator=g)  # noqa: E731
+    s, gamma = rand(t, d, k=2.0).bfloat16(), (1 + 0.2 * rand(d)).bfloat16()
+    s[t // 2] = 0                                        # rstd = 1 / sqrt(eps)
+    dy = rand(t, d, k=1e-3)
+    dy = dy if f32 else dy.bfloat16()
+    ds = rand(t, d, k=1e-3).bfloat16() if with_ds else None
+    rstd = (s.double().square().mean(1) + 1e-5).rsqrt().float()
+    seed, offset = 78, 2 ** 41 + 7
+    dsum, dx, dgamma = mx.fp4_rmsnorm_backward(dy, s, rstd, gamma, ds, p, seed, offset)
+    r = rstd.double()[:, None]
+    xh, gr = s.double() * r, dy.double() * gamma.double()
+    want = r * (gr - xh * (gr * xh).mean(1, keepdim=True))
+    size = r * (gr.abs() + xh.abs() * (gr * xh).abs().mean(1, keepdim=True))
+    if with_ds:
+        want, size = want + ds.double(), size + ds.double().abs()
+    near = lambda got, ref, m: bool(((got.double() - ref).abs() <= H * ref.abs() + 64 * U * m + TINY).all())  # noqa: E731
+    assert near(dsum, want, size)
+    terms = dy.double() * xh
+    assert ((dgamma.double() - terms.sum(0)).abs() <= (t / 512 + 72) * U * terms.abs().sum(0) + 2.0 ** -149).all()
+    if p == 0:
+        assert dx is dsum
+    else:
+        # the mask that dropout alone draws, and dx = 0 under it
+        scale = float(N.keep_scale(p))
+        keep = mx.fp4_dropout(torch.ones_like(s), p, seed, offset) != 0
+        assert (dx[~keep] == 0).all() and near(dx, torch.where(keep, want * scale, 0.0), scale * size)
+        for row in (0, t - 1):
+            assert np.array_equal(host(keep[row]), row_mask(row, d, p, seed, offset))
+    again = mx.fp4_rmsnorm_backward(dy, s, rstd, gamma, ds, p, seed, offset)
+    assert torch.equal(again[0], dsum) and torch.equal(again[2], dgamma)

@@ -96,3 +96,44 @@ def test_non_finite_rows_stay_apart(gpu_lib, t, d):
         assert torch.equal(dsum[rest], grad[0][rest]) and not dsum[rows].isfinite().all(1).any()
         # every column of a row whose rstd is NaN, else only the columns of the infinities and NaN
         assert dgamma.isnan().all() if second is bad else (~dgamma.isfinite()).sum() == len(rows)
+
+
+U, H = 2.0 ** -24, 2.0 ** -8                             # half an fp32 step, half a bf16 step
+WIDTHS = [32, 160, 544, 1056, 2048, 2080, 4128, 8192, 8224, 16416, 32768]
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+def test_the_statistic_is_held_in_64_bits(gpu_lib, d):
+    """Small integers: a thread's sum of at most 32 squares of up to 255 is exact
+    in fp32, so that what remains is 64-bit work, one rounding to fp32 of rstd
+    (2^-40 stands for the 64-bit roundings), and for y one fp32 rounding before
+    bf16's: y is the float64 value rounded once wherever no tie lies within that
+    rounding.  A statistic in fp32 steps, or y in three, is further off."""
+    mx, rng = gpu_lib, np.random.default_rng(d)
+    t = max(3, (1 << 19) // d)
+    s = rng.integers(-255, 256, (t, d)).astype(np.float32)
+    s[0] = rng.integers(1, 4, d)
+    g_bits = synthetic.bf16_bits((1 + 0.3 * rng.standard_normal(d)).astype(np.float32))
+    eps = 1e-5
+    got = mx.fp4_rmsnorm_producer(dev16(synthetic.bf16_bits(s)), dev16(g_bits), eps, emit_y=True)
+    r64, y64 = N.rmsnorm(s.astype(np.float64), F.bf16_bits_to_f64(g_bits), eps)
+    assert (np.abs(host(got[1]).astype(np.float64) - r64) <= (U + 2.0 ** -40) * r64).all()
+    size = np.abs(y64)
+    step = 2.0 ** (np.floor(np.log2(np.where(size > 0, size, 1.0))) - 7)
+    low = np.floor(size / step) * step                   # the bf16 value below
+    tie = np.abs(size - (low + step / 2)) <= (U + 2.0 ** -36) * size
+    want = np.copysign(np.where(size - low > step / 2, low + step, low), y64)
+    y = val(got[2])
+    assert tie.mean() < 2.0 ** -12
+    assert np.array_equal(y[~tie], want[~tie])
+    assert (np.abs(y - y64) <= (H + 2 * U) * size).all()
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+def test_the_statistic_of_any_row(gpu_lib, d):
+    """Squares that round: at most 32 fused steps of a thread on a sum of
+    positive terms, of which the root halves the error, and rstd's rounding."""
+    s_bits = synthetic.tensor((5, d), std=1.0, seed=56, outlier_rate=0.002, outlier_scale=20.0)
+    got = gpu_lib.fp4_rmsnorm_producer(dev16(s_bits), dev16(synthetic.bf16_bits(np.ones(d, np.float32))), emit_codes=False)
+    r64 = N.rmsnorm(F.bf16_bits_to_f64(s_bits), np.ones(d), 1e-5)[0]
+    assert (np.abs(host(got[1]).astype(np.float64) - r64) <= 17.5 * U * r64).all()
