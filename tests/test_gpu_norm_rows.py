@@ -112,3 +112,54 @@ def test_backward_walks_its_rows(gpu_lib, t, d, f32, with_ds, p):
             assert np.array_equal(host(keep[row]), row_mask(row, d, p, seed, offset))
     again = mx.fp4_rmsnorm_backward(dy, s, rstd, gamma, ds, p, seed, offset)
     assert torch.equal(again[0], dsum) and torch.equal(again[2], dgamma)
+
+
+def test_masks_past_2_to_32_blocks(gpu_lib, room):
+    """More than 2^32 groups of eight columns: the counter's second word."""
+    mx, p, seed, offset = gpu_lib, 0.25, 2 ** 50 + 1, 2 ** 34 + 5
+    scale = F.bf16_bits_to_f64(N.f32_to_bf16_rne(N.keep_scale(p)))
+    t, d = (1 << 20) + 3, 32768
+    size = 2 * t * (d + 8)
+    if room < 2.2 * size:
+        pytest.skip(f"needs {int(2.2 * size) >> 30} GiB of free device memory")
+    x = torch.ones((t, d + 8), dtype=torch.bfloat16, device="cuda")
+    assert mx.fp4_dropout(x, p, seed, offset, out=x) is x
+    near = (1 << 35) // (d + 8)                           # the row that holds block 2^32
+    for r in (0, near - 1, near, near + 1, t - 1):
+        assert np.array_equal(val(x[r:r + 1])[0], np.where(row_mask(r, d + 8, p, seed, offset), scale, 0.0)), r
+    del x
+    x, ones = torch.ones((t, d), dtype=torch.bfloat16, device="cuda"), torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    s, rstd, *_ = mx.fp4_rmsnorm_producer(x, ones, p=p, seed=seed, offset=offset, emit_codes=False)
+    for r in (0, (1 << 20) - 1, 1 << 20, t - 1):
+        assert np.array_equal(val(s[r:r + 1])[0], np.where(row_mask(r, d, p, seed, offset), scale, 0.0)), r
+        want = 1 / np.sqrt(np.mean(val(s[r:r + 1])[0] ** 2) + np.float64(np.float32(1e-5)))
+        assert abs(float(rstd[r]) - want) <= 17.5 * U * want
+
+
+def test_backward_past_32_bit_offsets(gpu_lib, room):
+    """Rows on both sides of 2^32 elements against calls on those rows alone."""
+    mx, p, seed, offset = gpu_lib, 0.3, 3, 2 ** 32 + 7
+    t, d = (1 << 21) + 9, 2080
+    if room < 6 * t * d * 2:
+        pytest.skip(f"needs {6 * t * d * 2 >> 30} GiB of free device memory")
+    g = torch.Generator("cuda").manual_seed(9)
+    dy, s = (torch.empty((t, d), dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    gamma, rstd = torch.linspace(0.5, 1.5, d, device="cuda").bfloat16(), torch.rand(t, device="cuda", generator=g) + 0.5
+    dsum, dx, dgamma = mx.fp4_rmsnorm_backward(dy, s, rstd, gamma, dy, p, seed, offset)
+    near = (1 << 32) // d
+    total = torch.zeros(d, dtype=torch.float64, device="cuda")
+    size = torch.zeros(d, dtype=torch.float64, device="cuda")
+    for a in range(0, t, 1 << 16):
+        b = min(t, a + (1 << 16))
+        part = mx.fp4_rmsnorm_backward(dy[a:b], s[a:b], rstd[a:b], gamma, dy[a:b])
+        assert torch.equal(dsum[a:b], part[0]), a
+        terms = dy[a:b].double() * (s[a:b].double() * rstd[a:b, None].double())
+        total += terms.sum(0)
+        size += terms.abs().sum(0)
+    assert ((dgamma.double() - total).abs() <= (t / 512 + 72) * U * size).all()
+    scale = N.keep_scale(p)
+    for r in (0, near - 1, near, near + 1, t - 1):
+        keep = row_mask(r, d, p, seed, offset)
+        got, want = val(dx[r:r + 1])[0], val(dsum[r:r + 1])[0] * float(scale)
+        # dx rounds the unrounded gradient: two half steps from the rounded one's multiple
+        assert (got[~keep] == 0).all() and (np.abs(got - want)[keep] <= 2.02 * H * np.abs(want[keep]) + TINY).all(), r
