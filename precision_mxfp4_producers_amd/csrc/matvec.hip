@@ -12,10 +12,10 @@
 //
 // Bound by HBM for few rows: 57344 x 8192 MXFP4 with five E4M3 rows, 250 MB,
 // 49 us (5.1 TB/s; a bare loop of the same loads takes 41, contiguous loads
-// 34); gate/up 14336 x 4096 with one row, 62 MB, 13.6 us; 4096 x 4096 with one
-// row, 9 MB, 4.8 us (a bare loop 3.8).  With more rows x's way through LDS
-// takes over: gate/up 14336 x 4096 with 16 rows 16.6 us, 4096 x 14336 NVFP4
-// with 33 rows 22 us.
+// 34); gate/up 14336 x 4096 with one row, 62 MB, 13.7 us (calls in a row; some 1
+// us more in a kernel trace); 4096 x 4096 with one row, 9 MB, 4.8 us (kernel
+// trace; a bare loop 3.8).  With more rows x's way through LDS takes over:
+// gate/up 14336 x 4096 with 16 rows 16.4 us, 4096 x 14336 NVFP4 with 33 rows 22.
 //
 // Method: "Format-Aware Fusion for Fast FP4 Pretraining", §2.2 (Eq. 1) decode,
 // §2.4 row layouts, §3.2 gated FFN.
@@ -592,8 +592,11 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   const int mt = (a.m + 15) / 16, nw = mt > 1 ? 8 : 16;
   // Where x is not staged its way through LDS bounds the kernel (110 cycles a
   // step and 16 rows): two tiles of W a wave share it, if there are as many for
-  // every CU (33 rows on 8192 x 14336: 37 to 25 us, NVFP4 38 to 29; with up to
-  // 16 rows MXFP4 18 to 15.6, NVFP4 20.3 to 21.5, which keeps one).
+  // every CU (8192 x 14336, one tile to two: 17 rows 26.6 to 20.4 us, 33 rows
+  // 36.6 to 25.5, 64 rows 47.3 to 38.4, NVFP4 29.6 to 24.9, 38.3 to 29.3 and
+  // 51.1 to 40.7; 16 rows MXFP4 20.3 to 17.5; NVFP4 lost, 20.3 to 21.5, and
+  // keeps one).  So also where two tiles spill a few registers, bf16 x with
+  // more than 48 rows, and gated with up to 16 (20.8 to 18.8).
   const bool words = (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0, whole = a.k % 128 == 0 && words;
   const int nt = !staged && whole && tiles >= 2 * kMatvecGrid && (WT == kMx || mt > 1) ? 2 : 1;
   // groups of tiles between two meetings of the sums: what LDS holds beside x

@@ -48,8 +48,10 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
 
 // ---------------------------------------------------------------- dropout
 // out = bf16(dropout(x) [+ residual]); one thread per group of eight columns.
-// Bound by HBM: bf16 8192 x 14336, 470 MB, takes 80 us (5.9 TB/s; a 1 GiB copy
-// moves 5.2); the generator is some 400 of a wave's cycles per 3 KB.
+// Bound by HBM: bf16 8192 x 14336, 470 MB, takes 80-84 us (5.6-5.9 TB/s; a 1 GiB
+// copy moves 5.2); the generator is some 400 of a wave's cycles per 3 KB.  With
+// a residual it is not: that it may be absent is known at run time only, which
+// keeps its values in scratch memory (fp32 x, 940 MB: 246 us, 3.8 TB/s).
 // VEC: every row of every tensor starts on a 16-byte boundary; a group that
 // runs past the row's end, and every group otherwise, goes element by element
 // (a view's last row may end with its last element).
@@ -159,7 +161,7 @@ struct NormOut {
 // one), and all of a thread's loads go out before its first use: 8192 x 4096,
 // fp32 x with dropout and residual to s and E4M3, 302 MB, takes 52 us (5.8
 // TB/s), and took 89 with the loads of each group of columns behind the stores
-// of the one before.  Bound by HBM; one token by its launch (2.8 us).
+// of the one before.  Bound by HBM; one token by its launch (3.3 us).
 template <int G, int V, bool F32, bool RES>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, int d, const void* __restrict__ x,
                                                                     int64_t ldx, const uint16_t* residual,
@@ -247,7 +249,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rmsnorm_kernel(int64_t t, i
 // the whole grid, loads the next row's tensors before it works on the current
 // one, keeps its columns' share of dgamma in registers and writes it once, as
 // one row of the workspace.  Bound by HBM: fp32 dy 8192 x 4096 with ds and
-// dropout, 402 MB, takes 68 us and 5 for the sums of dgamma (88 and 10 without
+// dropout, 403 MB, takes 70 us and 5 for the sums of dgamma (88 and 10 without
 // the next row's loads and with one column a thread in the sums).
 template <int V, bool F32, bool DS>
 struct BwdRow {
