@@ -597,6 +597,260 @@ fp4_status fp4_swiglu_matvec(int64_t m, int64_t f, int64_t d, const void* x, int
                              const uint8_t* w13_codes, const uint8_t* w13_scales, uint16_t* h,
                              hipStream_t stream);
 
+/* Activation of a product's epilogue (int-sized, like fp4_round). */
+#ifdef __cplusplus
+enum fp4_act : int { FP4_ACT_NONE = 0, FP4_ACT_RELU = 1, FP4_ACT_GELU = 2, FP4_ACT_GELU_TANH = 3, FP4_ACT_SILU = 4 };
+#else
+typedef enum { FP4_ACT_NONE = 0, FP4_ACT_RELU = 1, FP4_ACT_GELU = 2, FP4_ACT_GELU_TANH = 3, FP4_ACT_SILU = 4 } fp4_act;
+#endif
+
+/*
+ * fp4_gemm with an epilogue (§2.3 Eq. 4; §3.1: no round trip between a product
+ * and the boundary behind it):
+ *   z = sum_k dec(A)[m][k] dec(B)[n][k] + bias[n]         in fp32
+ *   y = act(z) + residual[m][n]                           rounded once to bf16, or fp32
+ * act: none; relu; gelu z erfc(-z / sqrt 2) / 2; gelu_tanh z / (1 + exp(-2 u)),
+ * u = sqrt(2/pi) (z + 0.044715 z^3); silu z / (1 + exp(-z)).  It takes the fp32
+ * z; z itself is kept rounded to bf16 for fp4_act_backward.  At minus infinity
+ * the last three are their limit 0.
+ *   a_codes [m][k/2], a_scales [m][k/32]; b_codes [n][k/2], b_scales [n][k/32]
+ *   bias      [n] bf16 or fp32 (bias_type), or NULL
+ *   residual  [m][ldr] bf16, or NULL
+ *   z         [m][n] bf16, or NULL
+ *   y         [m][ldy] bf16 or fp32 (y_type); y may be the residual (bf16, ldy = ldr)
+ * Any m; k = 0 gives z = bias.  Deterministic.
+ * Errors: FP4_EINVAL bad type or act, or null pointer; FP4_ESHAPE m negative, n
+ * or k not a non-negative multiple of 32, k >= 2^24, a leading dimension below
+ * n, or more than 2^31 - 1 output tiles of 256 x 256; FP4_EALIGN an operand,
+ * residual, z or y not 16-byte aligned, bias not aligned to its element, ldr
+ * or ldy (bf16) not a multiple of 8, or ldy (fp32) not a multiple of 4.
+ */
+fp4_status fp4_gemm_act(int64_t m, int64_t n, int64_t k,
+                        const uint8_t* a_codes, const uint8_t* a_scales,
+                        const uint8_t* b_codes, const uint8_t* b_scales,
+                        const void* bias, fp4_dtype bias_type, fp4_act act,
+                        const uint16_t* residual, int64_t ldr, uint16_t* z,
+                        void* y, fp4_dtype y_type, int64_t ldy, hipStream_t stream);
+
+/*
+ * The same epilogue on fp4_matvec: y = act(x dec(W)^T + bias) + residual for up
+ * to 64 rows of x (bf16, or E4M3 codes with x_scales).  No z is kept.
+ * Operands, limits and errors as fp4_matvec (ldy for ldc); types, bias and
+ * residual as fp4_gemm_act.  Any n.  FP4_EALIGN: x or w_codes not 16-byte
+ * aligned, ldx not a multiple of 8 (bf16), or bias, residual or y not aligned
+ * to its element.
+ */
+fp4_status fp4_matvec_act(int64_t m, int64_t n, int64_t k, const void* x, int64_t ldx, const uint8_t* x_scales,
+                          const uint8_t* w_codes, const uint8_t* w_scales,
+                          const void* bias, fp4_dtype bias_type, fp4_act act,
+                          const uint16_t* residual, int64_t ldr,
+                          void* y, fp4_dtype y_type, int64_t ldy, hipStream_t stream);
+
+/*
+ * Gradients of that epilogue from the saved bf16 z (the gradient of the
+ * residual is dy itself):
+ *   dz    = bf16(dy * act'(z))                            for fp4_quantize_dual
+ *   dbias (+)= sum over the m rows of dy * act'(z)        fp32 [n], before dz's rounding
+ * act' of relu is 0 at 0.  Deterministic: at most 512 partial sums of dbias
+ * meet in the workspace and are added in order.
+ *   dy [m][lddy] bf16 or fp32; z [m][ldz] bf16; dz [m][n] bf16
+ *   dbias [n] fp32, or NULL (then the workspace may be NULL too)
+ *   workspace  fp4_act_backward_workspace(m, n) bytes, 16-byte aligned, in use
+ *              until the call's work on the stream is done
+ * m = 0 sets dbias to 0 (leaves it unchanged when accumulating).  Outputs
+ * overlap no input.
+ * Errors: FP4_EINVAL bad type or act, accumulate not 0 or 1, or null pointer;
+ * FP4_ESHAPE m negative or above 2^40, n not a non-negative multiple of 32 or
+ * above 2^28, a leading dimension below n, or a workspace below that size;
+ * FP4_EALIGN dy, z, dz or the workspace not 16-byte aligned, dbias not 4-byte
+ * aligned, ldz or lddy (bf16) not a multiple of 8, or lddy (fp32) not a multiple
+ * of 4.
+ */
+fp4_status fp4_act_backward(int64_t m, int64_t n, const void* dy, fp4_dtype dy_type, int64_t lddy,
+                            const uint16_t* z, int64_t ldz, fp4_act act,
+                            uint16_t* dz, float* dbias, int accumulate,
+                            void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of the workspace above; -1 for a shape the call refuses.  Host-only. */
+int64_t fp4_act_backward_workspace(int64_t m, int64_t n);
+
+/*
+ * Layers of several experts.  A router gives each of t tokens k experts; slot
+ * t k + j is token t's j-th choice.  The sorted order gives expert e the rows
+ * offsets[e] .. offsets[e + 1] - 1 of every sorted tensor: its slots in
+ * ascending order, then padding up to a multiple of `align`.  align = 32 (or a
+ * multiple of it up to 256) is what products with column-facing codes need,
+ * whose blocks hold 32 tokens; align = 1 packs the rows for the few-row
+ * products.  Sorted tensors have `capacity` rows; those behind the last segment
+ * belong to no expert.  All of it stays on the device: no call waits for the
+ * counts.
+ *   offsets [experts + 1] int32
+ *   slots   [capacity] int32: the slot in a row, -1 where there is none
+ *   rows    [t][k] int32: the row of a slot, -1 where it is not routed
+ * ids outside 0 .. experts - 1 are not routed (padded tokens, dropped choices).
+ * The calls below check no index on the host; one that is out of its range is
+ * taken for "none", and segments that are not ascending are cut, so that no
+ * access leaves a tensor.
+ */
+
+/* Rows of the sorted tensors: t k for align = 1, else the slots and min(experts,
+ * t k) (align - 1) rows of padding, in whole 256s; -1 for a shape that the sort
+ * refuses.  Host-only. */
+int64_t fp4_expert_capacity(int64_t t, int64_t k, int64_t experts, int64_t align);
+
+/* Bytes of the sort's workspace (0 for a few thousand slots).  Host-only. */
+int64_t fp4_expert_sort_workspace(int64_t t, int64_t k, int64_t experts);
+
+/*
+ * Sorts the slots by expert, stably and deterministically.
+ *   ids       [t][k] int32 or int64 (id_bytes 4 or 8)
+ *   offsets, slots, rows as above, wholly written
+ *   workspace fp4_expert_sort_workspace(t, k, experts) bytes, 4-byte aligned, in
+ *             use until the call's work on the stream is done
+ * Errors: FP4_EINVAL bad id_bytes or null pointer; FP4_ESHAPE t negative, k
+ * below 1, t k above 2^30, experts outside 1 .. 1024, align not 1 or a multiple
+ * of 32 up to 256, a capacity below fp4_expert_capacity or above 2^30 + 2^18, or
+ * a workspace below its size; FP4_EALIGN a pointer not aligned to its element.
+ */
+fp4_status fp4_expert_sort(int64_t t, int64_t k, int64_t experts, const void* ids, int id_bytes, int64_t align,
+                           int64_t capacity, int32_t* offsets, int32_t* slots, int32_t* rows,
+                           void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The tokens' activations in sorted order, xs[r] = x[slots[r] / k], zero in rows
+ * without a token, and their codes: the bytes of fp4_quantize_rows(xs, FP4_RTN)
+ * (FP4_E2M1) or those of fp4_rmsnorm_producer's FP4_E4M3 on xs.  fp4_quantize_cols
+ * of xs gives the Wgrad's operand.
+ *   x     [t][ldx] bf16
+ *   xs    [rows][d] bf16, or NULL
+ *   codes [rows][d/2] (E2M1) or [rows][d] (E4M3), scales [rows][d/32]; both or
+ *         neither NULL
+ * The gradient of x is fp4_expert_combine of the gradient of xs without weights.
+ * Errors: FP4_EINVAL bad format, exactly one of codes, scales NULL, or another
+ * null pointer; FP4_ESHAPE a negative size, k below 1, t, k or d above 2^30, d
+ * not a multiple of 32, ldx below d, or rows above 2^30 + 2^18; FP4_EALIGN x, xs
+ * or codes not 16-byte aligned, slots not 4-byte aligned, or ldx not a multiple
+ * of 8.
+ */
+fp4_status fp4_expert_gather(int64_t t, int64_t k, int64_t d, int64_t rows, const uint16_t* x, int64_t ldx,
+                             const int32_t* slots, uint16_t* xs, fp4_format format, uint8_t* codes, uint8_t* scales,
+                             hipStream_t stream);
+
+/*
+ * The experts' results back at their tokens:
+ *   out[t] = bf16(sum over j of weights[t][j] z[where[t][j]] + residual[t])
+ * in fp32, j ascending, one rounding.  A choice that is not routed leaves no
+ * trace, its weight included.
+ *   z        [rows][ldz] bf16 or fp32 (z_type)
+ *   where    [t][k] int32: the rows of fp4_expert_sort
+ *   weights  [t][k] fp32, or NULL (all 1)
+ *   residual [t][ldr] bf16, or NULL
+ *   out      [t][ldo] bf16; may be the residual (ldo = ldr)
+ * Errors: FP4_EINVAL bad z_type or null pointer; FP4_ESHAPE a negative size, k
+ * below 1, t k above 2^30, d not a multiple of 32 or above 2^30, rows above 2^30
+ * + 2^18, or a leading dimension below d; FP4_EALIGN z, residual or out not
+ * 16-byte aligned, where or weights not 4-byte aligned, a bf16 leading dimension
+ * not a multiple of 8 or an fp32 one not of 4.
+ */
+fp4_status fp4_expert_combine(int64_t t, int64_t k, int64_t d, int64_t rows, const void* z, fp4_dtype z_type, int64_t ldz,
+                              const int32_t* where, const float* weights, const uint16_t* residual, int64_t ldr,
+                              uint16_t* out, int64_t ldo, hipStream_t stream);
+
+/*
+ * Gradients of that sum (the residual's is dy itself):
+ *   dz[r]    = bf16(weights[t][j] dy[t]) in the row of slot t k + j, zero in rows
+ *              without a slot
+ *   dw[t][j] = sum over d of dy[t] z[where[t][j]] in fp32, 0 where not routed
+ *   dy [t][lddy] bf16 or fp32; z [rows][ldz] bf16 or fp32; slots, where, weights
+ *   dz [rows][d] bf16; dw [t][k] fp32
+ * slots and where must be those of one sort: rows that neither names as a slot's
+ * are unspecified.  Deterministic.  Errors as fp4_expert_combine.
+ */
+fp4_status fp4_expert_combine_backward(int64_t t, int64_t k, int64_t d, int64_t rows, const void* dy, fp4_dtype dy_type,
+                                       int64_t lddy, const void* z, fp4_dtype z_type, int64_t ldz, const int32_t* slots,
+                                       const int32_t* where, const float* weights, uint16_t* dz, float* dw,
+                                       hipStream_t stream);
+
+/*
+ * Products of sorted rows with their experts' weights:
+ *   C[r][n] = sum_k dec(A)[r][k] dec(B_e)[n][k] for the rows r of expert e
+ * and 0 in the rows behind the last segment; with the second operands set, plus
+ * the same sum over A2 and B2 (as fp4_gemm_pair: the gated FFN's dX = dA W1 + dB
+ * W3), in fp32, rounded once.  Fprop: B the experts' row layouts; Dgrad: their
+ * column layouts.  Any segments (align 1 too).  Deterministic.
+ *   a_codes [rows][k/2], a_scales [rows][k/32]
+ *   b_codes [experts][n][k/2], b_scales [experts][n][k/32]
+ *   c       [rows][ldc] bf16 or fp32 (c_type)
+ * Errors: FP4_EINVAL bad c_type, or null pointer (the second operands: all four
+ * or none); FP4_ESHAPE experts outside 1 .. 1024, rows negative or above 2^30, n
+ * or k not a non-negative multiple of 32, n above 2^30, k >= 2^24, ldc below n,
+ * or more tiles than a launch holds; FP4_EALIGN an operand or c not 16-byte
+ * aligned, offsets not 4-byte aligned, or ldc not a multiple of 8 (bf16) or 4.
+ */
+fp4_status fp4_gemm_experts(int64_t experts, int64_t rows, int64_t n, int64_t k, const int32_t* offsets,
+                            const uint8_t* a_codes, const uint8_t* a_scales,
+                            const uint8_t* b_codes, const uint8_t* b_scales,
+                            const uint8_t* a2_codes, const uint8_t* a2_scales,
+                            const uint8_t* b2_codes, const uint8_t* b2_scales,
+                            void* c, fp4_dtype c_type, int64_t ldc, hipStream_t stream);
+
+/*
+ * The experts' weight gradients, from column-facing codes of sorted tensors:
+ *   C_e[m][n] (+)= sum over the tokens of e's segment of dec(A)[m][token] dec(B)[n][token]
+ * 0 (unchanged when accumulating) for an expert without tokens.  Segments must
+ * be multiples of 32 rows.  Deterministic.
+ *   a_codes [m][tokens/2], a_scales [m][tokens/32]; b_codes [n][tokens/2], ...
+ *   c       [experts][m][n] bf16 or fp32 (accumulate: fp32)
+ * Errors: FP4_EINVAL bad c_type, accumulate not 0 or 1, accumulate into bf16, or
+ * null pointer; FP4_ESHAPE experts outside 1 .. 1024, tokens negative, not a
+ * multiple of 256 or >= 2^24, m or n not a non-negative multiple of 32, or more
+ * than 2^31 - 1 tiles; FP4_EALIGN as fp4_gemm_experts.
+ */
+fp4_status fp4_gemm_experts_wgrad(int64_t experts, int64_t tokens, int64_t m, int64_t n, const int32_t* offsets,
+                                  const uint8_t* a_codes, const uint8_t* a_scales,
+                                  const uint8_t* b_codes, const uint8_t* b_scales,
+                                  void* c, fp4_dtype c_type, int accumulate, hipStream_t stream);
+
+/*
+ * fp4_swiglu_producer on sorted rows, each with its expert's weights; rows
+ * behind the last segment have a = b = h = +0.  Segments must be multiples of 32
+ * rows (others are cut down to one).
+ *   x_codes [rows][d/2], x_scales [rows][d/32]
+ *   w13_codes [experts][2f][d/2], w13_scales [experts][2f][d/32]
+ *   outputs as fp4_swiglu_producer with t = rows
+ * Errors as fp4_swiglu_producer; FP4_ESHAPE also for experts outside 1 .. 1024,
+ * rows or f above 2^30 or d >= 2^24; FP4_EALIGN also for offsets not 4-byte
+ * aligned.
+ */
+fp4_status fp4_swiglu_producer_experts(int64_t experts, int64_t rows, int64_t f, int64_t d, const int32_t* offsets,
+                                       const uint8_t* x_codes, const uint8_t* x_scales,
+                                       const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                       uint16_t* a_bf16, uint16_t* b_bf16,
+                                       uint8_t* h_codes, uint8_t* h_scales,
+                                       uint8_t* ht_codes, uint8_t* ht_scales,
+                                       uint32_t sign_mask16, hipStream_t stream);
+
+/*
+ * fp4_matvec and fp4_swiglu_matvec on sorted rows, each with its expert's
+ * weights: the form for a few decoded tokens, which reads the weights of the
+ * experts that have rows, once for every sixteen of them.  Rows behind the last
+ * segment get 0.
+ *   x        bf16 [rows][ldx], or E4M3 [rows][k] with x_scales [rows][k/32]
+ *   w_codes  [experts][n][k/2], w_scales [experts][n][k/32]; w13: [experts][2f]
+ *   c        [rows][ldc] fp32;  h [rows][f] bf16
+ * Errors as fp4_matvec and fp4_swiglu_matvec, with rows (up to 65536) for m;
+ * FP4_ESHAPE also for experts outside 1 .. 1024; FP4_EALIGN also for offsets not
+ * 4-byte aligned.
+ */
+fp4_status fp4_matvec_experts(int64_t experts, int64_t rows, int64_t n, int64_t k, const int32_t* offsets,
+                              const void* x, int64_t ldx, const uint8_t* x_scales,
+                              const uint8_t* w_codes, const uint8_t* w_scales,
+                              float* c, int64_t ldc, hipStream_t stream);
+fp4_status fp4_swiglu_matvec_experts(int64_t experts, int64_t rows, int64_t f, int64_t d, const int32_t* offsets,
+                                     const void* x, int64_t ldx, const uint8_t* x_scales,
+                                     const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                     uint16_t* h, hipStream_t stream);
+
 /*
  * Fixed 16-entry sign vector for H32 as a bit mask (bit j set => d_j = -1).
  * App. A.1 fixes one 16-entry sign vector, shared by both Wgrad operands and

@@ -20,6 +20,7 @@ from .build import lib_path
 FP4_RTN, FP4_SR = 0, 1
 FP4_BF16, FP4_F32 = 0, 1
 FP4_E2M1, FP4_E4M3 = 0, 1
+FP4_ACT_NONE, FP4_ACT_RELU, FP4_ACT_GELU, FP4_ACT_GELU_TANH, FP4_ACT_SILU = range(5)
 STATUS = {0: "FP4_OK", 1: "FP4_EINVAL", 2: "FP4_ESHAPE", 3: "FP4_EALIGN", 4: "FP4_EHIP"}
 
 _lib = None
@@ -50,11 +51,28 @@ _SIGS = {
     "fp4_matvec": [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _int, _vp],
     "fp4_nv_matvec": [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _int, _vp],
     "fp4_swiglu_matvec": [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp],
+    "fp4_gemm_act": [_i64, _i64, _i64] + [_vp] * 5 + [_int, _int, _vp, _i64, _vp, _vp, _int, _i64, _vp],
+    "fp4_matvec_act": [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _int, _int, _vp, _i64, _vp, _int, _i64, _vp],
+    "fp4_act_backward": [_i64, _i64, _vp, _int, _i64, _vp, _i64, _int, _vp, _vp, _int, _vp, _i64, _vp],
+    "fp4_act_backward_workspace": [_i64, _i64],
+    "fp4_expert_capacity": [_i64, _i64, _i64, _i64],
+    "fp4_expert_sort_workspace": [_i64, _i64, _i64],
+    "fp4_expert_sort": [_i64, _i64, _i64, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp],
+    "fp4_expert_gather": [_i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _int, _vp, _vp, _vp],
+    "fp4_expert_combine": [_i64, _i64, _i64, _i64, _vp, _int, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp],
+    "fp4_expert_combine_backward": [_i64, _i64, _i64, _i64, _vp, _int, _i64, _vp, _int, _i64] + [_vp] * 6,
+    "fp4_gemm_experts": [_i64, _i64, _i64, _i64] + [_vp] * 10 + [_int, _i64, _vp],
+    "fp4_gemm_experts_wgrad": [_i64, _i64, _i64, _i64] + [_vp] * 6 + [_int, _int, _vp],
+    "fp4_swiglu_producer_experts": [_i64, _i64, _i64, _i64] + [_vp] * 11 + [_u32, _vp],
+    "fp4_matvec_experts": [_i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp],
+    "fp4_swiglu_matvec_experts": [_i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp],
     "fp4_sign_mask_from_seed": [_u64],
     "fp4_last_hip_error": [],
     "fp4_abi_version": [],
 }
-_RESTYPES = {"fp4_sign_mask_from_seed": _u32, "fp4_rmsnorm_backward_workspace": _i64}
+_RESTYPES = {"fp4_sign_mask_from_seed": _u32}
+_RESTYPES |= {name: _i64 for name in ("fp4_rmsnorm_backward_workspace", "fp4_act_backward_workspace", "fp4_expert_capacity",
+                                      "fp4_expert_sort_workspace")}
 EXPORTS = tuple(_SIGS)
 
 
@@ -662,6 +680,344 @@ def fp4_swiglu_matvec(x, w13_codes, w13_scales, x_scales=None, h=None):
     h = _out16(h, (m, f), x.device, "h")
     _check(load().fp4_swiglu_matvec(m, f, d, x.data_ptr(), ldx, _p(x_scales), w13_codes.data_ptr(),
                                     w13_scales.data_ptr(), h.data_ptr(), _raw_stream(cur)))
+    return h
+
+
+_OUTPUT_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _typed_out(t, shape, dtype, device, name):
+    """An output of bf16 or fp32 rows: returns (tensor, its leading dimension).
+    `dtype` is that of one allocated here."""
+    if t is None:
+        if dtype not in _OUTPUT_TYPES:
+            raise Fp4Error(f"{name} must be bf16 or fp32, not {dtype}")
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device), shape[1]
+    _here(t, name, torch.cuda.current_device())
+    if t.dtype not in _OUTPUT_TYPES or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+        raise Fp4Error(f"{name} must be bf16 or fp32 of shape {tuple(shape)} with unit column stride")
+    return t, t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _bias(bias, n, cur):
+    if bias is None:
+        return None, 0
+    _vec(bias, "bias", n, _OUTPUT_TYPES, cur)
+    return bias.data_ptr(), 1 if bias.dtype is torch.float32 else 0
+
+
+def _ld(t, ld, cols):
+    """The leading dimension that _rows2d found; a single row's is its length."""
+    return ld if t.shape[0] > 1 else cols
+
+
+def fp4_gemm_act(a_codes, a_scales, b_codes, b_scales, act=FP4_ACT_NONE, bias=None, residual=None, dtype=torch.bfloat16,
+                 emit_z=False, z=None, y=None):
+    """y = act(A B^T + bias) + residual in bf16 or fp32 (`dtype`, or y's own):
+    returns (y, z), z the bf16 pre-activation where emit_z, else None."""
+    cur = _current(a_codes, "a_codes")
+    m, n, k = _gemm_shapes([((a_codes, "a_codes"), (a_scales, "a_scales"), (b_codes, "b_codes"), (b_scales, "b_scales"))])
+    shape = torch.Size((m, n))
+    bias_p, bias_f32 = _bias(bias, n, cur)
+    ldr = 0 if residual is None else _ld(residual, _rows2d(residual, "residual", cur, shape), n)
+    y, ldy = _typed_out(y, shape, dtype, a_codes.device, "y")
+    z = _out16(z, shape, a_codes.device, "z") if emit_z else None
+    _check(load().fp4_gemm_act(m, n, k, _p(a_codes), _p(a_scales), _p(b_codes), _p(b_scales), bias_p, bias_f32, int(act),
+                               _p(residual), ldr, _p(z), y.data_ptr(), 1 if y.dtype is torch.float32 else 0, ldy,
+                               _raw_stream(cur)))
+    return y, z
+
+
+def fp4_matvec_act(x, w_codes, w_scales, act=FP4_ACT_NONE, x_scales=None, bias=None, residual=None, dtype=torch.bfloat16,
+                   y=None):
+    """y = act(x dec(W)^T + bias) + residual for up to 64 rows of x (as
+    fp4_matvec), in bf16 or fp32."""
+    cur = _current(x, "x")
+    m, n, k, ldx = _few_rows(x, x_scales, w_codes, cur)
+    _bytes2d(w_scales, "w_scales", cur, (n, k // 32))
+    shape = torch.Size((m, n))
+    bias_p, bias_f32 = _bias(bias, n, cur)
+    ldr = 0 if residual is None else _ld(residual, _rows2d(residual, "residual", cur, shape), n)
+    y, ldy = _typed_out(y, shape, dtype, x.device, "y")
+    _check(load().fp4_matvec_act(m, n, k, x.data_ptr(), ldx, _p(x_scales), w_codes.data_ptr(), w_scales.data_ptr(), bias_p,
+                                 bias_f32, int(act), _p(residual), ldr, y.data_ptr(), 1 if y.dtype is torch.float32 else 0,
+                                 ldy, _raw_stream(cur)))
+    return y
+
+
+def fp4_act_backward(dy, z, act, emit_dbias=True, accumulate=False, dz=None, dbias=None):
+    """Gradients of fp4_gemm_act's epilogue: returns (dz, dbias), dz = bf16(dy
+    act'(z)) and dbias its fp32 column sums (None without emit_dbias)."""
+    cur = _current(dy, "dy")
+    lddy = _rows2d(dy, "dy", cur, None, _ROWS32)
+    shape = dy.shape
+    m, n = shape
+    ldz = _rows2d(z, "z", cur, shape)
+    if accumulate and dbias is None:
+        raise Fp4Error("accumulate needs a dbias tensor")
+    dz = _out16(dz, shape, dy.device, "dz")
+    dbias = _out32(dbias, n, dy.device, "dbias") if emit_dbias else None
+    lib = load()
+    size = lib.fp4_act_backward_workspace(m, n) if emit_dbias else 0
+    ws = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=dy.device) if size > 0 else None
+    _check(lib.fp4_act_backward(m, n, dy.data_ptr(), 1 if dy.dtype is torch.float32 else 0, lddy, z.data_ptr(), ldz, int(act),
+                                dz.data_ptr(), _p(dbias), 1 if accumulate else 0, _p(ws), max(size, 0), _raw_stream(cur)))
+    return dz, dbias
+
+
+def _index(t, name, shape, cur):
+    _here(t, name, cur)
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise Fp4Error(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+def _out_index(t, shape, device, name, cur):
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    _index(t, name, shape, cur)
+    return t
+
+
+def fp4_expert_capacity(t, k, experts, align=32):
+    """Rows of the sorted tensors of t tokens with k of `experts` each."""
+    rows = load().fp4_expert_capacity(t, k, experts, align)
+    if rows < 0:
+        raise Fp4Error("FP4_ESHAPE")
+    return rows
+
+
+def fp4_expert_sort(ids, experts, align=32, out=None):
+    """Sorts the slots of ids [t][k] (int32 or int64) by expert: returns (offsets
+    [experts + 1], slots [capacity], rows [t][k]).  `out` may hold the three; its
+    slots may be longer than the capacity."""
+    cur = _current(ids, "ids")
+    _here(ids, "ids", cur)
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2 or not ids.is_contiguous():
+        raise Fp4Error("ids must be a contiguous 2-D int32 or int64 tensor")
+    t, k = ids.shape
+    lib = load()
+    capacity = lib.fp4_expert_capacity(t, k, experts, align)
+    if capacity < 0:
+        raise Fp4Error("FP4_ESHAPE")
+    o_offsets, o_slots, o_rows = _NONE3 if out is None else out
+    if o_slots is not None:
+        capacity = max(capacity, o_slots.numel())
+    offsets = _out_index(o_offsets, (experts + 1,), ids.device, "offsets", cur)
+    slots = _out_index(o_slots, (capacity,), ids.device, "slots", cur)
+    rows = _out_index(o_rows, ids.shape, ids.device, "rows", cur)
+    size = lib.fp4_expert_sort_workspace(t, k, experts)
+    ws = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=ids.device) if size > 0 else None
+    _check(lib.fp4_expert_sort(t, k, experts, ids.data_ptr(), 4 if ids.dtype is torch.int32 else 8, align, capacity,
+                               offsets.data_ptr(), slots.data_ptr(), rows.data_ptr(), _p(ws), size, _raw_stream(cur)))
+    return offsets, slots, rows
+
+
+def fp4_expert_gather(x, slots, k, fmt=FP4_E2M1, emit_x=True, emit_codes=True, out=None):
+    """The tokens' bf16 activations x [t][d] in sorted order and their codes:
+    returns (xs, codes, scales), None where not emitted."""
+    cur = _current(x, "x")
+    ldx = _rows2d(x, "x", cur)
+    t, d = x.shape
+    if d % 32:
+        raise Fp4Error("the row length must be a multiple of 32")
+    _here(slots, "slots", cur)
+    if slots.dim() != 1:
+        raise Fp4Error("slots must be 1-D")
+    rows = slots.shape[0]
+    _index(slots, "slots", (rows,), cur)
+    o_xs, o_codes, o_scales = _NONE3 if out is None else out
+    xs = _out16(o_xs, torch.Size((rows, d)), x.device, "xs") if emit_x else None
+    codes = scales = None
+    if emit_codes:
+        codes = _out8(o_codes, rows, d // 2 if fmt == FP4_E2M1 else d, x.device, "codes")
+        scales = _out8(o_scales, rows, d // 32, x.device, "scales")
+    _check(load().fp4_expert_gather(t, int(k), d, rows, x.data_ptr(), ldx, slots.data_ptr(), _p(xs), int(fmt), _p(codes),
+                                    _p(scales), _raw_stream(cur)))
+    return xs, codes, scales
+
+
+def _combine_checks(z, rows, weights, cur):
+    """Shapes of the combine calls: returns (t, k, sorted rows, d, ldz)."""
+    ldz = _rows2d(z, "z", cur, None, _ROWS32)
+    _here(rows, "rows", cur)
+    if rows.dim() != 2:
+        raise Fp4Error("rows must be 2-D")
+    _index(rows, "rows", rows.shape, cur)
+    if weights is not None:
+        _here(weights, "weights", cur)
+        if weights.dtype is not torch.float32 or weights.shape != rows.shape or not weights.is_contiguous():
+            raise Fp4Error(f"weights must be a contiguous fp32 tensor of shape {tuple(rows.shape)}")
+    return *rows.shape, *z.shape, ldz
+
+
+def fp4_expert_combine(z, rows, weights=None, residual=None, out=None):
+    """out[t] = bf16(sum_j weights[t][j] z[rows[t][j]] + residual[t]); without
+    weights, of a gathered tensor's gradient, the gradient of what was gathered."""
+    cur = _current(z, "z")
+    t, k, n, d, ldz = _combine_checks(z, rows, weights, cur)
+    shape = torch.Size((t, d))
+    ldr = 0 if residual is None else _ld(residual, _rows2d(residual, "residual", cur, shape), d)
+    if out is None:
+        out = _out16(None, shape, z.device, "out")
+        ldo = d
+    else:
+        ldo = _ld(out, _rows2d(out, "out", cur, shape), d)
+    _check(load().fp4_expert_combine(t, k, d, n, z.data_ptr(), 1 if z.dtype is torch.float32 else 0, ldz, rows.data_ptr(),
+                                     _p(weights), _p(residual), ldr, out.data_ptr(), ldo, _raw_stream(cur)))
+    return out
+
+
+def fp4_expert_combine_backward(dy, z, slots, rows, weights, dz=None, dw=None):
+    """Gradients of fp4_expert_combine: returns (dz, dw), dz in sorted order and
+    zero in rows without a token."""
+    cur = _current(dy, "dy")
+    if weights is None:
+        raise Fp4Error("weights must be a contiguous fp32 tensor")
+    t, k, n, d, ldz = _combine_checks(z, rows, weights, cur)
+    lddy = _rows2d(dy, "dy", cur, torch.Size((t, d)), _ROWS32)
+    _index(slots, "slots", (n,), cur)
+    dz = _out16(dz, z.shape, z.device, "dz")
+    if dw is None:
+        dw = torch.empty_strided((t, k), (k, 1), dtype=torch.float32, device=z.device)
+    else:
+        _out(dw, (t, k), torch.float32, z.device, "dw")
+    _check(load().fp4_expert_combine_backward(t, k, d, n, dy.data_ptr(), 1 if dy.dtype is torch.float32 else 0, lddy,
+                                              z.data_ptr(), 1 if z.dtype is torch.float32 else 0, ldz, slots.data_ptr(),
+                                              rows.data_ptr(), weights.data_ptr(), dz.data_ptr(), dw.data_ptr(),
+                                              _raw_stream(cur)))
+    return dz, dw
+
+
+def _expert_weights(codes, scales, name, cur):
+    """[experts][n][k/2] codes with their scales: returns (experts, n, k)."""
+    _here(codes, f"{name}_codes", cur)
+    if codes.dtype is not torch.uint8 or codes.dim() != 3 or not codes.is_contiguous():
+        raise Fp4Error(f"{name}_codes must be a contiguous 3-D uint8 tensor")
+    e, n, k = codes.shape
+    _bytes2d(scales, f"{name}_scales", cur, (e, n, 2 * k // 32))
+    return e, n, 2 * k
+
+
+def _sorted_codes(offsets, codes, scales, name, experts, k, cur):
+    _index(offsets, "offsets", (experts + 1,), cur)
+    _here(codes, f"{name}_codes", cur)
+    if codes.dim() != 2 or codes.shape[1] * 2 != k:
+        raise Fp4Error(f"{name}_codes must be 2-D with {k} values per row")
+    _bytes2d(codes, f"{name}_codes", cur, codes.shape)
+    _bytes2d(scales, f"{name}_scales", cur, (codes.shape[0], k // 32))
+    return codes.shape[0]
+
+
+def fp4_gemm_experts(offsets, a_codes, a_scales, b_codes, b_scales, dtype=torch.float32, c=None, pair=None):
+    """C[r] = dec(A)[r] dec(B_e)^T for the rows of each expert's segment, 0 behind
+    the last; b_codes [experts][n][k/2].  `pair`: (a2_codes, a2_scales, b2_codes,
+    b2_scales) of the same shapes, whose products are added.  C is bf16 or fp32."""
+    cur = _current(a_codes, "a_codes")
+    e, n, k = _expert_weights(b_codes, b_scales, "b", cur)
+    rows = _sorted_codes(offsets, a_codes, a_scales, "a", e, k, cur)
+    second = (None,) * 4
+    if pair is not None:
+        if _expert_weights(pair[2], pair[3], "b2", cur) != (e, n, k) or _sorted_codes(offsets, pair[0], pair[1], "a2", e, k, cur) != rows:
+            raise Fp4Error("operand shapes disagree")
+        second = tuple(x.data_ptr() for x in pair)
+    c, ldc = _typed_out(c, torch.Size((rows, n)), dtype, a_codes.device, "c")
+    _check(load().fp4_gemm_experts(e, rows, n, k, offsets.data_ptr(), a_codes.data_ptr(), a_scales.data_ptr(),
+                                   b_codes.data_ptr(), b_scales.data_ptr(), *second, c.data_ptr(),
+                                   1 if c.dtype is torch.float32 else 0, ldc, _raw_stream(cur)))
+    return c
+
+
+def fp4_gemm_experts_wgrad(offsets, a_codes, a_scales, b_codes, b_scales, dtype=torch.float32, c=None, accumulate=False):
+    """C_e = dec(A)[:, segment] dec(B)[:, segment]^T per expert, from column-facing
+    codes [m][tokens/2] and [n][tokens/2]: returns [experts][m][n]."""
+    cur = _current(a_codes, "a_codes")
+    m, n, tokens = _gemm_shapes([((a_codes, "a_codes"), (a_scales, "a_scales"), (b_codes, "b_codes"), (b_scales, "b_scales"))])
+    _here(offsets, "offsets", cur)
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise Fp4Error("offsets must be a vector of experts + 1 elements")
+    _index(offsets, "offsets", offsets.shape, cur)
+    e = offsets.shape[0] - 1
+    if c is None:
+        if accumulate:
+            raise Fp4Error("accumulate needs an output tensor")
+        if dtype not in _OUTPUT_TYPES:
+            raise Fp4Error(f"c must be bf16 or fp32, not {dtype}")
+        c = torch.empty((e, m, n), dtype=dtype, device=a_codes.device)
+    else:
+        _here(c, "c", cur)
+        if c.dtype not in _OUTPUT_TYPES or c.shape != (e, m, n) or not c.is_contiguous():
+            raise Fp4Error(f"c must be a contiguous bf16 or fp32 tensor of shape {(e, m, n)}")
+    _check(load().fp4_gemm_experts_wgrad(e, tokens, m, n, offsets.data_ptr(), _p(a_codes), _p(a_scales), _p(b_codes),
+                                         _p(b_scales), c.data_ptr(), 1 if c.dtype is torch.float32 else 0,
+                                         1 if accumulate else 0, _raw_stream(cur)))
+    return c
+
+
+def fp4_swiglu_producer_experts(offsets, x_codes, x_scales, w13_codes, w13_scales, sign_mask16=0, emit_cols=True, out=None):
+    """fp4_swiglu_producer on sorted rows, each with its expert's stacked W1 and W3
+    (w13_codes [experts][2f][d/2]): returns (a, b, h_codes, h_scales, ht_codes,
+    ht_scales); `out` may hold them."""
+    cur = _current(x_codes, "x_codes")
+    e, f2, d = _expert_weights(w13_codes, w13_scales, "w13", cur)
+    if f2 % 2:
+        raise Fp4Error("w13_codes must stack W1 and W3: an even number of rows")
+    f = f2 // 2
+    rows = _sorted_codes(offsets, x_codes, x_scales, "x", e, d, cur)
+    dev = x_codes.device
+    o = (None,) * 6 if out is None else tuple(out)
+    a = _out16(o[0], torch.Size((rows, f)), dev, "a")
+    b = _out16(o[1], torch.Size((rows, f)), dev, "b")
+    h_codes, h_scales = _out8(o[2], rows, f // 2, dev, "h_codes"), _out8(o[3], rows, f // 32, dev, "h_scales")
+    ht_codes = ht_scales = None
+    if emit_cols:
+        ht_codes, ht_scales = _out8(o[4], f, rows // 2, dev, "ht_codes"), _out8(o[5], f, rows // 32, dev, "ht_scales")
+    _check(load().fp4_swiglu_producer_experts(e, rows, f, d, offsets.data_ptr(), x_codes.data_ptr(), x_scales.data_ptr(),
+                                              w13_codes.data_ptr(), w13_scales.data_ptr(), a.data_ptr(), b.data_ptr(),
+                                              h_codes.data_ptr(), h_scales.data_ptr(), _p(ht_codes), _p(ht_scales),
+                                              int(sign_mask16), _raw_stream(cur)))
+    return a, b, h_codes, h_scales, ht_codes, ht_scales
+
+
+def _few_sorted_rows(offsets, x, x_scales, experts, k, cur):
+    """Sorted activations of the few-row products: returns (rows, ldx)."""
+    _index(offsets, "offsets", (experts + 1,), cur)
+    if x_scales is None:
+        ldx = _rows2d(x, "x", cur)
+    else:
+        _here(x, "x", cur)
+        if x.dim() != 2:
+            raise Fp4Error("x must be 2-D")
+        _bytes2d(x, "x", cur, x.shape)
+        _bytes2d(x_scales, "x_scales", cur, (x.shape[0], x.shape[1] // 32))
+        ldx = x.shape[1]
+    if x.shape[1] != k:
+        raise Fp4Error(f"the weights have {k} values per row, x {x.shape[1]}")
+    return x.shape[0], ldx
+
+
+def fp4_matvec_experts(offsets, x, w_codes, w_scales, x_scales=None, c=None):
+    """fp4_matvec on sorted rows, each with its expert's weights (w_codes
+    [experts][n][k/2]): C fp32, 0 in rows behind the last segment."""
+    cur = _current(x, "x")
+    e, n, k = _expert_weights(w_codes, w_scales, "w", cur)
+    rows, ldx = _few_sorted_rows(offsets, x, x_scales, e, k, cur)
+    c = _gemm_out(c, rows, n, False, x.device)
+    _check(load().fp4_matvec_experts(e, rows, n, k, offsets.data_ptr(), x.data_ptr(), ldx, _p(x_scales), w_codes.data_ptr(),
+                                     w_scales.data_ptr(), c.data_ptr(), _ldc(c), _raw_stream(cur)))
+    return c
+
+
+def fp4_swiglu_matvec_experts(offsets, x, w13_codes, w13_scales, x_scales=None, h=None):
+    """fp4_swiglu_matvec on sorted rows, each with its expert's stacked W1 and W3
+    (w13_codes [experts][2f][d/2]): h bf16, 0 in rows behind the last segment."""
+    cur = _current(x, "x")
+    e, f2, d = _expert_weights(w13_codes, w13_scales, "w13", cur)
+    if f2 % 2:
+        raise Fp4Error("w13_codes must stack W1 and W3: an even number of rows")
+    rows, ldx = _few_sorted_rows(offsets, x, x_scales, e, d, cur)
+    h = _out16(h, torch.Size((rows, f2 // 2)), x.device, "h")
+    _check(load().fp4_swiglu_matvec_experts(e, rows, f2 // 2, d, offsets.data_ptr(), x.data_ptr(), ldx, _p(x_scales),
+                                            w13_codes.data_ptr(), w13_scales.data_ptr(), h.data_ptr(), _raw_stream(cur)))
     return h
 
 

@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libmxfp4.so"
 SOURCES = ["quantize.hip", "gemm.hip", "swiglu_bwd.hip", "dgrad_swiglu_bwd.hip", "nvfp4.hip", "norm.hip",
-           "matvec.hip"]
+           "matvec.hip", "gemm_act.hip", "gemm_experts.hip", "experts.hip", "act.hip", "matvec_act.hip", "matvec_experts.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -49,7 +49,7 @@ def probe_path(name):
     return os.path.join(TEST_HIP, f"lib{name}.so")
 
 
-def build(verbose=False, jobs=4):
+def build(verbose=False, jobs=8):
     """Compile every source and link the shared library; raises on failure."""
     objs = []
     with tempfile.TemporaryDirectory(prefix="mxfp4_build_") as tmp:

@@ -14,6 +14,8 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool mult32(int64_t v) { return v > 0 && (v % 32) == 0; }
 inline bool mult32z(int64_t v) { return v >= 0 && (v % 32) == 0; }   // zero allowed (empty)
 
+inline bool dtype_ok(fp4_dtype t) { return t == FP4_BF16 || t == FP4_F32; }
+
 inline fp4_status launch_status() {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) {

@@ -1,0 +1,68 @@
+// Block-scaled E2M1 product with bias, activation and residual in its epilogue
+// (fp4_gemm_act), on the fast main loop of the plain product.
+//
+// Method: "Format-Aware Fusion for Fast FP4 Pretraining", §2.3 (Eq. 4) for the
+// product, §3.1 (a boundary leaves its consumer's operands without a round
+// trip) for the epilogue.
+#include <hip/hip_runtime.h>
+
+#include "abi_common.h"
+#include "gemm_core.h"
+#include "gemm_epilogue.h"
+
+namespace mx {
+
+template <int kMode>
+__global__ __launch_bounds__(kFastThreads) void gemm_act_kernel(int64_t M, int64_t N, int64_t K,
+                                                                const uint8_t* __restrict__ a_codes,
+                                                                const uint8_t* __restrict__ a_scales,
+                                                                const uint8_t* __restrict__ b_codes,
+                                                                const uint8_t* __restrict__ b_scales, Epilogue e) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kSmemBytes];
+  int64_t tm, tn;
+  tile_coords((M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
+  const int64_t m0 = tm * BM, n0 = tn * BN;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wm = wave >> 2, wn = wave & 3, hl = lane >> 5;
+  const Operand A{a_codes, a_scales, M}, B{b_codes, b_scales, N};
+  v16f acc[4][2];
+  if (kMode == kShort && K == 0) zero_tile(acc);          // z = bias
+  else main_loop_fast<false, kMode>(smem, A, B, m0, n0, 0, K, acc, wm, wn, nullptr, nullptr, k_range(0, (int)(K >> 5)));
+  store_epilogue(smem, acc, e, M, N, m0, n0, wave, lane, wm, wn, hl);
+}
+
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" {
+
+fp4_status fp4_gemm_act(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes, const uint8_t* a_scales,
+                        const uint8_t* b_codes, const uint8_t* b_scales, const void* bias, fp4_dtype bias_type,
+                        fp4_act act, const uint16_t* residual, int64_t ldr, uint16_t* z, void* y, fp4_dtype y_type,
+                        int64_t ldy, hipStream_t stream) {
+  if (!dtype_ok(bias_type) || !dtype_ok(y_type) || act < FP4_ACT_NONE || act > FP4_ACT_SILU) return FP4_EINVAL;
+  if (m < 0 || !mult32z(n) || !mult32z(k) || k >= ((int64_t)1 << 24) || ldy < n || (residual && ldr < n)) return FP4_ESHAPE;
+  if (m == 0 || n == 0) return FP4_OK;
+  if (!y || (k > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return FP4_EINVAL;
+  const int64_t tiles = tiles_of(m, BM, n, BN);
+  if (tiles < 0) return FP4_ESHAPE;
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(residual) ||
+      !aligned16(z) || !aligned16(y) || (residual && ldr % 8 != 0) || ldy % (y_type == FP4_F32 ? 4 : 8) != 0 ||
+      (reinterpret_cast<uintptr_t>(bias) & (bias_type == FP4_F32 ? 3 : 1)))
+    return FP4_EALIGN;
+  const bool f32 = y_type == FP4_F32;
+  const Epilogue e{y, ldy, bias, residual, ldr, z, (int)act, f32, bias_type == FP4_F32, 0,
+                   streams(m * n * ((f32 ? 4 : 2) + (z ? 2 : 0)))};
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(kFastThreads), 0, as_stream(stream), m, n, k, a_codes,
+                       a_scales, b_codes, b_scales, e);
+  };
+  const int mode = k_mode(k);
+  if (mode == kWhole) go(gemm_act_kernel<kWhole>);
+  else if (mode == kWindow) go(gemm_act_kernel<kWindow>);
+  else go(gemm_act_kernel<kShort>);
+  return launch_status();
+}
+
+}  // extern "C"

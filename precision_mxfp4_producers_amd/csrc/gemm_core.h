@@ -288,6 +288,28 @@ static_assert(kLdsSB + 2 * BN * 8 == kSmemBytes, "fast path LDS layout");
 // s_waitcnt immediate (gfx9 encoding: vmcnt[3:0]+[15:14], expcnt[6:4], lgkmcnt[11:8])
 constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 0xF) | ((vm >> 4) << 14) | 0x70 | ((lgkm & 0xF) << 8); }
 
+// K ranges the fast loop walks beside whole K steps from the operands' first
+// column (kWhole):
+//   kWindow  the 32-value blocks lo .. lo + count - 1 of the operands' rows, in
+//            K steps from `first` on (lo lies in the first): lanes whose
+//            16-byte code chunk, one block, lies outside read zero codes,
+//            whose products are zero under any finite scale.  K (the row
+//            length) is at least 256.
+//   kShort   the same for rows of less than 256 values (one K step), whose
+//            scale bytes come one by one.
+// A K step's eight scale bytes come with one load that stays inside the row:
+// in the last, partial step it is moved back to end with the row and the bytes
+// are shifted into place.
+constexpr int kWhole = 0, kWindow = 1, kShort = 2;
+struct KRange {
+  int first, steps;                    // K steps
+  int lo, count;                       // 32-value blocks
+};
+// Blocks lo .. hi - 1 of a row.
+__host__ __device__ __forceinline__ KRange k_range(int lo, int hi) {
+  return KRange{lo >> 3, hi > lo ? ((hi + 7) >> 3) - (lo >> 3) : 0, lo, hi - lo};
+}
+
 struct FastPlan {
   __amdgpu_buffer_rsrc_t ra, rb, rs;   // A codes, this wave's B codes, this wave's scales
   __amdgpu_buffer_rsrc_t ra2, rb2, rs2;  // the same for the second operand pair (K steps nk1 ..)
@@ -297,6 +319,8 @@ struct FastPlan {
   uint32_t ldb8;                       // 8 code rows (bytes)
   uint32_t wa0, wa1;                   // lane LDS offsets (even / odd j) of its code chunk
   uint32_t ws;                         // lane LDS offset of its scale row (stage 0)
+  KRange kr;                           // kWindow, kShort
+  int row_scales;                      // scale bytes of a row (kWindow, kShort)
 };
 
 // Wave w loads code rows 32w..32w+31 of both tiles (load j: rows 32w + 8j +
@@ -396,30 +420,71 @@ struct PartB {
   uint2 s;
 };
 
+// The lane's code offset in K step kit, or one past any operand where its
+// block lies outside the K range.
+template <int kMode>
+__device__ __forceinline__ uint32_t code_offset(const FastPlan& p, uint32_t v, int kit) {
+  if constexpr (kMode == kWhole) return v;
+  const int block = 8 * kit + (int)(threadIdx.x & 7);
+  return (uint32_t)(block - p.kr.lo) < (uint32_t)p.kr.count ? v : kOffNone;
+}
+
+// The eight scale bytes of K step kit of the lane's scale row.
+template <int kMode>
+__device__ __forceinline__ uint2 load_scales(const FastPlan& p, __amdgpu_buffer_rsrc_t rs, int kit) {
+  if constexpr (kMode == kShort) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      w[q >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, q < p.row_scales ? p.vs + (uint32_t)q : kOffNone, 0, 0)
+                   << (8 * (q & 3));
+    return make_uint2(w[0], w[1]);
+  } else {
+    const int at = kMode == kWindow ? min(8 * kit, p.row_scales - 8) : 8 * kit;
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rs, p.vs, (uint32_t)at, 0));
+  }
+}
+
+// Those bytes in place: a load that was moved back is shifted.
+template <int kMode>
+__device__ __forceinline__ uint2 placed_scales(const FastPlan& p, uint2 s, int kit) {
+  if constexpr (kMode != kWindow) return s;
+  const int moved = max(8 * kit - (p.row_scales - 8), 0);
+  return __builtin_bit_cast(uint2, __builtin_bit_cast(uint64_t, s) >> (8 * moved));
+}
+
 // Load j of a part reads 8 rows further down.  The row offset stays in the
 // lane offset: the buffer range check (rows past the operand read zero) covers
 // the lane offset, not the scalar one, which carries only the K position.
 // K step `kit` of the concatenated K range: steps from nk1 on come from the
 // second operand pair (a wave-uniform choice of buffer resources).
-__device__ __forceinline__ void load_part_a(const FastPlan& p, int kit, PartA& x) {
-  const bool second = kit >= p.nk1;
-  const __amdgpu_buffer_rsrc_t ra = second ? p.ra2 : p.ra;
-  const uint32_t so = (uint32_t)(second ? kit - p.nk1 : kit) * BKB;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    x.a[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, p.va + (uint32_t)j * p.ldb8, so, 0));
+// With a K range, steps count from its first one.
+template <int kMode>
+__device__ __forceinline__ int operand_step(const FastPlan& p, int kit) {
+  return (kMode == kWhole ? 0 : p.kr.first) + (kit >= p.nk1 ? kit - p.nk1 : kit);
 }
 
+template <int kMode>
+__device__ __forceinline__ void load_part_a(const FastPlan& p, int kit, PartA& x) {
+  const __amdgpu_buffer_rsrc_t ra = kit >= p.nk1 ? p.ra2 : p.ra;
+  const int k1 = operand_step<kMode>(p, kit);
+  const uint32_t so = (uint32_t)k1 * BKB, v = code_offset<kMode>(p, p.va, k1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    x.a[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, v + (uint32_t)j * p.ldb8, so, 0));
+}
+
+template <int kMode>
 __device__ __forceinline__ void load_part_b(const FastPlan& p, int kit, PartB& x) {
   const bool second = kit >= p.nk1;
   const __amdgpu_buffer_rsrc_t rb = second ? p.rb2 : p.rb;
   const __amdgpu_buffer_rsrc_t rs = second ? p.rs2 : p.rs;
-  const int k1 = second ? kit - p.nk1 : kit;
-  const uint32_t so = (uint32_t)k1 * BKB, sso = (uint32_t)k1 * 8u;
+  const int k1 = operand_step<kMode>(p, kit);
+  const uint32_t so = (uint32_t)k1 * BKB, v = code_offset<kMode>(p, p.vb, k1);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    x.b[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, p.vb + (uint32_t)j * p.ldb8, so, 0));
-  x.s = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rs, p.vs, sso, 0));
+    x.b[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, v + (uint32_t)j * p.ldb8, so, 0));
+  x.s = load_scales<kMode>(p, rs, k1);
 }
 
 // Stage `stg` (0 or 1, wave-uniform) of the part: 32 KB per code stage, 2 KB
@@ -431,12 +496,14 @@ __device__ __forceinline__ void write_part_a(uint8_t* smem, const FastPlan& p, u
   for (int j = 0; j < 4; ++j) *reinterpret_cast<v4i*>(((j & 1) ? b1 : b0) + (kLdsA + j * 1024)) = x.a[j];
 }
 
-__device__ __forceinline__ void write_part_b(uint8_t* smem, const FastPlan& p, uint32_t stg, const PartB& x) {
+// `kit`: the step that x was loaded for.
+template <int kMode>
+__device__ __forceinline__ void write_part_b(uint8_t* smem, const FastPlan& p, uint32_t stg, int kit, const PartB& x) {
   uint8_t* b0 = smem + (p.wa0 + (stg << 15));
   uint8_t* b1 = smem + (p.wa1 + (stg << 15));
 #pragma unroll
   for (int j = 0; j < 4; ++j) *reinterpret_cast<v4i*>(((j & 1) ? b1 : b0) + (kLdsB + j * 1024)) = x.b[j];
-  *reinterpret_cast<uint2*>(smem + (p.ws + (stg << 11))) = x.s;
+  *reinterpret_cast<uint2*>(smem + (p.ws + (stg << 11))) = placed_scales<kMode>(p, x.s, operand_step<kMode>(p, kit));
 }
 
 // Fragment addresses without per-sub-step registers: the chunk swizzle only
@@ -503,11 +570,11 @@ __device__ __forceinline__ void pp_compute(const Frags8& f0, const Frags8& f1, c
 }
 
 // Memory work of a phase: fragments of half H of stage `frs` (for H = 0 also
-// the stage's scale dwords), one part written to stage `wst`, the same part of
-// K step `lkit` loaded.
-template <bool kSwiGLU, int H, bool kPartA, bool kSync>
+// the stage's scale dwords), one part (of K step `wkit`) written to stage
+// `wst`, the same part of K step `lkit` loaded.
+template <bool kSwiGLU, int H, bool kPartA, bool kSync, int kMode>
 __device__ __forceinline__ void pp_memory(uint8_t* smem, const FastPlan& p, const PPAddr& q, uint32_t frs,
-                                          uint32_t wst, int lkit, Frags8& f0, Frags8& f1, uint32_t (&sa)[4],
+                                          uint32_t wst, int wkit, int lkit, Frags8& f0, Frags8& f1, uint32_t (&sa)[4],
                                           uint32_t (&sb)[2], PartA& xa, PartB& xb) {
   pp_read_frags<kSwiGLU, 2 * H>(smem, q, frs, f0);
   pp_read_frags<kSwiGLU, 2 * H + 1>(smem, q, frs, f1);
@@ -515,20 +582,23 @@ __device__ __forceinline__ void pp_memory(uint8_t* smem, const FastPlan& p, cons
   // the part's registers are written out before they are loaded again: kept
   // in this order, one set of staging registers per part suffices
   if constexpr (kPartA) write_part_a(smem, p, wst, xa);
-  else write_part_b(smem, p, wst, xb);
+  else write_part_b<kMode>(smem, p, wst, wkit, xb);
   __builtin_amdgcn_sched_barrier(0);
-  if constexpr (kPartA) load_part_a(p, lkit, xa);
-  else load_part_b(p, lkit, xb);
+  if constexpr (kPartA) load_part_a<kMode>(p, lkit, xa);
+  else load_part_b<kMode>(p, lkit, xb);
   if constexpr (kSync) pp_sync();
   else pp_next();
 }
 
 // With A2/B2 (plain GEMM only) the loop runs over K of (A, B) and then K of
 // (A2, B2) into the same accumulators: one fp32 sum over the concatenated K.
-template <bool kSwiGLU>
+// kMode kWindow or kShort: the loop walks K range `kr` (at least one step) of
+// the rows, which are K long.
+template <bool kSwiGLU, int kMode = kWhole>
 __device__ __forceinline__ void main_loop_fast(uint8_t* smem, const Operand& A, const Operand& B, int64_t m0,
                                                int64_t n0, int64_t f, int64_t K, v16f (&acc)[4][2], int wm, int wn,
-                                               const Operand* A2 = nullptr, const Operand* B2 = nullptr) {
+                                               const Operand* A2 = nullptr, const Operand* B2 = nullptr,
+                                               const KRange& kr = KRange{}) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -536,9 +606,15 @@ __device__ __forceinline__ void main_loop_fast(uint8_t* smem, const Operand& A, 
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
-  const int nk = (int)(K / 256) * ((A2 != nullptr && A2->codes != nullptr) ? 2 : 1), last = nk - 1;
+  const bool pair = A2 != nullptr && A2->codes != nullptr;
+  const int nk = (kMode == kWhole ? (int)(K / 256) : kr.steps) * (pair ? 2 : 1), last = nk - 1;
   FastPlan p;
   make_fast_plan<kSwiGLU>(p, A, B, m0, n0, f, K, A2, B2);
+  if constexpr (kMode != kWhole) {
+    p.kr = kr;
+    p.row_scales = (int)(K >> 5);
+    if (pair) p.nk1 = kr.steps;
+  }
   PPAddr q;
   make_pp_addr<kSwiGLU>(q, wm, wn, r, h);
   PartA xa;
@@ -546,19 +622,19 @@ __device__ __forceinline__ void main_loop_fast(uint8_t* smem, const Operand& A, 
   Frags8 f0, f1;
   uint32_t sa[4], sb[2];
   // every wave: stage 0 whole, then its stage-1 parts in registers
-  load_part_a(p, 0, xa);
-  load_part_b(p, 0, xb);
+  load_part_a<kMode>(p, 0, xa);
+  load_part_b<kMode>(p, 0, xb);
   write_part_a(smem, p, 0u, xa);
-  write_part_b(smem, p, 0u, xb);
+  write_part_b<kMode>(smem, p, 0u, 0, xb);
   __builtin_amdgcn_sched_barrier(0);
-  load_part_a(p, min(1, last), xa);
-  load_part_b(p, min(1, last), xb);
+  load_part_a<kMode>(p, min(1, last), xa);
+  load_part_b<kMode>(p, min(1, last), xb);
   if (__builtin_amdgcn_readfirstlane(wm) == 0) {
     // group 0 writes its A part of stage 1 now (its phase 4s-1 for s = 0),
     // loads A of stage 2, and reads its first fragments after the barrier
     write_part_a(smem, p, 1u, xa);
     __builtin_amdgcn_sched_barrier(0);
-    load_part_a(p, min(2, last), xa);
+    load_part_a<kMode>(p, min(2, last), xa);
     pp_sync();
     pp_read_frags<kSwiGLU, 0>(smem, q, 0u, f0);
     pp_read_frags<kSwiGLU, 1>(smem, q, 0u, f1);
@@ -566,17 +642,17 @@ __device__ __forceinline__ void main_loop_fast(uint8_t* smem, const Operand& A, 
     for (int s = 0; s < nk; ++s) {
       const uint32_t cur = (uint32_t)(s & 1), nxt = cur ^ 1u;
       pp_compute<0, false>(f0, f1, sa, sb, acc);
-      pp_memory<kSwiGLU, 1, false, false>(smem, p, q, cur, nxt, min(s + 2, last), f0, f1, sa, sb, xa, xb);
+      pp_memory<kSwiGLU, 1, false, false, kMode>(smem, p, q, cur, nxt, min(s + 1, last), min(s + 2, last), f0, f1, sa, sb, xa, xb);
       pp_compute<1, true>(f0, f1, sa, sb, acc);
-      pp_memory<kSwiGLU, 0, true, false>(smem, p, q, nxt, cur, min(s + 3, last), f0, f1, sa, sb, xa, xb);
+      pp_memory<kSwiGLU, 0, true, false, kMode>(smem, p, q, nxt, cur, min(s + 2, last), min(s + 3, last), f0, f1, sa, sb, xa, xb);
     }
   } else {
     pp_sync();
     for (int s = 0; s < nk; ++s) {
       const uint32_t cur = (uint32_t)(s & 1), nxt = cur ^ 1u;
-      pp_memory<kSwiGLU, 0, true, false>(smem, p, q, cur, nxt, min(s + 2, last), f0, f1, sa, sb, xa, xb);
+      pp_memory<kSwiGLU, 0, true, false, kMode>(smem, p, q, cur, nxt, min(s + 1, last), min(s + 2, last), f0, f1, sa, sb, xa, xb);
       pp_compute<0, false>(f0, f1, sa, sb, acc);
-      pp_memory<kSwiGLU, 1, false, true>(smem, p, q, cur, nxt, min(s + 2, last), f0, f1, sa, sb, xa, xb);
+      pp_memory<kSwiGLU, 1, false, true, kMode>(smem, p, q, cur, nxt, min(s + 1, last), min(s + 2, last), f0, f1, sa, sb, xa, xb);
       pp_compute<1, false>(f0, f1, sa, sb, acc);
     }
   }

@@ -592,6 +592,6 @@ uint32_t fp4_sign_mask_from_seed(uint64_t seed) {
 
 int fp4_last_hip_error(void) { return g_last_hip_error; }
 
-int fp4_abi_version(void) { return (1 << 16) | 5; }
+int fp4_abi_version(void) { return (1 << 16) | 6; }
 
 }  // extern "C"

@@ -1,0 +1,228 @@
+"""GPU checks of the experts' products against float64 within the GEMM bound 1e-5
+sum |a b|, and of the gated producer byte for byte against the plain one expert
+by expert."""
+
+import numpy as np
+import pytest
+import torch
+
+import synthetic
+from oracle import experts as X
+from oracle import formats as F
+from oracle import gemm as G
+from oracle import norm as N
+from oracle import quant as Q
+
+pytestmark = pytest.mark.gpu
+H = 2.0 ** -8                                            # half a bf16 step
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.float().cpu().numpy() if t.dtype is torch.bfloat16 else t.cpu().numpy()
+
+
+def codes(shape, seed):
+    """Random codes (every nibble) and scale bytes of [..., k] values."""
+    rng = np.random.default_rng(seed)
+    *lead, k = shape
+    return rng.integers(0, 256, (*lead, k // 2), dtype=np.uint8), rng.integers(116, 126, (*lead, k // 32), dtype=np.uint8)
+
+
+def segments(sizes, align, rows=None):
+    """(offsets, rows of the buffers) of experts with so many tokens."""
+    padded = [-(-s // align) * align for s in sizes]
+    offsets = np.concatenate(([0], np.cumsum(padded))).astype(np.int32)
+    return offsets, int(offsets[-1]) if rows is None else rows
+
+
+def check(got, ref, e, k, f32=True):
+    got = host(got)
+    if f32:
+        ok = G.within_bound(got, ref, e, k=k)
+    else:                                                # the fp32 value rounded once
+        tol = 1e-5 * e + k * 2.0 ** -150
+        ok = np.abs(got - ref) <= tol + H * (np.abs(ref) + tol)
+    assert ok.all(), f"{(~ok).sum()} outside the bound, first {np.argwhere(~ok)[0]}"
+
+
+ROWS = [((1,), 32, 32), ((0, 3), 64, 64), ((5, 0, 1, 40), 32, 96), ((64, 32, 0, 0, 300), 96, 160), ((256, 257, 255), 256, 224),
+        ((33, 1), 288, 256), ((100, 200, 300), 512, 288), ((7,) * 70, 64, 512), ((0,) * 65 + (9,), 320, 1056),
+        ((513, 0, 700), 544, 768), ((3, 2000), 256, 4096), ((0, 0, 0), 64, 64)]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("align,extra", [(1, 0), (1, 5), (32, 0), (32, 301)])
+@pytest.mark.parametrize("sizes,n,k", ROWS)
+def test_rows(gpu_lib, sizes, n, k, align, extra, f32):
+    offsets, rows = segments(sizes, align)
+    rows += extra
+    a, b = codes((rows, k), 1), codes((len(sizes), n, k), 2)
+    a2, b2 = codes((rows, k), 3), codes((len(sizes), n, k), 4)
+    dtype = torch.float32 if f32 else torch.bfloat16
+    ref, e = np.zeros((2, rows, n))
+    ref2, e2 = np.zeros((2, rows, n))
+    for i in range(len(sizes)):
+        at = slice(offsets[i], offsets[i + 1])
+        ref[at], e[at] = G.gemm_ref(a[0][at], a[1][at], b[0][i], b[1][i])
+        ref2[at], e2[at] = G.gemm_ref(a2[0][at], a2[1][at], b2[0][i], b2[1][i])
+    args = [dev(offsets), *map(dev, a), *map(dev, b)]
+    c = torch.full((rows, n + 8), 7.0, dtype=dtype, device="cuda")
+    out = gpu_lib.fp4_gemm_experts(*args, c=c[:, :n])
+    check(out, ref, e, k, f32)
+    assert (host(c)[:, n:] == 7).all() and (host(c)[offsets[-1]:, :n] == 0).all()
+    check(gpu_lib.fp4_gemm_experts(*args, dtype=dtype, pair=[*map(dev, a2), *map(dev, b2)]), ref + ref2, e + e2, 2 * k, f32)
+
+
+@pytest.mark.parametrize("sizes,n,k", [((64, 32, 96), 96, 256), ((300, 20), 288, 1024), ((33,), 256, 288)])
+def test_rows_are_those_of_the_plain_product(gpu_lib, sizes, n, k):
+    """One expert's rows by fp4_gemm: the same sums in the same order where K is whole steps, the same bound elsewhere."""
+    offsets, rows = segments(sizes, 32)
+    a, b = codes((rows, k), 1), codes((len(sizes), n, k), 2)
+    got = gpu_lib.fp4_gemm_experts(dev(offsets), *map(dev, a), *map(dev, b))
+    for i in range(len(sizes)):
+        at = slice(offsets[i], offsets[i + 1])
+        want = gpu_lib.fp4_gemm(dev(a[0][at]), dev(a[1][at]), dev(b[0][i]), dev(b[1][i]))
+        if k % 256 == 0:
+            assert torch.equal(got[at], want)
+        else:
+            _, e = G.gemm_ref(a[0][at], a[1][at], b[0][i], b[1][i])
+            assert (np.abs(host(got[at]) - host(want)) <= 2e-5 * e).all()
+
+
+def test_segments_that_are_not_ascending_stay_inside(gpu_lib):
+    """Nothing is promised of their values, but that no other memory is touched:
+    the columns beside C and the rows behind it keep what they hold."""
+    a, b = codes((64, 64), 1), codes((4, 32, 64), 2)
+    x = torch.randn(64, 64, device="cuda").bfloat16()
+    for bad in ([0, 40, 20, 70, 90], [-5, 10, 1000, 20, 64], [2 ** 31 - 1] * 5, [-2 ** 31] * 5, [64, 0, 0, 0, 0]):
+        offsets = dev(np.array(bad, np.int32))
+        c = torch.full((80, 40), 7.0, device="cuda")
+        gpu_lib.fp4_gemm_experts(offsets, *map(dev, a), *map(dev, b), c=c[:64, :32])
+        assert (c[64:] == 7).all() and (c[:, 32:] == 7).all()
+        c = torch.full((80, 40), 7.0, device="cuda")
+        gpu_lib.fp4_matvec_experts(offsets, x, *map(dev, b), c=c[:64, :32])
+        assert (c[64:] == 7).all() and (c[:, 32:] == 7).all()
+
+
+WGRAD = [((1,), 32, 32), ((0, 5, 0, 64), 64, 96), ((256, 300, 31, 0, 700), 96, 288), ((33,) * 9, 288, 64), ((2000, 1), 256, 256),
+         ((7, 8, 9, 250), 544, 320), ((0,) * 66 + (40,), 32, 64), ((0, 0), 64, 32)]
+
+
+@pytest.mark.parametrize("align,extra", [(32, 0), (32, 256), (256, 0)])
+@pytest.mark.parametrize("sizes,m,n", WGRAD)
+def test_wgrad(gpu_lib, sizes, m, n, align, extra):
+    offsets, rows = segments(sizes, align)
+    tokens = -(-rows // 256) * 256 + extra
+    a, b = codes((m, tokens), 1), codes((n, tokens), 2)
+    A, B = F.decode(*a), F.decode(*b)
+    ref, e = np.zeros((2, len(sizes), m, n))
+    for i in range(len(sizes)):
+        at = slice(offsets[i], offsets[i + 1])
+        ref[i], e[i] = A[:, at] @ B[:, at].T, abs(A[:, at]) @ abs(B[:, at]).T
+    args = [dev(offsets), *map(dev, a), *map(dev, b)]
+    check(gpu_lib.fp4_gemm_experts_wgrad(*args), ref, e, tokens)
+    check(gpu_lib.fp4_gemm_experts_wgrad(*args, dtype=torch.bfloat16), ref, e, tokens, f32=False)
+    prev = np.random.default_rng(5).normal(size=ref.shape).astype(np.float32)
+    c = dev(prev)
+    assert gpu_lib.fp4_gemm_experts_wgrad(*args, c=c, accumulate=True) is c
+    assert G.within_bound(host(c), ref, e, c_prev=prev).all()
+    assert all(np.array_equal(host(c)[i], prev[i]) for i in range(len(sizes)) if sizes[i] == 0)
+
+
+SWIGLU = [((32,), 32, 32), ((5, 0, 70, 300), 64, 96), ((256, 257), 96, 256), ((33, 1, 0), 160, 288), ((40,) * 67, 32, 64),
+          ((600, 8), 288, 512), ((0, 0), 64, 64)]
+
+
+@pytest.mark.parametrize("extra", [0, 32, 320])
+@pytest.mark.parametrize("sizes,f,d", SWIGLU)
+def test_swiglu_producer(gpu_lib, sizes, f, d, extra):
+    """Each expert's rows byte for byte as fp4_swiglu_producer gives them; zeros behind."""
+    offsets, rows = segments(sizes, 32)
+    rows += extra
+    if rows == 0:
+        return
+    xq, mask = codes((rows, d), 1), gpu_lib.fp4_sign_mask_from_seed(3)
+    w = [Q.quantize_w2d32(synthetic.tensor((2 * f, d), std=0.05, seed=10 + i), 0.87)[:2] for i in range(len(sizes))]
+    wc, ws = np.stack([c for c, _ in w]), np.stack([s for _, s in w])
+    out = [torch.full(s, 9, dtype=t, device="cuda") for s, t in (((rows, f), torch.bfloat16), ((rows, f), torch.bfloat16),
+           ((rows, f // 2), torch.uint8), ((rows, f // 32), torch.uint8), ((f, rows // 2), torch.uint8), ((f, rows // 32), torch.uint8))]
+    got = gpu_lib.fp4_swiglu_producer_experts(dev(offsets), *map(dev, xq), dev(wc), dev(ws), mask, out=out)
+    some = gpu_lib.fp4_swiglu_producer_experts(dev(offsets), *map(dev, xq), dev(wc), dev(ws), mask, emit_cols=False)
+    assert some[4] is None and all(torch.equal(g, s) for g, s in zip(got[:4], some[:4]))
+    bits = [host(t.view(torch.int16)) if t.dtype is torch.bfloat16 else host(t) for t in got]
+    whole = d % 256 == 0
+    for i in range(len(sizes)):
+        lo, hi = offsets[i], offsets[i + 1]
+        if lo == hi:
+            continue
+        want = [host(t) for t in gpu_lib.fp4_swiglu_producer(dev(xq[0][lo:hi]), dev(xq[1][lo:hi]), dev(wc[i]), dev(ws[i]), mask)]
+        mine = [b[lo:hi] for b in bits[:4]] + [bits[4][:, lo // 2:hi // 2], bits[5][:, lo // 32:hi // 32]]
+        if whole:
+            assert all(np.array_equal(m, v) for m, v in zip(mine, want)), i
+        else:                                            # another main loop: a and b within a bf16 step, h from them
+            for m, v in zip(mine[:2], want[:2]):
+                m64, v64 = F.bf16_bits_to_f64(m.view(np.uint16)), F.bf16_bits_to_f64(v.view(np.uint16))
+                assert (np.abs(m64 - v64) <= 2 * H * np.abs(v64) + 1e-4).all()
+            hq = [F.decode(m[2], m[3]) for m in (mine, want)]
+            assert np.linalg.norm(hq[0] - hq[1]) <= 0.02 * np.linalg.norm(hq[1])
+    tail = [b[offsets[-1]:] for b in bits[:4]] + [bits[4][:, offsets[-1] // 2:] & 0x77, bits[5][:, offsets[-1] // 32:]]
+    assert all((b == 0).all() for b in tail)
+
+
+FEW = [((1,), 16, 32), ((0, 2), 17, 64), ((1, 0, 0, 1), 33, 96), ((16, 17, 33), 48, 128), ((3,) * 70, 20, 160), ((15, 1), 512, 1024),
+       ((40, 0, 5), 100, 2080), ((2, 2), 4100, 512), ((9, 64), 256, 4096), ((1, 1), 64, 14336), ((5, 20), 40, 8192), ((0, 0), 8, 64)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("align,extra", [(1, 0), (1, 3), (32, 0)])
+@pytest.mark.parametrize("sizes,n,k", FEW)
+def test_few(gpu_lib, sizes, n, k, align, extra, kind):
+    offsets, rows = segments(sizes, align)
+    rows += extra
+    if rows == 0:
+        return
+    bits = synthetic.tensor((rows, k), seed=k, outlier_rate=0.002, outlier_scale=20.0)
+    if kind == "bf16":
+        x64, scales = F.bf16_bits_to_f64(bits), None
+        x = torch.zeros((rows, k + 8), dtype=torch.bfloat16, device="cuda")[:, :k]
+        x.copy_(dev(bits.view(np.int16)).view(torch.bfloat16))
+    else:
+        c, s = N.encode_e4m3(bits)
+        x64, x, scales = N.decode_e4m3(c, s), dev(c), dev(s)
+    w = codes((len(sizes), n, k), 2)
+    ref, e = np.zeros((2, rows, n))
+    for i in range(len(sizes)):
+        at, wi = slice(offsets[i], offsets[i + 1]), F.decode(w[0][i], w[1][i])
+        ref[at], e[at] = x64[at] @ wi.T, abs(x64[at]) @ abs(wi).T
+    out = torch.full((rows, n + 3), 7.0, device="cuda")
+    got = gpu_lib.fp4_matvec_experts(dev(offsets), x, *map(dev, w), x_scales=scales, c=out[:, :n])
+    check(got, ref, e, k)
+    assert (host(out)[:, n:] == 7).all() and (host(got)[offsets[-1]:] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("sizes,f,d", [((1,), 8, 32), ((0, 2, 1), 17, 96), ((16, 17, 33), 48, 128), ((2, 2), 1500, 4096), ((20, 3), 40, 8192),
+                                       ((3,) * 66, 24, 544)])
+def test_few_gated_rows_are_those_of_the_plain_call(gpu_lib, sizes, f, d, kind):
+    """h of each row against fp4_swiglu_matvec on it: another split of the fp32
+    sums may move a, b and h by a rounding."""
+    offsets, rows = segments(sizes, 1)
+    rows += 2
+    bits = synthetic.tensor((rows, d), seed=d)
+    x, scales = dev(bits.view(np.int16)).view(torch.bfloat16), None
+    if kind == "e4m3":
+        x, scales = map(dev, N.encode_e4m3(bits))
+    w = [dev(t) for t in codes((len(sizes), 2 * f, d), 2)]
+    got = gpu_lib.fp4_swiglu_matvec_experts(dev(offsets), x, *w, x_scales=scales)
+    assert (host(got)[offsets[-1]:] == 0).all()
+    for i in range(len(sizes)):
+        for lo in range(offsets[i], offsets[i + 1], 64):
+            at = slice(lo, min(lo + 64, offsets[i + 1]))
+            want = host(gpu_lib.fp4_swiglu_matvec(x[at], w[0][i], w[1][i], x_scales=None if scales is None else scales[at]))
+            # a's rounding moves h by at most 1.1 |a|-relative steps, b's and h's own by one each
+            assert (np.abs(host(got[at]) - want) <= 4 * 2 * H * np.abs(want) + 1e-6).all()
