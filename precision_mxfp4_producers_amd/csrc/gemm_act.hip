@@ -28,7 +28,7 @@ __global__ __launch_bounds__(kFastThreads) void gemm_act_kernel(int64_t M, int64
   v16f acc[4][2];
   if (kMode == kShort && K == 0) zero_tile(acc);          // z = bias
   else main_loop_fast<false, kMode>(smem, A, B, m0, n0, 0, K, acc, wm, wn, nullptr, nullptr, k_range(0, (int)(K >> 5)));
-  store_epilogue(smem, acc, e, M, N, m0, n0, wave, lane, wm, wn, hl);
+  store_epilogue<false>(smem, acc, e, M, N, m0, n0, wave, lane, wm, wn, hl);
 }
 
 }  // namespace mx
