@@ -725,16 +725,22 @@ fp4_status fp4_expert_sort(int64_t t, int64_t k, int64_t experts, const void* id
  *   xs    [rows][d] bf16, or NULL
  *   codes [rows][d/2] (E2M1) or [rows][d] (E4M3), scales [rows][d/32]; both or
  *         neither NULL
+ *   workspace fp4_expert_gather_workspace(t, k, d, rows) bytes, 4-byte aligned, in
+ *             use until the call's work on the stream is done; holds anything
  * The gradient of x is fp4_expert_combine of the gradient of xs without weights.
  * Errors: FP4_EINVAL bad format, exactly one of codes, scales NULL, or another
- * null pointer; FP4_ESHAPE a negative size, k below 1, t, k or d above 2^30, d
- * not a multiple of 32, ldx below d, or rows above 2^30 + 2^18; FP4_EALIGN x, xs
- * or codes not 16-byte aligned, slots not 4-byte aligned, or ldx not a multiple
- * of 8.
+ * null pointer; FP4_ESHAPE a negative size, k below 1, t k or d above 2^30, d
+ * not a multiple of 32, ldx below d, rows above 2^30 + 2^18, or a workspace below
+ * its size; FP4_EALIGN x, xs or codes not 16-byte aligned, slots or the workspace
+ * not 4-byte aligned, or ldx not a multiple of 8.
  */
 fp4_status fp4_expert_gather(int64_t t, int64_t k, int64_t d, int64_t rows, const uint16_t* x, int64_t ldx,
                              const int32_t* slots, uint16_t* xs, fp4_format format, uint8_t* codes, uint8_t* scales,
-                             hipStream_t stream);
+                             void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of the workspace above (0 where the rows are few); -1 for a shape that
+ * the call refuses.  Host-only. */
+int64_t fp4_expert_gather_workspace(int64_t t, int64_t k, int64_t d, int64_t rows);
 
 /*
  * The experts' results back at their tokens:

@@ -58,7 +58,8 @@ _SIGS = {
     "fp4_expert_capacity": [_i64, _i64, _i64, _i64],
     "fp4_expert_sort_workspace": [_i64, _i64, _i64],
     "fp4_expert_sort": [_i64, _i64, _i64, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp],
-    "fp4_expert_gather": [_i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _int, _vp, _vp, _vp],
+    "fp4_expert_gather": [_i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _int, _vp, _vp, _vp, _i64, _vp],
+    "fp4_expert_gather_workspace": [_i64, _i64, _i64, _i64],
     "fp4_expert_combine": [_i64, _i64, _i64, _i64, _vp, _int, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp],
     "fp4_expert_combine_backward": [_i64, _i64, _i64, _i64, _vp, _int, _i64, _vp, _int, _i64] + [_vp] * 6,
     "fp4_gemm_experts": [_i64, _i64, _i64, _i64] + [_vp] * 10 + [_int, _i64, _vp],
@@ -72,7 +73,7 @@ _SIGS = {
 }
 _RESTYPES = {"fp4_sign_mask_from_seed": _u32}
 _RESTYPES |= {name: _i64 for name in ("fp4_rmsnorm_backward_workspace", "fp4_act_backward_workspace", "fp4_expert_capacity",
-                                      "fp4_expert_sort_workspace")}
+                                      "fp4_expert_sort_workspace", "fp4_expert_gather_workspace")}
 EXPORTS = tuple(_SIGS)
 
 
@@ -831,8 +832,11 @@ def fp4_expert_gather(x, slots, k, fmt=FP4_E2M1, emit_x=True, emit_codes=True, o
     if emit_codes:
         codes = _out8(o_codes, rows, d // 2 if fmt == FP4_E2M1 else d, x.device, "codes")
         scales = _out8(o_scales, rows, d // 32, x.device, "scales")
-    _check(load().fp4_expert_gather(t, int(k), d, rows, x.data_ptr(), ldx, slots.data_ptr(), _p(xs), int(fmt), _p(codes),
-                                    _p(scales), _raw_stream(cur)))
+    lib, k = load(), int(k)
+    size = lib.fp4_expert_gather_workspace(t, k, d, rows)
+    ws = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=x.device) if size > 0 else None
+    _check(lib.fp4_expert_gather(t, k, d, rows, x.data_ptr(), ldx, slots.data_ptr(), _p(xs), int(fmt), _p(codes),
+                                 _p(scales), _p(ws), size, _raw_stream(cur)))
     return xs, codes, scales
 
 

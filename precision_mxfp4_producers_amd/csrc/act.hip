@@ -20,6 +20,7 @@ struct ActGradArgs {
   int64_t m, n;
   int64_t rows;                                          // rows of a workgroup
   int accumulate;                                        // sums is dbias and keeps what it holds
+  int stream;                                            // dz past the caches
 };
 
 // A workgroup takes 8 << LG columns (eight a thread) of `rows` rows; the 256 >>
@@ -43,7 +44,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
         y[j] = __fmul_rn(y[j], act_slope<ACT>(z[j]));
         sum[j] = __fadd_rn(sum[j], y[j]);
       }
-      *reinterpret_cast<uint4*>(a.dz + r * a.n + c) = pack8(y);
+      put(reinterpret_cast<u32x4v*>(a.dz + r * a.n + c), __builtin_bit_cast(u32x4v, pack8(y)), a.stream);
     }
   }
   if (!a.sums) return;
@@ -157,7 +158,7 @@ fp4_status fp4_act_backward(int64_t m, int64_t n, const void* dy, fp4_dtype dy_t
   if (partial && workspace_bytes < fp4_act_backward_workspace(m, n)) return FP4_ESHAPE;
   if (partial && !workspace) return FP4_EINVAL;
   const ActGradArgs a{dy, lddy, z, ldz, dz, partial ? static_cast<float*>(workspace) : dbias, m, n, p.rows,
-                      partial ? 0 : accumulate};
+                      partial ? 0 : accumulate, streams(m * n * 2)};
   const bool f32 = dy_type == FP4_F32;
   hipStream_t s = as_stream(stream);
   switch (act) {

@@ -161,37 +161,126 @@ struct GatherArgs {
   uint16_t* xs;                                          // [rows][d], or null
   uint8_t *codes, *scales;                               // or null
   int e4m3;
+  int stream;                                            // xs past the caches
+  int32_t* where;                                        // [t][k] rows of the slots (by tokens)
+  int token_groups;                                      // workgroups that take tokens
 };
 
-// 2^LG lanes a row, eight values a lane and turn.  A row without a token is zero.
+// The token of a row's slot, or -1.
+__device__ __forceinline__ int row_token(const GatherArgs& a, int slot) {
+  const int token = slot >= 0 ? slot / a.k : -1;
+  return token < a.t ? token : -1;
+}
+
+// Codes and scale of eight values, four neighbouring lanes a block of 32.
+struct Coded {
+  uint2 codes;                                           // E2M1: the first word
+  int e;
+};
+__device__ __forceinline__ Coded encode8(const GatherArgs& a, const uint4 v) {
+  const uint32_t am = max_quad(bf16_absmax8(v.x, v.y, v.z, v.w)) << 16;
+  const int e = a.e4m3 ? upward_exp_e4m3(am) : upward_exp(am);
+  return Coded{a.e4m3 ? e4m3_8(v, pow2_scale(e)) : make_uint2(rtn8_bf16(v.x, v.y, v.z, v.w, pow2_scale(e)), 0u), e};
+}
+
+// Columns c .. c + 7 of row r.
+__device__ __forceinline__ void put_gathered(const GatherArgs& a, int64_t r, int c, const uint4 v, const Coded& q) {
+  if (a.xs) put(reinterpret_cast<u32x4v*>(a.xs + r * a.d + c), u32x4v{v.x, v.y, v.z, v.w}, a.stream);
+  if (a.codes) {
+    if (a.e4m3) *reinterpret_cast<uint2*>(a.codes + r * a.d + c) = q.codes;
+    else *reinterpret_cast<uint32_t*>(a.codes + r * (a.d >> 1) + (c >> 1)) = q.codes.x;
+    if ((threadIdx.x & 3) == 0) a.scales[r * (a.d >> 5) + (c >> 5)] = (uint8_t)(q.e + 127);
+  }
+}
+
+// Row r whole, by G lanes, of which this is lane i: a token's activations, or
+// zeros.
+template <int G>
+__device__ __forceinline__ void gather_row(const GatherArgs& a, int64_t r, int token, int i) {
+  const uint16_t* const x = a.x + (int64_t)std::max(token, 0) * a.ldx;
+  for (int c0 = i * 8; c0 < a.d; c0 += 4 * G * 8) {
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = make_uint4(0, 0, 0, 0);
+    if (token >= 0) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const uint4*>(x + std::min(c0 + u * G * 8, a.d - 8));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + u * G * 8;
+      if (c >= a.d) break;                               // whole groups of four lanes
+      put_gathered(a, r, c, v[u], a.codes ? encode8(a, v[u]) : Coded{});
+    }
+  }
+}
+
+// Row by row, 2^LG lanes a row: one launch.
 template <int LG>
 __global__ __launch_bounds__(256) void expert_gather_kernel(GatherArgs a) {
   constexpr int G = 1 << LG;
-  const int i = threadIdx.x & (G - 1);
-  for (int64_t r = (int64_t)blockIdx.x * (256 / G) + (threadIdx.x >> LG); r < a.rows; r += (int64_t)gridDim.x * (256 / G)) {
-    const int slot = a.slots[r], token = slot >= 0 ? slot / a.k : -1;
-    const bool live = token >= 0 && token < a.t;
-    const uint16_t* const x = a.x + (live ? token : 0) * a.ldx;
-    for (int c0 = i * 8; c0 < a.d; c0 += 4 * G * 8) {
-      uint4 v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = make_uint4(0, 0, 0, 0);
-      if (live) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const uint4*>(x + std::min(c0 + u * G * 8, a.d - 8));
+  for (int64_t r = (int64_t)blockIdx.x * (256 / G) + (threadIdx.x >> LG); r < a.rows; r += (int64_t)gridDim.x * (256 / G))
+    gather_row<G>(a, r, row_token(a, a.slots[r]), threadIdx.x & (G - 1));
+}
+
+// By tokens: x is read and encoded once for all of a token's rows, where rows in
+// their order would bring it from the Infinity Cache once for each (8192 tokens x
+// 2048 to eight rows each, 277 MB of rows: 76 us by rows, 61 by tokens).  The rows
+// of the slots come first:
+__global__ __launch_bounds__(256) void expert_where_kernel(GatherArgs a) {
+  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < a.rows; r += (int64_t)gridDim.x * 256) {
+    const int s = a.slots[r];
+    if (row_token(a, s) >= 0) a.where[s] = (int32_t)r;
+  }
+}
+
+// then a wave takes 2048 columns of a token to all its rows.  where[s] may hold
+// anything if no row has slot s, and holds one of them if several have: a row
+// counts as the slot's if its slot is that.  The workgroups behind those of the
+// tokens take the rows that are no slot's: those without a token, and others than
+// where[s] with slot s.
+__global__ __launch_bounds__(256) void expert_scatter_kernel(GatherArgs a) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if ((int)blockIdx.x >= a.token_groups) {
+    // a wave's rows lie apart, so that a run of padding is many waves'
+    const int64_t waves = ((int64_t)gridDim.x - a.token_groups) * 4, first = ((int64_t)blockIdx.x - a.token_groups) * 4 + wave;
+    for (int64_t r0 = first; r0 < a.rows; r0 += waves * 64) {
+      const int64_t r = r0 + lane * waves;
+      int token = -1;
+      bool mine = false;
+      if (r < a.rows) {
+        const int s = a.slots[r];
+        token = row_token(a, s);
+        mine = token < 0 || a.where[s] != r;
       }
+      for (uint64_t left = __builtin_amdgcn_ballot_w64(mine); left; left &= left - 1) {
+        const int l = __builtin_ctzll(left);
+        gather_row<64>(a, r0 + l * waves, __builtin_amdgcn_readlane(token, l), lane);
+      }
+    }
+    return;
+  }
+  const int parts = (a.d + 2047) / 2048;
+  for (int64_t q = (int64_t)blockIdx.x * 4 + wave; q < (int64_t)a.t * parts; q += (int64_t)a.token_groups * 4) {
+    const int token = (int)(q / parts), first = (int)(q - (int64_t)token * parts) * 2048 + lane * 8;
+    uint4 v[4];
+    Coded e[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = c0 + u * G * 8;
-        if (c >= a.d) break;                               // whole groups of four lanes
-        if (a.xs) *reinterpret_cast<uint4*>(a.xs + r * a.d + c) = v[u];
-        if (a.codes) {
-          const uint32_t am = max_quad(bf16_absmax8(v[u].x, v[u].y, v[u].z, v[u].w)) << 16;
-          const int e = a.e4m3 ? upward_exp_e4m3(am) : upward_exp(am);
-          if (a.e4m3) *reinterpret_cast<uint2*>(a.codes + r * a.d + c) = e4m3_8(v[u], pow2_scale(e));
-          else *reinterpret_cast<uint32_t*>(a.codes + r * (a.d >> 1) + (c >> 1)) = rtn8_bf16(v[u].x, v[u].y, v[u].z, v[u].w, pow2_scale(e));
-          if ((threadIdx.x & 3) == 0) a.scales[r * (a.d >> 5) + (c >> 5)] = (uint8_t)(e + 127);
-        }
+    for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const uint4*>(a.x + token * a.ldx + std::min(first + u * 512, a.d - 8));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) e[u] = a.codes ? encode8(a, v[u]) : Coded{};
+    for (int j0 = 0; j0 < a.k; j0 += 64) {
+      int row = -1;
+      if (j0 + lane < a.k) {
+        const int s = token * a.k + j0 + lane;
+        row = a.where[s];
+        if ((uint32_t)row >= (uint32_t)a.rows || a.slots[row] != s) row = -1;
+      }
+      for (uint64_t left = __builtin_amdgcn_ballot_w64(row >= 0); left; left &= left - 1) {
+        const int64_t r = __builtin_amdgcn_readlane(row, __builtin_ctzll(left));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (first + u * 512 < a.d) put_gathered(a, r, first + u * 512, v[u], e[u]);
       }
     }
   }
@@ -276,10 +365,15 @@ template <bool DYF32, bool ZF32>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(CombineGradArgs a) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   if ((int)blockIdx.x >= a.slot_groups) {
-    for (int64_t r = ((int64_t)blockIdx.x - a.slot_groups) * 4 + wave; r < a.rows; r += ((int64_t)gridDim.x - a.slot_groups) * 4) {
-      const int s = a.slots[r];
-      if (s >= 0 && s < a.t * a.k) continue;
-      for (int c = lane * 8; c < a.d; c += 512) *reinterpret_cast<uint4*>(a.dz + r * a.d + c) = make_uint4(0, 0, 0, 0);
+    // a wave's rows lie apart, so that a run of padding is many waves'
+    const int64_t waves = ((int64_t)gridDim.x - a.slot_groups) * 4;
+    for (int64_t r0 = ((int64_t)blockIdx.x - a.slot_groups) * 4 + wave; r0 < a.rows; r0 += waves * 64) {
+      const int64_t mine = r0 + lane * waves;
+      const bool clear = mine < a.rows && (uint32_t)a.slots[mine] >= (uint32_t)(a.t * a.k);
+      for (uint64_t left = __builtin_amdgcn_ballot_w64(clear); left; left &= left - 1) {
+        const int64_t r = r0 + __builtin_ctzll(left) * waves;
+        for (int c = lane * 8; c < a.d; c += 512) *reinterpret_cast<uint4*>(a.dz + r * a.d + c) = make_uint4(0, 0, 0, 0);
+      }
     }
     return;
   }
@@ -321,6 +415,19 @@ static int sort_groups(int64_t slots, int64_t& chunk) {
   int64_t groups = slots <= kOne ? 1 : std::min((slots + 4095) / 4096, kMost);
   chunk = std::max<int64_t>((slots + groups - 1) / groups + kSortThreads - 1, kSortThreads) / kSortThreads * kSortThreads;
   return (int)std::max<int64_t>((slots + chunk - 1) / chunk, 1);
+}
+
+static bool gather_shape_ok(int64_t t, int64_t k, int64_t d, int64_t rows) {
+  return t >= 0 && k >= 1 && k <= kMaxExpertRows && t <= kMaxExpertRows / k && mult32z(d) && d <= kMaxExpertRows && rows >= 0 &&
+         rows <= kMaxExpertRows + kMaxExperts * 256;
+}
+
+// By tokens where the rows outgrow the L2s and a token has several (bf16 rows
+// alone, by rows and by tokens: 8 experts a token, 48 MB of rows 11 and 16 us, 66
+// MB 21 and 18, 264 MB 76 and 61; 2 a token, 130 MB 41 and 36, with codes 48 and
+// 49).
+static bool gather_by_tokens(int64_t t, int64_t k, int64_t d, int64_t rows) {
+  return t > 0 && k > 1 && d > 128 && rows * d * 2 > ((int64_t)56 << 20);
 }
 
 static bool sort_shape_ok(int64_t t, int64_t k, int64_t experts) {
@@ -377,22 +484,39 @@ fp4_status fp4_expert_sort(int64_t t, int64_t k, int64_t experts, const void* id
                        : go(expert_count_kernel<false>, expert_sort_kernel<false>);
 }
 
+int64_t fp4_expert_gather_workspace(int64_t t, int64_t k, int64_t d, int64_t rows) {
+  if (!gather_shape_ok(t, k, d, rows)) return -1;
+  return gather_by_tokens(t, k, d, rows) ? t * k * (int64_t)sizeof(int32_t) : 0;
+}
+
 fp4_status fp4_expert_gather(int64_t t, int64_t k, int64_t d, int64_t rows, const uint16_t* x, int64_t ldx,
                              const int32_t* slots, uint16_t* xs, fp4_format format, uint8_t* codes, uint8_t* scales,
-                             hipStream_t stream) {
+                             void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   if ((format != FP4_E2M1 && format != FP4_E4M3) || (codes == nullptr) != (scales == nullptr)) return FP4_EINVAL;
-  if (t < 0 || t > kMaxExpertRows || k < 1 || k > kMaxExpertRows || !mult32z(d) || d > kMaxExpertRows || ldx < d || rows < 0 ||
-      rows > kMaxExpertRows + kMaxExperts * 256)
-    return FP4_ESHAPE;
+  if (!gather_shape_ok(t, k, d, rows) || ldx < d) return FP4_ESHAPE;
   if (rows == 0 || d == 0 || (!xs && !codes)) return FP4_OK;
   if (!slots || (t > 0 && !x)) return FP4_EINVAL;
-  if (!aligned16(x) || !aligned16(xs) || !aligned16(codes) || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(slots) & 3))
+  const bool by_tokens = gather_by_tokens(t, k, d, rows);
+  if (workspace_bytes < fp4_expert_gather_workspace(t, k, d, rows)) return FP4_ESHAPE;
+  if (by_tokens && !workspace) return FP4_EINVAL;
+  if (!aligned16(x) || !aligned16(xs) || !aligned16(codes) || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(slots) & 3) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 3))
     return FP4_EALIGN;
-  const GatherArgs a{x, ldx, slots, (int)rows, (int)t, (int)k, (int)d, xs,
-                     codes, scales, format == FP4_E4M3};
+  GatherArgs a{x, ldx, slots, (int)rows, (int)t, (int)k, (int)d, xs, codes, scales, format == FP4_E4M3,
+               streams(rows * d * 2), static_cast<int32_t*>(workspace), 0};
+  hipStream_t s = as_stream(stream);
+  if (by_tokens) {
+    hipLaunchKernelGGL(expert_where_kernel, dim3((unsigned)std::min((rows + 255) / 256, kMostGroups)), dim3(256), 0, s, a);
+    const fp4_status st = launch_status();
+    if (st != FP4_OK) return st;
+    const int64_t tokens = std::min((t * ((d + 2047) / 2048) + 3) / 4, kMostGroups), others = std::min<int64_t>((rows + 31) / 32, 1024);
+    a.token_groups = (int)tokens;
+    hipLaunchKernelGGL(expert_scatter_kernel, dim3((unsigned)(tokens + others)), dim3(256), 0, s, a);
+    return launch_status();
+  }
   const auto go = [&](auto kernel, int lg) {
     const int64_t per = 256 >> lg;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min((rows + per - 1) / per, kMostGroups)), dim3(256), 0, as_stream(stream), a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min((rows + per - 1) / per, kMostGroups)), dim3(256), 0, s, a);
   };
   if (d <= 128) go(expert_gather_kernel<4>, 4);
   else go(expert_gather_kernel<6>, 6);

@@ -4,6 +4,7 @@
 
 #include "activation.h"
 #include "gemm_core.h"
+#include "rows.h"
 
 namespace mx {
 
@@ -20,19 +21,6 @@ struct Epilogue {
   int accumulate;                                        // fp32 y, nothing else
   int stream;                                            // y past the caches (non-temporal stores)
 };
-
-// A store past the caches or an ordinary one, by a wave-uniform flag.  The empty
-// statements keep the compiler from making one (ordinary) store of both.
-template <typename T>
-__device__ __forceinline__ void put(T* p, const T& v, int stream) {
-  if (stream) {
-    asm volatile("");
-    __builtin_nontemporal_store(v, p);
-    asm volatile("");
-  } else {
-    *p = v;
-  }
-}
 
 // Four or eight neighbouring values as bf16.
 template <int W>
@@ -204,10 +192,6 @@ __device__ __forceinline__ void zero_tile(v16f (&acc)[4][2]) {
 
 // Row lengths by the main loop's K range (see kWindow).
 inline int k_mode(int64_t k) { return k > 0 && k % 256 == 0 ? kWhole : (k >= 256 ? kWindow : kShort); }
-
-// An output that cannot stay in the 256 MB Infinity Cache for its reader goes
-// past it (the plain product's rule).
-inline bool streams(int64_t bytes) { return bytes > ((int64_t)192 << 20); }
 
 // Number of bm x bn tiles, or -1 when it exceeds a grid's 2^31 - 1 workgroups.
 inline int64_t tiles_of(int64_t m, int64_t bm, int64_t n, int64_t bn) {

@@ -30,7 +30,7 @@ namespace mx {
 
 template <int XT, int WT, int MT, int NT, int NW, int U, bool GATE, bool STAGED, bool WHOLE>
 __global__ __launch_bounds__(NW * 64) void matvec_kernel(MatvecArgs a, MvPlan plan) {
-  matvec_body<XT, WT, MT, NT, NW, U, GATE, STAGED, WHOLE, false>(a, plan, MvEpilogue{});
+  matvec_body<XT, WT, MT, NT, NW, U, GATE, STAGED, WHOLE ? kWholeScales : kByteScales, false>(a, plan, MvEpilogue{});
 }
 
 // C (+)= 0 for an empty reduction.
@@ -51,7 +51,7 @@ static fp4_status matvec_launch(const MatvecArgs& a, hipStream_t stream) {
   }
   matvec_variant<WT, GATE>(a, kMatvecGrid, [&](auto v, const MvPlan& plan, unsigned grid) {
     using V = decltype(v);
-    hipLaunchKernelGGL((matvec_kernel<XT, WT, V::MT, V::NT, V::NW, V::U, GATE, V::STAGED, V::WHOLE>), dim3(grid),
+    hipLaunchKernelGGL((matvec_kernel<XT, WT, V::MT, V::NT, V::NW, V::U, GATE, V::STAGED, V::SC == kWholeScales>), dim3(grid),
                        dim3(V::NW * 64), 0, stream, a, plan);
   });
   return launch_status();

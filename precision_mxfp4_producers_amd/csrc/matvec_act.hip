@@ -12,27 +12,28 @@
 
 namespace mx {
 
-template <int XT, int MT, int NT, int NW, int U, bool STAGED, bool WHOLE>
+template <int XT, int MT, int NT, int NW, int U, bool STAGED, int SC>
 __global__ __launch_bounds__(NW * 64) void matvec_act_kernel(MatvecArgs a, MvPlan plan, MvEpilogue e) {
-  matvec_body<XT, kMx, MT, NT, NW, U, false, STAGED, WHOLE, true>(a, plan, e);
+  matvec_body<XT, kMx, MT, NT, NW, U, false, STAGED, SC, true>(a, plan, e);
 }
 
-// The epilogue of an empty reduction.
-__global__ __launch_bounds__(256) void matvec_act_zero_kernel(int m, int64_t n, MvEpilogue e) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < m * n; i += (int64_t)gridDim.x * 256)
-    put_epilogue(e, (int)(i / n), i % n, 0.0f);
+// The epilogue of an empty reduction or one of a few weights.
+template <int XT>
+__global__ __launch_bounds__(256) void matvec_act_small_kernel(MatvecArgs a, MvEpilogue e) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.m * a.n; i += (int64_t)gridDim.x * 256)
+    put_epilogue(e, (int)(i / a.n), i % a.n, small_sum<XT>(a, i / a.n, i % a.n));
 }
 
 template <int XT>
 static fp4_status matvec_act_launch(const MatvecArgs& a, const MvEpilogue& e, hipStream_t stream) {
-  if (a.k == 0) {
+  if (a.n * (a.k / 32) < 4) {
     const int64_t grid = std::min<int64_t>((a.m * a.n + 255) / 256, 65536);
-    hipLaunchKernelGGL(matvec_act_zero_kernel, dim3((unsigned)grid), dim3(256), 0, stream, a.m, a.n, e);
+    hipLaunchKernelGGL(matvec_act_small_kernel<XT>, dim3((unsigned)grid), dim3(256), 0, stream, a, e);
     return launch_status();
   }
-  matvec_variant<kMx, false>(a, kMatvecGrid, [&](auto v, const MvPlan& plan, unsigned grid) {
+  matvec_variant<kMx, false, kWordScales>(a, kMatvecGrid, [&](auto v, const MvPlan& plan, unsigned grid) {
     using V = decltype(v);
-    hipLaunchKernelGGL((matvec_act_kernel<XT, V::MT, V::NT, V::NW, V::U, V::STAGED, V::WHOLE>), dim3(grid),
+    hipLaunchKernelGGL((matvec_act_kernel<XT, V::MT, V::NT, V::NW, V::U, V::STAGED, V::SC>), dim3(grid),
                        dim3(V::NW * 64), 0, stream, a, plan, e);
   });
   return launch_status();

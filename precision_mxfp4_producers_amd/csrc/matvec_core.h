@@ -184,9 +184,18 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
 // (STAGED), else each wave brings its own steps, with the item, into a room of
 // its own (no barrier between waves; wave_lds_order between its writes and
 // its reads).
-// WHOLE: K is a multiple of U steps and the scales are aligned to words, so
-// that the scale bytes of an item come with one load, spread like the codes,
-// and reach the other lanes of a row by permutes.
+// How the scales come (SC).
+//   kWholeScales  K is a multiple of U steps and the scales are aligned to words,
+//                 so that the scale bytes of an item come with one load, spread
+//                 like the codes, and reach the other lanes of a row by permutes.
+//   kWordScales   MXFP4, any K and alignment: the same with unaligned words; one
+//                 that would end behind the scales is moved back and shifted (they
+//                 are four bytes at least).  Its other bytes may be those of the
+//                 next row, and meet zero codes.
+//   kByteScales   any K, one step an item: each lane loads the bytes that its
+//                 products take.  (64 experts' 2048 x 1056, three rows each: 33 us,
+//                 with words 27.)
+constexpr int kByteScales = 0, kWholeScales = 1, kWordScales = 2;
 constexpr int kLds = 160 * 1024;
 constexpr int kStageBytes = 143 * 1024;                  // most of x in LDS; the rest is the partial sums'
 constexpr int kXPitch = 256 + 64;                        // of a wave's own step of x
@@ -210,10 +219,10 @@ constexpr int kScaleWords = WT == kMx ? U : 2 * U;
 
 // One item of W as loaded: pieces of codes, and one word of a row's scale
 // bytes; of a partial step the four bytes that this lane's products take.
-template <int WT, int NT, int U, bool WHOLE>
+template <int WT, int NT, int U, int SC>
 struct MvItem {
   v4i c[NT][U];
-  uint32_t s[NT][WHOLE ? 1 : 4];
+  uint32_t s[NT][SC == kWholeScales ? 1 : (SC == kWordScales ? 2 : 4)];   // kWordScales: the word and its shift
 };
 
 // One step of x, as loaded: sixteen bytes a lane, 16 (bf16) or 8 (E4M3) lanes a row.
@@ -239,10 +248,10 @@ __device__ __forceinline__ void wave_lds_order() {
 
 // The kernel's body.  EPI: the epilogue of fp4_matvec_act (`e`) takes the sums
 // to their output.
-template <int XT, int WT, int MT, int NT, int NW, int U, bool GATE, bool STAGED, bool WHOLE, bool EPI>
+template <int XT, int WT, int MT, int NT, int NW, int U, bool GATE, bool STAGED, int SC, bool EPI>
 __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& plan, const MvEpilogue& e) {
   static_assert(!STAGED || (MT == 1 && NT == 1), "sixteen rows of x and one tile at a time");
-  static_assert((WHOLE && STAGED) || U == 1, "a partial step, and one that brings its x, is an item of its own");
+  static_assert((SC != kByteScales && STAGED) || U == 1, "a partial step, and one that brings its x, is an item of its own");
   constexpr int ROWS = GATE ? 8 : 16;                    // output columns of a tile
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   constexpr int kWaveFloats = STAGED ? 260 : room_bytes(MT) / 4;   // between two waves' partial sums
@@ -255,6 +264,7 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
   const int steps = (int)((a.k + 127) >> 7), items = (steps + U - 1) / U;
   const int per = (items + (1 << plan.kw_log2) - 1) >> plan.kw_log2;   // turns of a wave per tile
   const int64_t groups = (a.n + ROWS * NT * RT - 1) / (ROWS * NT * RT);
+  const int64_t scale_bytes = (GATE ? 2 : 1) * a.n * ks;
   const __amdgpu_buffer_rsrc_t rx =
       buffer_rsrc(a.x, XT == kXBf16 ? ((a.m - 1) * a.ldx + a.k) * 2 : (int64_t)a.m * a.k);
   const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(a.x_scales, XT == kXBf16 ? 0 : (int64_t)a.m * (a.k >> 5));
@@ -272,17 +282,28 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
   const auto row_of = [&](int64_t group, int j, int r) {
     return std::min(((group * RT + rt) * NT + j) * ROWS + (r & (ROWS - 1)), a.n - 1) + (GATE && r >= ROWS ? a.n : 0);
   };
-  const auto load_w = [&](MvItem<WT, NT, U, WHOLE>& it, int64_t group, int turn) {
+  const auto load_w = [&](MvItem<WT, NT, U, SC>& it, int64_t group, int turn) {
     const int item = item_of(turn), piece = lane & 3;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int64_t row = row_of(group, j, 4 * ((lane >> 2) & 3) + (lane >> 4));
       const uint8_t* const c = a.codes + row * kc;
-      if constexpr (WHOLE) {
+      if constexpr (SC == kWholeScales) {
 #pragma unroll
         for (int u = 0; u < U; ++u) it.c[j][u] = *reinterpret_cast<const v4i*>(c + (item * U + u) * 64 + piece * 16);
         constexpr int D = kScaleWords<WT, U>;
         it.s[j][0] = reinterpret_cast<const uint32_t*>(a.scales + row * ks)[item * D + (piece & (D - 1))];
+      } else if constexpr (SC == kWordScales) {
+        const int blocks = (int)(a.k >> 5);              // a block of 32 values is whole or absent
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int kb = (item * U + u) * 4 + piece;
+          const v4i v = *reinterpret_cast<const v4i*>(c + std::min(kb, blocks - 1) * 16);
+          it.c[j][u] = kb < blocks ? v : v4i{0, 0, 0, 0};
+        }
+        const int64_t at = row * ks + 4 * (item * U + (piece & (U - 1))), in = std::min(at, scale_bytes - 4);
+        __builtin_memcpy(&it.s[j][0], a.scales + in, 4);
+        it.s[j][1] = (uint32_t)std::min<int64_t>(8 * (at - in), 24);
       } else {
         const int blocks = (int)(a.k >> 5), kb = item * 4;   // a block of 32 values is whole or absent
         const uint8_t* const s = a.scales + row_of(group, j, r) * ks;
@@ -338,19 +359,22 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
 
   v4f acc[MT][NT];
   const uint32_t xrow = (STAGED ? (uint32_t)(r < a.m ? r : 0) * (uint32_t)stage_pitch(a.k) : (uint32_t)r * kXPitch) + g * 16;
-  const auto multiply = [&](const MvItem<WT, NT, U, WHOLE>& it, int turn) {
+  const auto multiply = [&](const MvItem<WT, NT, U, SC>& it, int turn) {
     if (kw + (turn << plan.kw_log2) >= items) return;    // wave-uniform
     const int item = item_of(turn);
     // the item's scale words of this lane's row r, from the lanes that loaded the row
     uint32_t sw[NT][kScaleWords<WT, U>];
-    if constexpr (WHOLE)
+    if constexpr (SC != kByteScales)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j) {
+        const uint32_t mine = SC == kWordScales ? it.s[j][0] >> it.s[j][SC == kWordScales ? 1 : 0] : it.s[j][0];
 #pragma unroll
         for (int d = 0; d < kScaleWords<WT, U>; ++d)
-          sw[j][d] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * (4 * (r & 3) + (r >> 2)) + d), (int)it.s[j][0]);
+          sw[j][d] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * (4 * (r & 3) + (r >> 2)) + d), (int)mine);
+      }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (SC == kWordScales && U > 1 && item * U + u >= steps) break;   // no x is staged there
       bf16x8_t w[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -358,7 +382,7 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
         uint32_t c[4] = {(uint32_t)cw[0], (uint32_t)cw[1], (uint32_t)cw[2], (uint32_t)cw[3]};
         to_operand(c);
         float sc[4];                                     // the scale of product q's values
-        if constexpr (WT == kMx && WHOLE) {
+        if constexpr (WT == kMx && SC != kByteScales) {
           sc[0] = e8m0_byte<0>(sw[j][u]);
           sc[1] = e8m0_byte<1>(sw[j][u]);
           sc[2] = e8m0_byte<2>(sw[j][u]);
@@ -369,7 +393,7 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t b = WHOLE ? (sw[j][2 * u + (q >> 1)] >> (16 * (q & 1) + 8 * (g >> 1))) & 0xFFu : it.s[j][q];
+            const uint32_t b = SC != kByteScales ? (sw[j][2 * u + (q >> 1)] >> (16 * (q & 1) + 8 * (g >> 1))) & 0xFFu : it.s[j][q];
             const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 1.0f, false);
             sc[q] = d[0];
           }
@@ -446,7 +470,7 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
   const auto step = [&](int64_t& gr, int& tn) {
     if (++tn == per) { tn = 0; gr += gridDim.x; }
   };
-  using W = MvItem<WT, NT, U, WHOLE>;
+  using W = MvItem<WT, NT, U, SC>;
   MvX<XT, MT> x;                                         // the next step of x, on its way to the wave's room
   const auto ahead = [&](W& w) {                         // loads of the item after the current one
     int64_t gr = group;
@@ -581,17 +605,39 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
 constexpr int kMatvecMaxM = 64;
 constexpr int64_t kMatvecGrid = 256;                     // one workgroup of 16 waves per CU
 
+// One sum of a product with fewer than four bytes of scales (96 weights at most),
+// of which no word can be loaded.
+template <int XT>
+__device__ __forceinline__ float small_sum(const MatvecArgs& a, int64_t mr, int64_t row) {
+  float v = 0.0f;
+  for (int64_t i = 0; i < a.k; ++i) {
+    const uint32_t c = (a.codes[(row * a.k + i) >> 1] >> (4 * (i & 1))) & 15u, e = (c >> 1) & 3u;
+    const float mag = e ? __uint_as_float((126u + e) << 23 | (c & 1u) << 22) : 0.5f * (float)(c & 1u);
+    const int ws = a.scales[(row * a.k + i) >> 5];
+    float x;
+    if constexpr (XT == kXBf16) {
+      x = bf16_bits_to_f32(static_cast<const uint16_t*>(a.x)[mr * a.ldx + i]);
+    } else {
+      const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(static_cast<const uint8_t*>(a.x)[mr * a.k + i], 1.0f, false);
+      x = __builtin_amdgcn_ldexpf(d[0], (int)a.x_scales[(mr * a.k + i) >> 5] - 127);
+    }
+    v = __builtin_fmaf(x, __builtin_amdgcn_ldexpf(c & 8u ? -mag : mag, ws - 127), v);
+  }
+  return v;
+}
+
 // A compiled variant of the kernel.
-template <int MT_, int NT_, int NW_, int U_, bool STAGED_, bool WHOLE_>
+template <int MT_, int NT_, int NW_, int U_, bool STAGED_, int SC_>
 struct MvVariant {
-  static constexpr int MT = MT_, NT = NT_, NW = NW_, U = U_;
-  static constexpr bool STAGED = STAGED_, WHOLE = WHOLE_;
+  static constexpr int MT = MT_, NT = NT_, NW = NW_, U = U_, SC = SC_;
+  static constexpr bool STAGED = STAGED_;
 };
 
 // Calls go(variant, plan, workgroups) for a product of a.m rows at most that
 // `cus` CUs share (k > 0).  MANY: more than sixteen rows, and two tiles a wave,
-// are among them.
-template <int WT, bool GATE, bool MANY = true, typename F>
+// are among them.  PART: how the scales come where K is not whole steps or they
+// are not aligned to words.
+template <int WT, bool GATE, int PART = kByteScales, bool MANY = true, typename F>
 static void matvec_variant(const MatvecArgs& a, int64_t cus, F&& launch) {
   constexpr int ROWS = GATE ? 8 : 16;
   const int64_t tiles = (a.n + ROWS - 1) / ROWS, steps = (a.k + 127) / 128;
@@ -619,7 +665,7 @@ static void matvec_variant(const MatvecArgs& a, int64_t cus, F&& launch) {
   const auto groups_of = [&](int log2) { return (tiles + nt * (nw >> log2) - 1) / (nt * (nw >> log2)); };
   constexpr int kMaxU = WT == kMx ? 4 : 2;               // what the registers hold
   for (int uu = staged ? kMaxU : 1; uu >= 1; uu >>= 1) {
-    if (uu > 1 && (a.k % (128 * uu) != 0 || !words)) continue;
+    if (uu > 1 && PART == kByteScales && (a.k % (128 * uu) != 0 || !words)) continue;
     for (int log2 = 2; log2 <= (nw == 16 ? 4 : 3); ++log2) {
       const int64_t rounds = (groups_of(log2) + cus - 1) / cus;
       const int64_t cost =
@@ -630,19 +676,24 @@ static void matvec_variant(const MatvecArgs& a, int64_t cus, F&& launch) {
   const MvPlan plan{kw, batch};
   const unsigned grid = (unsigned)std::min(groups_of(kw), cus);
   const auto go = [&](auto variant) { launch(variant, plan, grid); };
+  const bool exact = whole && a.k % (128 * u) == 0;
   if (staged) {
-    if (u == 2) go(MvVariant<1, 1, 16, 2, true, true>{});
-    else if (u == 1 && whole) go(MvVariant<1, 1, 16, 1, true, true>{});
-    else if (u == 1) go(MvVariant<1, 1, 16, 1, true, false>{});
+    const auto of = [&](auto uc) {
+      constexpr int U = uc();
+      if (exact) go(MvVariant<1, 1, 16, U, true, kWholeScales>{});
+      else if constexpr (PART != kByteScales || U == 1) go(MvVariant<1, 1, 16, U, true, PART>{});
+    };
+    if (u == 2) of(std::integral_constant<int, 2>{});
+    else if (u == 1) of(std::integral_constant<int, 1>{});
     if constexpr (kMaxU == 4)
-      if (u == 4) go(MvVariant<1, 1, 16, 4, true, true>{});
+      if (u == 4) of(std::integral_constant<int, 4>{});
     return;
   }
   const auto own = [&](auto mtc) {                       // each wave brings its own steps of x
     constexpr int MT = mtc(), NW = MT > 1 ? 8 : 16;
     if constexpr (MANY && (WT == kMx || MT > 1))
-      if (nt == 2) return go(MvVariant<MT, 2, NW, 1, false, true>{});
-    whole ? go(MvVariant<MT, 1, NW, 1, false, true>{}) : go(MvVariant<MT, 1, NW, 1, false, false>{});
+      if (nt == 2) return go(MvVariant<MT, 2, NW, 1, false, kWholeScales>{});
+    exact ? go(MvVariant<MT, 1, NW, 1, false, kWholeScales>{}) : go(MvVariant<MT, 1, NW, 1, false, PART>{});
   };
   if (mt == 1) return own(std::integral_constant<int, 1>{});
   if constexpr (MANY) {

@@ -64,7 +64,7 @@ __device__ __forceinline__ void clear_behind(const ExpertRows& x, const MatvecAr
   }
 }
 
-template <int XT, int U, bool GATE, bool STAGED, bool WHOLE>
+template <int XT, int U, bool GATE, bool STAGED, int SC>
 __global__ __launch_bounds__(1024) void matvec_experts_kernel(MatvecArgs a, MvPlan plan, ExpertRows x) {
   clear_behind(x, a);
   int expert, first, count;
@@ -77,32 +77,53 @@ __global__ __launch_bounds__(1024) void matvec_experts_kernel(MatvecArgs a, MvPl
   a.scales += expert * n * (a.k >> 5);
   if (GATE) a.h += first * a.n;
   else a.c += first * a.ldc;
-  matvec_body<XT, kMx, 1, 1, 16, U, GATE, STAGED, WHOLE, false>(a, plan, MvEpilogue{});
+  matvec_body<XT, kMx, 1, 1, 16, U, GATE, STAGED, SC, false>(a, plan, MvEpilogue{});
 }
 
-// An empty reduction: all rows 0.
-__global__ __launch_bounds__(256) void matvec_experts_zero_kernel(MatvecArgs a, int rows) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * a.n; i += (int64_t)gridDim.x * 256) {
-    if (a.h) a.h[i] = 0;
-    else a.c[i / a.n * a.ldc + i % a.n] = 0.0f;
+// An empty reduction or one of a few weights an expert.
+template <int XT, bool GATE>
+__global__ __launch_bounds__(256) void matvec_experts_small_kernel(MatvecArgs a, ExpertRows x) {
+  const uint8_t* const codes = a.codes;
+  const uint8_t* const scales = a.scales;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < x.rows * a.n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / a.n, col = i % a.n;
+    float v = 0.0f, w = 0.0f;
+    int e = 0;
+    while (e < x.experts && !(r >= x.offsets[e] && r < x.offsets[e + 1])) ++e;
+    if (e < x.experts) {
+      const int64_t weights = e * (GATE ? 2 : 1) * a.n * a.k;
+      a.codes = codes + (weights >> 1);
+      a.scales = scales + (weights >> 5);
+      v = small_sum<XT>(a, r, col);
+      if (GATE) w = small_sum<XT>(a, r, a.n + col);
+    }
+    if constexpr (GATE) {
+      const uint32_t both = bf16_pack2_rne(v, w);
+      const float av[1] = {__uint_as_float(both << 16)};
+      float sig[1], sl[1];
+      sigmoid_silu_n(av, sig, sl);
+      a.h[i] = (uint16_t)bf16_pack2_rne(__fmul_rn(sl[0], __uint_as_float(both & 0xFFFF0000u)), 0.0f);
+    } else {
+      a.c[r * a.ldc + col] = v;
+    }
   }
 }
 
 template <int XT, bool GATE>
 static fp4_status matvec_experts_launch(MatvecArgs a, const ExpertRows& x, hipStream_t stream) {
-  if (a.k == 0) {
+  if ((GATE ? 2 : 1) * a.n * (a.k / 32) < 4) {
     const int64_t grid = std::min<int64_t>((x.rows * a.n + 255) / 256, 65536);
-    hipLaunchKernelGGL(matvec_experts_zero_kernel, dim3((unsigned)grid), dim3(256), 0, stream, a, x.rows);
+    hipLaunchKernelGGL((matvec_experts_small_kernel<XT, GATE>), dim3((unsigned)grid), dim3(256), 0, stream, a, x);
     return launch_status();
   }
   a.m = std::min(x.rows, kUnitRows);                     // of a unit, at most
   // every expert that can have a row, and a unit more for every sixteen rows
   const int experts = std::min(x.experts, x.rows), units = experts + x.rows / kUnitRows;
   const int64_t cus = std::max<int64_t>(kMatvecGrid / experts, 1);
-  matvec_variant<kMx, GATE, false>(a, cus, [&](auto v, const MvPlan& plan, unsigned grid) {
+  matvec_variant<kMx, GATE, kWordScales, false>(a, cus, [&](auto v, const MvPlan& plan, unsigned grid) {
     using V = decltype(v);
     static_assert(V::MT == 1 && V::NT == 1 && V::NW == 16, "a unit is one tile of rows");
-    hipLaunchKernelGGL((matvec_experts_kernel<XT, V::U, GATE, V::STAGED, V::WHOLE>), dim3(grid, (unsigned)units), dim3(1024),
+    hipLaunchKernelGGL((matvec_experts_kernel<XT, V::U, GATE, V::STAGED, V::SC>), dim3(grid, (unsigned)units), dim3(1024),
                        0, stream, a, plan, x);
   });
   return launch_status();

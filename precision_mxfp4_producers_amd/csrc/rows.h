@@ -1,5 +1,5 @@
-// Eight neighbouring values of a row: loads, stores and E4M3 codes, shared by
-// the kernels that hold rows of activations in registers.
+// Neighbouring values of a row: loads, stores and E4M3 codes, shared by the
+// kernels that hold rows of activations in registers.
 #pragma once
 
 #include "mx_device.h"
@@ -36,6 +36,24 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
   if constexpr (F32) return static_cast<const float*>(p)[i];
   else return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
+
+// ---------------------------------------------------------------- stores
+// A store past the caches or an ordinary one, by a wave-uniform flag.  The empty
+// statements keep the compiler from making one (ordinary) store of both.
+template <typename T>
+__device__ __forceinline__ void put(T* p, const T& v, int stream) {
+  if (stream) {
+    asm volatile("");
+    __builtin_nontemporal_store(v, p);
+    asm volatile("");
+  } else {
+    *p = v;
+  }
+}
+
+// An output that cannot stay in the 256 MB Infinity Cache for its reader goes
+// past it (the plain product's rule).
+inline bool streams(int64_t bytes) { return bytes > ((int64_t)192 << 20); }
 
 // ---------------------------------------------------------------- E4M3 codes
 // Upward exponent for E4M3 (largest magnitude 448 = 1.75 * 2^8) of a finite

@@ -108,14 +108,15 @@ def test_sort(lib, changes, want):
     assert call(lib.fp4_expert_sort, SORT, **changes) == want
 
 
-GATHER = dict(t=4, k=2, d=64, rows=512, x=P, ldx=64, slots=P, xs=P, fmt=0, codes=P, scales=P, stream=None)
+GATHER = dict(t=4, k=2, d=64, rows=512, x=P, ldx=64, slots=P, xs=P, fmt=0, codes=P, scales=P, ws=None, size=0, stream=None)
 
 
 @pytest.mark.parametrize("changes,want", [
     (dict(fmt=2), EINVAL), (dict(codes=None), EINVAL), (dict(scales=None), EINVAL), (dict(x=None), EINVAL), (dict(slots=None), EINVAL),
     (dict(t=-1), ESHAPE), (dict(k=0), ESHAPE), (dict(d=48), ESHAPE), (dict(ldx=56), ESHAPE), (dict(rows=-1), ESHAPE), (dict(rows=1 << 31), ESHAPE),
     (dict(t=1 << 31), ESHAPE), (dict(d=1 << 31, ldx=1 << 31), ESHAPE),
-    (dict(x=P + 8), EALIGN), (dict(xs=P + 8), EALIGN), (dict(codes=P + 8), EALIGN), (dict(ldx=68), EALIGN), (dict(slots=P + 2), EALIGN),
+    (dict(x=P + 8), EALIGN), (dict(xs=P + 8), EALIGN), (dict(codes=P + 8), EALIGN), (dict(ldx=68), EALIGN), (dict(slots=P + 2), EALIGN), (dict(ws=P + 2), EALIGN),
+    (dict(t=1 << 16, d=4096, ldx=4096, rows=1 << 17), ESHAPE), (dict(t=1 << 16, d=4096, ldx=4096, rows=1 << 17, size=1 << 20), EINVAL),
     (dict(rows=0, x=None, slots=None), OK), (dict(d=0, x=None), OK), (dict(xs=None, codes=None, scales=None), OK),
 ])
 def test_gather(lib, changes, want):

@@ -107,6 +107,25 @@ def test_gather_takes_slots_of_no_token_for_padding(gpu_lib):
     assert np.array_equal(host(xs.view(torch.int16)).view(np.uint16), want)
 
 
+@pytest.mark.parametrize("t,k,e,d,align", [(2500, 6, 40, 2080, 32), (4100, 2, 8, 4160, 1), (450, 70, 90, 1024, 32)])
+def test_gather_of_many_rows(gpu_lib, t, k, e, d, align):
+    """Past the size from which the rows go out token by token: the same bytes, rows without a token zero."""
+    x = synthetic.tensor((t, d), seed=d)
+    _, slots, _ = X.sort(choices(t, k, e, d, "holes"), e, align)
+    assert gpu_lib.load().fp4_expert_gather_workspace(t, k, d, len(slots)) == 4 * t * k
+    slots[-3:] = slots[0], -7, t * k                       # a slot twice, and two that are none
+    want = X.gather(x, np.where((slots >= 0) & (slots < t * k), slots, -1), k)
+    some = np.random.default_rng(0).choice(len(slots), 500)
+    some = np.concatenate((some, [0, len(slots) - 3, len(slots) - 2, len(slots) - 1]))
+    for fmt, codec in ((gpu_lib.FP4_E2M1, Q.quantize_rows), (gpu_lib.FP4_E4M3, N.encode_e4m3)):
+        xs, codes, scales = gpu_lib.fp4_expert_gather(bf16(x), dev(slots), k, fmt=fmt)
+        assert np.array_equal(host(xs.view(torch.int16)).view(np.uint16), want)
+        wc, ws = codec(want[some])
+        assert np.array_equal(host(codes)[some], wc) and np.array_equal(host(scales)[some], ws)
+        rest = gpu_lib.fp4_expert_gather(bf16(x), dev(slots), k, fmt=fmt, emit_x=False)
+        assert torch.equal(rest[1], codes) and torch.equal(rest[2], scales)
+
+
 def parts(t, k, e, d, align, seed, zf32, spread="holes"):
     """Plan and tensors: (slots, where, z float64, z, weights)."""
     _, slots, where = X.sort(choices(t, k, e, seed, spread), e, align)

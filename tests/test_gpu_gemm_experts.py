@@ -110,7 +110,8 @@ def test_segments_that_are_not_ascending_stay_inside(gpu_lib):
 
 
 WGRAD = [((1,), 32, 32), ((0, 5, 0, 64), 64, 96), ((256, 300, 31, 0, 700), 96, 288), ((33,) * 9, 288, 64), ((2000, 1), 256, 256),
-         ((7, 8, 9, 250), 544, 320), ((0,) * 66 + (40,), 32, 64), ((0, 0), 64, 32)]
+         ((7, 8, 9, 250), 544, 320), ((0,) * 66 + (40,), 32, 64), ((0, 0), 64, 32),
+         ((300, 40), 1312, 288), ((33, 0, 64), 96, 1312)]
 
 
 @pytest.mark.parametrize("align,extra", [(32, 0), (32, 256), (256, 0)])
