@@ -687,14 +687,30 @@ def fp4_swiglu_matvec(x, w13_codes, w13_scales, x_scales=None, h=None):
 _OUTPUT_TYPES = (torch.bfloat16, torch.float32)
 
 
-def _typed_out(t, shape, dtype, device, name):
+def _operands(a_codes, a_scales, b_codes, b_scales, cur):
+    """(m, n, k) of a product's codes [m][k/2], [n][k/2] and their scales."""
+    _here(a_codes, "a_codes", cur)
+    _here(b_codes, "b_codes", cur)
+    a, b = a_codes.shape, b_codes.shape
+    if len(a) != 2 or len(b) != 2:
+        raise Fp4Error(("a" if len(a) != 2 else "b") + "_codes must be a contiguous 2-D uint8 tensor")
+    if a[1] != b[1]:
+        raise Fp4Error("operand shapes disagree")
+    _bytes2d(a_codes, "a_codes", cur, a)
+    _bytes2d(b_codes, "b_codes", cur, b)
+    _bytes2d(a_scales, "a_scales", cur, (a[0], a[1] // 16))
+    _bytes2d(b_scales, "b_scales", cur, (b[0], b[1] // 16))
+    return a[0], b[0], 2 * a[1]
+
+
+def _typed_out(t, shape, dtype, device, name, cur):
     """An output of bf16 or fp32 rows: returns (tensor, its leading dimension).
     `dtype` is that of one allocated here."""
     if t is None:
         if dtype not in _OUTPUT_TYPES:
             raise Fp4Error(f"{name} must be bf16 or fp32, not {dtype}")
         return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device), shape[1]
-    _here(t, name, torch.cuda.current_device())
+    _here(t, name, cur)
     if t.dtype not in _OUTPUT_TYPES or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
         raise Fp4Error(f"{name} must be bf16 or fp32 of shape {tuple(shape)} with unit column stride")
     return t, t.stride(0) if shape[0] > 1 else shape[1]
@@ -717,13 +733,13 @@ def fp4_gemm_act(a_codes, a_scales, b_codes, b_scales, act=FP4_ACT_NONE, bias=No
     """y = act(A B^T + bias) + residual in bf16 or fp32 (`dtype`, or y's own):
     returns (y, z), z the bf16 pre-activation where emit_z, else None."""
     cur = _current(a_codes, "a_codes")
-    m, n, k = _gemm_shapes([((a_codes, "a_codes"), (a_scales, "a_scales"), (b_codes, "b_codes"), (b_scales, "b_scales"))])
+    m, n, k = _operands(a_codes, a_scales, b_codes, b_scales, cur)
     shape = torch.Size((m, n))
     bias_p, bias_f32 = _bias(bias, n, cur)
     ldr = 0 if residual is None else _ld(residual, _rows2d(residual, "residual", cur, shape), n)
-    y, ldy = _typed_out(y, shape, dtype, a_codes.device, "y")
+    y, ldy = _typed_out(y, shape, dtype, a_codes.device, "y", cur)
     z = _out16(z, shape, a_codes.device, "z") if emit_z else None
-    _check(load().fp4_gemm_act(m, n, k, _p(a_codes), _p(a_scales), _p(b_codes), _p(b_scales), bias_p, bias_f32, int(act),
+    _check(load().fp4_gemm_act(m, n, k, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), bias_p, bias_f32, int(act),
                                _p(residual), ldr, _p(z), y.data_ptr(), 1 if y.dtype is torch.float32 else 0, ldy,
                                _raw_stream(cur)))
     return y, z
@@ -739,7 +755,7 @@ def fp4_matvec_act(x, w_codes, w_scales, act=FP4_ACT_NONE, x_scales=None, bias=N
     shape = torch.Size((m, n))
     bias_p, bias_f32 = _bias(bias, n, cur)
     ldr = 0 if residual is None else _ld(residual, _rows2d(residual, "residual", cur, shape), n)
-    y, ldy = _typed_out(y, shape, dtype, x.device, "y")
+    y, ldy = _typed_out(y, shape, dtype, x.device, "y", cur)
     _check(load().fp4_matvec_act(m, n, k, x.data_ptr(), ldx, _p(x_scales), w_codes.data_ptr(), w_scales.data_ptr(), bias_p,
                                  bias_f32, int(act), _p(residual), ldr, y.data_ptr(), 1 if y.dtype is torch.float32 else 0,
                                  ldy, _raw_stream(cur)))
@@ -774,7 +790,7 @@ def _index(t, name, shape, cur):
 
 def _out_index(t, shape, device, name, cur):
     if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=device)
+        return torch.empty_strided(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype=torch.int32, device=device)
     _index(t, name, shape, cur)
     return t
 
@@ -924,7 +940,7 @@ def fp4_gemm_experts(offsets, a_codes, a_scales, b_codes, b_scales, dtype=torch.
         if _expert_weights(pair[2], pair[3], "b2", cur) != (e, n, k) or _sorted_codes(offsets, pair[0], pair[1], "a2", e, k, cur) != rows:
             raise Fp4Error("operand shapes disagree")
         second = tuple(x.data_ptr() for x in pair)
-    c, ldc = _typed_out(c, torch.Size((rows, n)), dtype, a_codes.device, "c")
+    c, ldc = _typed_out(c, torch.Size((rows, n)), dtype, a_codes.device, "c", cur)
     _check(load().fp4_gemm_experts(e, rows, n, k, offsets.data_ptr(), a_codes.data_ptr(), a_scales.data_ptr(),
                                    b_codes.data_ptr(), b_scales.data_ptr(), *second, c.data_ptr(),
                                    1 if c.dtype is torch.float32 else 0, ldc, _raw_stream(cur)))
@@ -935,7 +951,7 @@ def fp4_gemm_experts_wgrad(offsets, a_codes, a_scales, b_codes, b_scales, dtype=
     """C_e = dec(A)[:, segment] dec(B)[:, segment]^T per expert, from column-facing
     codes [m][tokens/2] and [n][tokens/2]: returns [experts][m][n]."""
     cur = _current(a_codes, "a_codes")
-    m, n, tokens = _gemm_shapes([((a_codes, "a_codes"), (a_scales, "a_scales"), (b_codes, "b_codes"), (b_scales, "b_scales"))])
+    m, n, tokens = _operands(a_codes, a_scales, b_codes, b_scales, cur)
     _here(offsets, "offsets", cur)
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise Fp4Error("offsets must be a vector of experts + 1 elements")
@@ -946,7 +962,7 @@ def fp4_gemm_experts_wgrad(offsets, a_codes, a_scales, b_codes, b_scales, dtype=
             raise Fp4Error("accumulate needs an output tensor")
         if dtype not in _OUTPUT_TYPES:
             raise Fp4Error(f"c must be bf16 or fp32, not {dtype}")
-        c = torch.empty((e, m, n), dtype=dtype, device=a_codes.device)
+        c = torch.empty_strided((e, m, n), (m * n, n, 1), dtype=dtype, device=a_codes.device)
     else:
         _here(c, "c", cur)
         if c.dtype not in _OUTPUT_TYPES or c.shape != (e, m, n) or not c.is_contiguous():

@@ -13,14 +13,13 @@ constexpr float kLog2e = 0x1.715476p+0f;
 constexpr float kTanhC = -2.30220818f;                   // -2 sqrt(2/pi) log2(e)
 constexpr float kTanhA = 0.044715f;
 
-// Normal distribution function at -a, 0 <= a <= 16, as 2^P(a): P is a weighted
+// Normal distribution function at -a, a >= 0, as 2^P(a): P is a weighted
 // least-squares fit of log2(erfc(a / sqrt 2) / 2), the weights sharpened until
 // the largest error of the function and of a times it was least.  In fp32
 // arithmetic both are within 2.9e-7, and the function within 4e-4 of itself up to
-// a = 4.5 (a bf16 rounding is up to 4e-3); at 16 it is 0.  A fit of degree 9 in
+// a = 4.5 (a bf16 rounding is up to 4e-3); from 16 on it is 0.  A fit of degree 9 in
 // 1 / (1 + c a), with its reciprocal and one multiplication more, made the
 // epilogue of 8192 x 14336 16 us longer at no gain in the rounded result.
-constexpr float kTailEnd = 16.0f;
 __device__ __forceinline__ float normal_tail(float a) {
   float p = -0x1.b4df74p-21f;
   p = __builtin_fmaf(p, a, 0x1.51375ap-15f);
@@ -44,9 +43,9 @@ template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == FP4_ACT_RELU) return z <= 0.0f ? 0.0f : z;
   if constexpr (ACT == FP4_ACT_GELU) {
-    // z for positive z, less |z| times the tail on both sides
-    const float a = fminf(fabsf(z), kTailEnd);
-    return __builtin_fmaf(-a, normal_tail(a), z <= 0.0f ? 0.0f : z);
+    // z for positive z, less |z| times the tail on both sides (which is 0 from 16
+    // on; a NaN comes with the tail)
+    return __builtin_fmaf(-fminf(fabsf(z), 16.0f), normal_tail(fabsf(z)), fmaxf(z, 0.0f));
   }
   if constexpr (ACT == FP4_ACT_GELU_TANH)
     return times_gate(z, sigmoid_of_exponent(__fmul_rn(kTanhC, __builtin_fmaf(__fmul_rn(__fmul_rn(z, z), z), kTanhA, z))));
@@ -62,7 +61,7 @@ __device__ __forceinline__ float act_slope(float z) {
   const float x = __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f);
   float d = 1.0f;
   if constexpr (ACT == FP4_ACT_GELU) {
-    const float q = normal_tail(fminf(fabsf(x), kTailEnd));
+    const float q = normal_tail(fabsf(x));
     const float density = __fmul_rn(0.39894228f, exp2_hw(__fmul_rn(__fmul_rn(x, x), -0.5f * kLog2e)));
     d = __builtin_fmaf(x, density, x < 0.0f ? q : __fsub_rn(1.0f, q));
   } else if constexpr (ACT == FP4_ACT_GELU_TANH) {

@@ -100,12 +100,7 @@ __global__ __launch_bounds__(kSortThreads) void expert_sort_kernel(SortArgs a) {
   }
   // first row of the expert: sum of the padded totals of the earlier ones
   const uint32_t padded = (total + a.align - 1) / a.align * a.align;
-  uint32_t sum = padded;
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const uint32_t other = __shfl_up(sum, s, 64);
-    sum += lane >= s ? other : 0u;
-  }
+  const uint32_t sum = wave_prefix_sum(padded);
   if (lane == 63) wave_sum[wave] = sum;
   __syncthreads();
   uint32_t start = sum - padded;

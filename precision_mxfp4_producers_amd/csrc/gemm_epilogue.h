@@ -28,7 +28,10 @@ __device__ __forceinline__ void put_row(uint16_t* p, const float (&v)[W], int st
   typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
   words o;
 #pragma unroll
-  for (int u = 0; u < W / 2; ++u) o[u] = bf16_pack2_rne(v[2 * u], v[2 * u + 1]);
+  for (int u = 0; u < W / 2; ++u) {
+    const bf16x2_t b = {(__bf16)v[2 * u], (__bf16)v[2 * u + 1]};   // a NaN stays one
+    o[u] = __builtin_bit_cast(uint32_t, b);
+  }
   put(reinterpret_cast<words*>(p), o, stream);
 }
 

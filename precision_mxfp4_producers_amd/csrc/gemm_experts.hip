@@ -41,26 +41,20 @@ __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int experts,
     lo = std::min(std::max(offsets[std::min(e, experts)] & -unit, 0), rows);
     hi = e < experts ? std::min(std::max(offsets[std::min(e + 1, experts)] & -unit, lo), rows) : (e == experts ? rows : lo);
   };
-  // tiles_m of the experts of a turn, summed up to and with each lane's
+  // row tiles of the experts of a turn, summed up to and with each lane's
   const auto count = [&](int at, int& lo, int& hi, int& mine) {
     segment(at + lane, lo, hi);
     mine = (hi - lo + BM - 1) / BM;
-    int sum = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int other = __shfl_up(sum, s, 64);
-      sum += lane >= s ? other : 0;
-    }
-    return sum;
+    return wave_prefix_sum(mine);
   };
-  int lo, hi, mine, total = 0;
-  for (int at = 0; at <= experts; at += 64) total += __shfl(count(at, lo, hi, mine), 63, 64);
+  int lo, hi, mine, sum = 0, total = 0;
+  for (int at = 0; at <= experts; at += 64) total += __builtin_amdgcn_readlane(sum = count(at, lo, hi, mine), 63);
   total *= tiles_n;
   const int share = (total + 7) >> 3, l = (pid & 7) * share + (pid >> 3);
   if ((pid >> 3) >= share || l >= total) return false;
   int before = 0;                                        // row tiles of earlier turns
   for (int at = 0; at <= experts; at += 64) {
-    const int sum = count(at, lo, hi, mine);
+    if (experts >= 64) sum = count(at, lo, hi, mine);    // one turn: as it stands
     const uint64_t behind = __builtin_amdgcn_ballot_w64(l < (before + sum) * tiles_n);
     if (behind) {
       const int src = __builtin_ctzll(behind);
@@ -74,7 +68,7 @@ __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int experts,
       t.tn = __builtin_amdgcn_readfirstlane(rest / height);
       return true;
     }
-    before += __shfl(sum, 63, 64);
+    before += __builtin_amdgcn_readlane(sum, 63);
   }
   return false;
 }

@@ -34,12 +34,7 @@ __device__ __forceinline__ bool expert_unit(const ExpertRows& x, int unit, int& 
     const int lo = std::min(std::max(x.offsets[std::min(e, x.experts)], 0), x.rows);
     const int hi = std::min(std::max(x.offsets[std::min(e + 1, x.experts)], lo), x.rows);
     const int mine = (hi - lo + kUnitRows - 1) / kUnitRows;
-    int sum = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int other = __shfl_up(sum, s, 64);
-      sum += lane >= s ? other : 0;
-    }
+    const int sum = wave_prefix_sum(mine);
     const uint64_t behind = __builtin_amdgcn_ballot_w64(unit < before + sum);
     if (behind) {
       const int src = __builtin_ctzll(behind);
@@ -49,7 +44,7 @@ __device__ __forceinline__ bool expert_unit(const ExpertRows& x, int unit, int& 
       count = std::min(__builtin_amdgcn_readlane(hi, src) - first, kUnitRows);
       return true;
     }
-    before += __shfl(sum, 63, 64);
+    before += __builtin_amdgcn_readlane(sum, 63);
   }
   return false;
 }
