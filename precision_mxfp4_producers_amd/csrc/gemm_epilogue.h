@@ -63,6 +63,9 @@ __device__ __forceinline__ void store_epilogue_as(uint8_t* smem, const v16f (&ac
   constexpr int W = T::kPer, PASSES = 64 / T::kCols;
   uint8_t* const buf = smem + wave * T::kSlice;
   const int r = lane & 31, rr0 = lane >> 3, ch = lane & 7;
+  // sub-tiles past the last row or column: a small product's last tile
+  const int live_rows = (int)min(M - (m0 + wm * 128), (int64_t)128);
+  if (live_rows <= 0 || n0 + wn * 64 >= N) return;
   float b[PASSES][W];
   uint32_t res[4][PASSES][4][W / 2];
   if constexpr (!PLAIN) {
@@ -105,6 +108,7 @@ __device__ __forceinline__ void store_epilogue_as(uint8_t* smem, const v16f (&ac
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (32 * i >= live_rows) break;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       const int64_t row0 = m0 + wm * 128 + 32 * i + rr0, col = n0 + wn * 64 + p * T::kCols + W * ch;
