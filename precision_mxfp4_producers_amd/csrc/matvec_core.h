@@ -197,7 +197,7 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
 //                 with words 27.)
 constexpr int kByteScales = 0, kWholeScales = 1, kWordScales = 2;
 constexpr int kLds = 160 * 1024;
-constexpr int kStageBytes = 143 * 1024;                  // most of x in LDS; the rest is the partial sums'
+constexpr int kStagedXBytes = 143 * 1024;                  // most of x in LDS; the rest is the partial sums'
 constexpr int kXPitch = 256 + 64;                        // of a wave's own step of x
 // A wave's own room: 16 MT rows of a step; its partial sums take the same place.
 __host__ __device__ constexpr int room_bytes(int mt) { return 16 * mt * kXPitch; }
@@ -641,7 +641,7 @@ template <int WT, bool GATE, int PART = kByteScales, bool MANY = true, typename 
 static void matvec_variant(const MatvecArgs& a, int64_t cus, F&& launch) {
   constexpr int ROWS = GATE ? 8 : 16;
   const int64_t tiles = (a.n + ROWS - 1) / ROWS, steps = (a.k + 127) / 128;
-  const bool staged = a.m <= 16 && a.m * stage_pitch(a.k) <= kStageBytes;
+  const bool staged = a.m <= 16 && a.m * stage_pitch(a.k) <= kStagedXBytes;
   const int mt = (a.m + 15) / 16, nw = mt > 1 ? 8 : 16;
   // Where x is not staged its way through LDS bounds the kernel (110 cycles a
   // step and 16 rows): two tiles of W a wave share it, if there are as many for

@@ -107,7 +107,10 @@ def test_gather_takes_slots_of_no_token_for_padding(gpu_lib):
     assert np.array_equal(host(xs.view(torch.int16)).view(np.uint16), want)
 
 
-@pytest.mark.parametrize("t,k,e,d,align", [(2500, 6, 40, 2080, 32), (4100, 2, 8, 4160, 1), (450, 70, 90, 1024, 32)])
+MANY_ROWS = [(2500, 6, 40, 2080, 32), (4100, 2, 8, 4160, 1), (450, 70, 90, 1024, 32)]
+
+
+@pytest.mark.parametrize("t,k,e,d,align", MANY_ROWS)
 def test_gather_of_many_rows(gpu_lib, t, k, e, d, align):
     """Past the size from which the rows go out token by token: the same bytes, rows without a token zero."""
     x = synthetic.tensor((t, d), seed=d)

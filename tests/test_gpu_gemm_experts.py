@@ -7,11 +7,13 @@ import pytest
 import torch
 
 import synthetic
+from oracle import act as A
 from oracle import experts as X
 from oracle import formats as F
 from oracle import gemm as G
 from oracle import norm as N
 from oracle import quant as Q
+from test_gpu_matvec_variants import KINDS, SHAPES
 
 pytestmark = pytest.mark.gpu
 H = 2.0 ** -8                                            # half a bf16 step
@@ -206,24 +208,115 @@ def test_few(gpu_lib, sizes, n, k, align, extra, kind):
     assert (host(out)[:, n:] == 7).all() and (host(got)[offsets[-1]:] == 0).all()
 
 
+FEW_GATED = [((1,), 8, 32), ((1,), 1, 32), ((0, 2, 1), 17, 96), ((16, 17, 33), 48, 128), ((2, 2), 1500, 4096), ((20, 3), 40, 8192),
+             ((3,) * 66, 24, 544)]
+
+
+def check_gate(got, want, x64, w13):
+    """Two h of the same rows by different splits of the fp32 sums.  The sums a and
+    b are each within 1e-5 sum |x w| of their values, so that two differ by twice
+    that, which moves h by 1.1 |b| times a's and |silu(a)| times b's (silu' is below
+    1.1).  They may then round to neighbouring bf16 values: d ln silu(a) / d ln a = 1
+    + a (1 - sig(a)) lies within 1 + |a|, so that one step of a, 2 H of it, moves
+    ln |h| by 2 H (1 + |a|) at most, a step of b and h's own by 2 H each."""
+    f = len(w13) // 2
+    a, b = x64 @ w13[:f].T, x64 @ w13[f:].T
+    ea, eb = abs(x64) @ abs(w13[:f]).T, abs(x64) @ abs(w13[f:]).T
+    tol = 2e-5 * (1.1 * abs(b) * ea + abs(A.value(a, A.SILU)) * eb + 2e-5 * ea * eb)
+    got, want = host(got), host(want)
+    steps = np.exp(2 * H * (3 + 1.01 * abs(a)))
+    assert (np.abs(got - want) <= (steps - 1) * np.abs(want) + steps * tol + 2.0 ** -130).all()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-@pytest.mark.parametrize("sizes,f,d", [((1,), 8, 32), ((0, 2, 1), 17, 96), ((16, 17, 33), 48, 128), ((2, 2), 1500, 4096), ((20, 3), 40, 8192),
-                                       ((3,) * 66, 24, 544)])
+@pytest.mark.parametrize("sizes,f,d", FEW_GATED)
 def test_few_gated_rows_are_those_of_the_plain_call(gpu_lib, sizes, f, d, kind):
-    """h of each row against fp4_swiglu_matvec on it: another split of the fp32
-    sums may move a, b and h by a rounding."""
+    """h of each row against fp4_swiglu_matvec on it."""
     offsets, rows = segments(sizes, 1)
     rows += 2
     bits = synthetic.tensor((rows, d), seed=d)
-    x, scales = dev(bits.view(np.int16)).view(torch.bfloat16), None
+    x64, x, scales = F.bf16_bits_to_f64(bits), dev(bits.view(np.int16)).view(torch.bfloat16), None
     if kind == "e4m3":
-        x, scales = map(dev, N.encode_e4m3(bits))
+        x64, (x, scales) = N.decode_e4m3(*N.encode_e4m3(bits)), map(dev, N.encode_e4m3(bits))
     w = [dev(t) for t in codes((len(sizes), 2 * f, d), 2)]
     got = gpu_lib.fp4_swiglu_matvec_experts(dev(offsets), x, *w, x_scales=scales)
     assert (host(got)[offsets[-1]:] == 0).all()
     for i in range(len(sizes)):
         for lo in range(offsets[i], offsets[i + 1], 64):
             at = slice(lo, min(lo + 64, offsets[i + 1]))
-            want = host(gpu_lib.fp4_swiglu_matvec(x[at], w[0][i], w[1][i], x_scales=None if scales is None else scales[at]))
-            # a's rounding moves h by at most 1.1 |a|-relative steps, b's and h's own by one each
-            assert (np.abs(host(got[at]) - want) <= 4 * 2 * H * np.abs(want) + 1e-6).all()
+            want = gpu_lib.fp4_swiglu_matvec(x[at], w[0][i], w[1][i], x_scales=None if scales is None else scales[at])
+            check_gate(got[at], want, x64[at], F.decode(host(w[0][i]), host(w[1][i])))
+
+
+# rows a unit, output columns, K: scales one byte off a word, K of whole and part steps, x staged or not
+UNALIGNED = [(1, 1, 64), (2, 40, 128), (3, 33, 160), (1, 70, 512), (2, 300, 544), (16, 64, 1024), (5, 200, 2080), (16, 48, 8192), (20, 33, 8224),
+             (1, 9000, 512), (1, 16400, 1056)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("m,n,k", UNALIGNED)
+def test_few_with_scales_off_words(gpu_lib, m, n, k, kind):
+    """Weight scales that start one byte off a word (a view into a larger buffer), plain, gated and with an epilogue."""
+    bits = synthetic.tensor((3 * m, k), seed=k)
+    x64, x, scales = F.bf16_bits_to_f64(bits), dev(bits.view(np.int16)).view(torch.bfloat16), None
+    if kind == "e4m3":
+        c, s = N.encode_e4m3(bits)
+        x64, x, scales = N.decode_e4m3(c, s), dev(c), dev(s)
+    offsets = dev(np.array([0, m, m, 3 * m], np.int32))
+
+    def off(a):
+        buf = torch.zeros(a.size + 1, dtype=torch.uint8, device="cuda")
+        buf[1:] = dev(a).reshape(-1)
+        return buf[1:].reshape(a.shape)
+
+    w = codes((3, n, k), 2)
+    wd = [F.decode(w[0][i], w[1][i]) for i in range(3)]
+    ref, e = np.zeros((2, 3 * m, n))
+    for i, at in ((0, slice(0, m)), (2, slice(m, 3 * m))):
+        ref[at], e[at] = x64[at] @ wd[i].T, abs(x64[at]) @ abs(wd[i]).T
+    check(gpu_lib.fp4_matvec_experts(offsets, x, dev(w[0]), off(w[1]), x_scales=scales), ref, e, k)
+    few = slice(0, m)
+    got = gpu_lib.fp4_matvec_act(x[few], dev(w[0][0]), off(w[1][0]), x_scales=None if scales is None else scales[few], dtype=torch.float32)
+    check(got, ref[few], e[few], k)
+    w = codes((3, 2 * n, k), 3)
+    want = gpu_lib.fp4_swiglu_matvec_experts(offsets, x, dev(w[0]), dev(w[1]), x_scales=scales)
+    got = gpu_lib.fp4_swiglu_matvec_experts(offsets, x, dev(w[0]), off(w[1]), x_scales=scales)
+    for i, at in ((0, slice(0, m)), (2, slice(m, 3 * m))):
+        check_gate(got[at], want[at], x64[at], F.decode(w[0][i], w[1][i]))
+
+
+# and items of four steps with scales off words, or ending in a part step
+VARIANTS = SHAPES + [(3, 14336, 2048, 1), (2, 14337, 1952, 0)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n,k,off", VARIANTS)
+def test_few_row_variants(gpu_lib, m, n, k, off, kind):
+    """The shapes that reach every variant of the plain few-row products, for the
+    one with an epilogue and, up to sixteen rows, for one expert's rows."""
+    bits = synthetic.tensor((m, k), seed=k)
+    x64, x, scales = F.bf16_bits_to_f64(bits), dev(bits.view(np.int16)).view(torch.bfloat16), None
+    if kind == "e4m3":
+        c, s = N.encode_e4m3(bits)
+        x64, x, scales = N.decode_e4m3(c, s), dev(c), dev(s)
+
+    def at(a):
+        buf = torch.zeros(a.size + off, dtype=torch.uint8, device="cuda")
+        buf[off:] = dev(a).reshape(-1)
+        return buf[off:].reshape(a.shape)
+
+    w = codes((1, n, k), 2)
+    W = torch.from_numpy(F.decode(w[0][0], w[1][0])).cuda()
+    X = torch.from_numpy(np.ascontiguousarray(x64)).cuda()
+    ref, e = host(X @ W.t()), host(X.abs() @ W.abs().t())
+    wc, ws = dev(w[0]), at(w[1])
+    check(gpu_lib.fp4_matvec_act(x, wc[0], ws[0], x_scales=scales, dtype=torch.float32), ref, e, k)
+    if m > 16:
+        return
+    offsets = dev(np.array([0, m], np.int32))
+    check(gpu_lib.fp4_matvec_experts(offsets, x, wc, ws, x_scales=scales), ref, e, k)
+    w = codes((1, 2 * n, k), 3)
+    wc, ws = dev(w[0]), at(w[1])
+    got = gpu_lib.fp4_swiglu_matvec_experts(offsets, x, wc, ws, x_scales=scales)
+    want = gpu_lib.fp4_swiglu_matvec(x, wc[0], ws[0], x_scales=scales)
+    check_gate(got, want, x64, F.decode(w[0][0], w[1][0]))
