@@ -664,12 +664,16 @@ static void matvec_variant(const MatvecArgs& a, int64_t cus, F&& launch) {
   int64_t best = INT64_MAX;
   const auto groups_of = [&](int log2) { return (tiles + nt * (nw >> log2) - 1) / (nt * (nw >> log2)); };
   constexpr int kMaxU = WT == kMx ? 4 : 2;               // what the registers hold
+  // With word scales, whose items need not divide K, a turn counts as a step more:
+  // its loads' latency (64 experts' 2048 x 1056 or 1312, three rows each: 27 us with
+  // items of one step, 24 of four; 2048 x 2080: 41, of two 36).
+  constexpr int kTurn = PART == kWordScales ? 1 : 0;
   for (int uu = staged ? kMaxU : 1; uu >= 1; uu >>= 1) {
     if (uu > 1 && PART == kByteScales && (a.k % (128 * uu) != 0 || !words)) continue;
     for (int log2 = 2; log2 <= (nw == 16 ? 4 : 3); ++log2) {
       const int64_t rounds = (groups_of(log2) + cus - 1) / cus;
       const int64_t cost =
-          rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2) * uu + (rounds + batch - 1) / batch;
+          rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2) * (uu + kTurn) + (rounds + batch - 1) / batch;
       if (cost < best) best = cost, u = uu, kw = log2;
     }
   }
