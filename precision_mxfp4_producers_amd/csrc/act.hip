@@ -158,7 +158,7 @@ fp4_status fp4_act_backward(int64_t m, int64_t n, const void* dy, fp4_dtype dy_t
   if (partial && workspace_bytes < fp4_act_backward_workspace(m, n)) return FP4_ESHAPE;
   if (partial && !workspace) return FP4_EINVAL;
   const ActGradArgs a{dy, lddy, z, ldz, dz, partial ? static_cast<float*>(workspace) : dbias, m, n, p.rows,
-                      partial ? 0 : accumulate, streams(m * n * 2)};
+                      partial ? 0 : accumulate, streams(m, n * 2)};
   const bool f32 = dy_type == FP4_F32;
   hipStream_t s = as_stream(stream);
   switch (act) {

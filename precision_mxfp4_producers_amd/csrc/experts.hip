@@ -407,7 +407,7 @@ constexpr int64_t kMostGroups = 1 << 22;
 // then takes one launch.
 static int sort_groups(int64_t slots, int64_t& chunk) {
   constexpr int64_t kOne = 8192, kMost = 256;
-  int64_t groups = slots <= kOne ? 1 : std::min((slots + 4095) / 4096, kMost);
+  int64_t groups = slots <= kOne ? 1 : std::min((slots + 2047) / 2048, kMost);
   chunk = std::max<int64_t>((slots + groups - 1) / groups + kSortThreads - 1, kSortThreads) / kSortThreads * kSortThreads;
   return (int)std::max<int64_t>((slots + chunk - 1) / chunk, 1);
 }
@@ -498,7 +498,7 @@ fp4_status fp4_expert_gather(int64_t t, int64_t k, int64_t d, int64_t rows, cons
       (reinterpret_cast<uintptr_t>(workspace) & 3))
     return FP4_EALIGN;
   GatherArgs a{x, ldx, slots, (int)rows, (int)t, (int)k, (int)d, xs, codes, scales, format == FP4_E4M3,
-               streams(rows * d * 2), static_cast<int32_t*>(workspace), 0};
+               streams(rows, d * 2), static_cast<int32_t*>(workspace), 0};
   hipStream_t s = as_stream(stream);
   if (by_tokens) {
     hipLaunchKernelGGL(expert_where_kernel, dim3((unsigned)std::min((rows + 255) / 256, kMostGroups)), dim3(256), 0, s, a);

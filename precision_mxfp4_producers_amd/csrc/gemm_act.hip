@@ -53,7 +53,7 @@ fp4_status fp4_gemm_act(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
     return FP4_EALIGN;
   const bool f32 = y_type == FP4_F32;
   const Epilogue e{y, ldy, bias, residual, ldr, z, (int)act, f32, bias_type == FP4_F32, 0,
-                   streams(m * n * ((f32 ? 4 : 2) + (z ? 2 : 0)))};
+                   streams(m, n * ((f32 ? 4 : 2) + (z ? 2 : 0)))};
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(kFastThreads), 0, as_stream(stream), m, n, k, a_codes,
                        a_scales, b_codes, b_scales, e);

@@ -166,8 +166,9 @@ __global__ __launch_bounds__(kFastThreads) void swiglu_experts_kernel(ExpertsArg
 // that of the rows behind the last), times the column tiles, in eights (one of
 // each for an XCD); -1 past a grid.
 static int64_t experts_grid(int64_t rows, int64_t experts, int64_t n, int64_t bn) {
+  if (n > kMaxExpertRows) return -1;
   const int64_t tm = rows / BM + std::min(experts + 1, rows), tn = (n + bn - 1) / bn;
-  return n > kMaxExpertRows || tm > 0x7FFFFFF0 / tn ? -1 : (tm * tn + 7) / 8 * 8;
+  return tm > 0x7FFFFFF0 / tn ? -1 : (tm * tn + 7) / 8 * 8;
 }
 
 static bool operands_aligned(const uint8_t* c, const uint8_t* s) { return aligned16(c) && aligned16(s); }
@@ -203,7 +204,7 @@ fp4_status fp4_gemm_experts(int64_t experts, int64_t rows, int64_t n, int64_t k,
   e.y = c;
   e.ldy = ldc;
   e.y_f32 = c_type == FP4_F32;
-  e.stream = streams(rows * n * (e.y_f32 ? 4 : 2));
+  e.stream = streams(rows, n * (e.y_f32 ? 4 : 2));
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kFastThreads), 0, as_stream(stream), a, e);
   };
@@ -232,7 +233,7 @@ fp4_status fp4_gemm_experts_wgrad(int64_t experts, int64_t tokens, int64_t m, in
   e.ldy = n;
   e.y_f32 = c_type == FP4_F32;
   e.accumulate = accumulate;
-  e.stream = streams(experts * m * n * (e.y_f32 ? 4 : 2));
+  e.stream = streams(experts * m, n * (e.y_f32 ? 4 : 2));
   hipLaunchKernelGGL(gemm_experts_wgrad_kernel, dim3((unsigned)(tiles * experts)), dim3(kFastThreads), 0, as_stream(stream),
                      offsets, tokens, m, n, a_codes, a_scales, b_codes, b_scales, e);
   return launch_status();

@@ -84,8 +84,8 @@ __global__ __launch_bounds__(256) void matvec_experts_small_kernel(MatvecArgs a,
     const int64_t r = i / a.n, col = i % a.n;
     float v = 0.0f, w = 0.0f;
     int e = 0;
-    while (e < x.experts && !(r >= x.offsets[e] && r < x.offsets[e + 1])) ++e;
-    if (e < x.experts) {
+    while (a.k > 0 && e < x.experts && !(r >= x.offsets[e] && r < x.offsets[e + 1])) ++e;
+    if (a.k > 0 && e < x.experts) {
       const int64_t weights = e * (GATE ? 2 : 1) * a.n * a.k;
       a.codes = codes + (weights >> 1);
       a.scales = scales + (weights >> 5);

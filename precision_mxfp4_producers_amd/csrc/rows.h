@@ -53,7 +53,7 @@ __device__ __forceinline__ void put(T* p, const T& v, int stream) {
 
 // An output that cannot stay in the 256 MB Infinity Cache for its reader goes
 // past it (the plain product's rule).
-inline bool streams(int64_t bytes) { return bytes > ((int64_t)192 << 20); }
+inline bool streams(int64_t rows, int64_t row_bytes) { return row_bytes > 0 && rows > ((int64_t)192 << 20) / row_bytes; }
 
 // ---------------------------------------------------------------- E4M3 codes
 // Upward exponent for E4M3 (largest magnitude 448 = 1.75 * 2^8) of a finite
