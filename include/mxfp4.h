@@ -839,7 +839,8 @@ fp4_status fp4_swiglu_producer_experts(int64_t experts, int64_t rows, int64_t f,
 /*
  * fp4_matvec and fp4_swiglu_matvec on sorted rows, each with its expert's
  * weights: the form for a few decoded tokens, which reads the weights of the
- * experts that have rows, once for every sixteen of them.  Rows behind the last
+ * experts that have rows, once for every sixteen of them (fewer where K is above
+ * 4480 and LDS does not hold sixteen).  Rows behind the last
  * segment get 0.
  *   x        bf16 [rows][ldx], or E4M3 [rows][k] with x_scales [rows][k/32]
  *   w_codes  [experts][n][k/2], w_scales [experts][n][k/32]; w13: [experts][2f]

@@ -292,9 +292,9 @@ constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 0xF) | ((vm >> 4) << 
 // column (kWhole):
 //   kWindow  the 32-value blocks lo .. lo + count - 1 of the operands' rows, in
 //            K steps from `first` on (lo lies in the first): lanes whose
-//            16-byte code chunk, one block, lies outside read zero codes,
-//            whose products are zero under any finite scale.  K (the row
-//            length) is at least 256.
+//            16-byte code chunk, one block, lies outside read zero codes;
+//            their scale bytes are cleared, since another block's may stand for
+//            no number.  K (the row length) is at least 256.
 //   kShort   the same for rows of less than 256 values (one K step), whose
 //            scale bytes come one by one.
 // A K step's eight scale bytes come with one load that stays inside the row:
@@ -445,12 +445,15 @@ __device__ __forceinline__ uint2 load_scales(const FastPlan& p, __amdgpu_buffer_
   }
 }
 
-// Those bytes in place: a load that was moved back is shifted.
+// Those bytes in place: a load that was moved back is shifted, and the bytes of
+// blocks outside the K range are cleared.
 template <int kMode>
 __device__ __forceinline__ uint2 placed_scales(const FastPlan& p, uint2 s, int kit) {
   if constexpr (kMode != kWindow) return s;
   const int moved = max(8 * kit - (p.row_scales - 8), 0);
-  return __builtin_bit_cast(uint2, __builtin_bit_cast(uint64_t, s) >> (8 * moved));
+  const int from = max(p.kr.lo - 8 * kit, 0), to = min(p.kr.lo + p.kr.count - 8 * kit, 8);   // bytes of the range
+  const uint64_t in = (~(uint64_t)0 << (8 * from)) & (~(uint64_t)0 >> (8 * (8 - to)));
+  return __builtin_bit_cast(uint2, (__builtin_bit_cast(uint64_t, s) >> (8 * moved)) & in);
 }
 
 // Load j of a part reads 8 rows further down.  The row offset stays in the

@@ -190,8 +190,8 @@ __device__ __forceinline__ void decode_x16(const v4i w, uint32_t sc, bf16x8_t& a
 //                 like the codes, and reach the other lanes of a row by permutes.
 //   kWordScales   MXFP4, any K and alignment: the same with unaligned words; one
 //                 that would end behind the scales is moved back and shifted (they
-//                 are four bytes at least).  Its other bytes may be those of the
-//                 next row, and meet zero codes.
+//                 are four bytes at least).  Bytes behind the row's own are
+//                 cleared.
 //   kByteScales   any K, one step an item: each lane loads the bytes that its
 //                 products take.  (64 experts' 2048 x 1056, three rows each: 33 us,
 //                 with words 27.)
@@ -282,6 +282,10 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
   const auto row_of = [&](int64_t group, int j, int r) {
     return std::min(((group * RT + rt) * NT + j) * ROWS + (r & (ROWS - 1)), a.n - 1) + (GATE && r >= ROWS ? a.n : 0);
   };
+  // kWordScales: the bytes of a row's last words that are its own (another's may
+  // stand for no number).
+  const int own = (int)(a.k >> 5) - 4 * ((items - 1) * U + (lane & (U - 1)));
+  const uint32_t tail = own <= 0 ? 0u : 0xFFFFFFFFu >> (8 * (4 - std::min(own, 4)));
   const auto load_w = [&](MvItem<WT, NT, U, SC>& it, int64_t group, int turn) {
     const int item = item_of(turn), piece = lane & 3;
 #pragma unroll
@@ -367,7 +371,8 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
     if constexpr (SC != kByteScales)
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const uint32_t mine = SC == kWordScales ? it.s[j][0] >> it.s[j][SC == kWordScales ? 1 : 0] : it.s[j][0];
+        uint32_t mine = SC == kWordScales ? it.s[j][0] >> it.s[j][SC == kWordScales ? 1 : 0] : it.s[j][0];
+        if (SC == kWordScales && item == items - 1) mine &= tail;
 #pragma unroll
         for (int d = 0; d < kScaleWords<WT, U>; ++d)
           sw[j][d] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * (4 * (r & 3) + (r >> 2)) + d), (int)mine);
@@ -420,7 +425,7 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
   const float* const rf = reinterpret_cast<const float*>(lds);
   const auto finish = [&](int64_t group, int slots) {     // group: the first one since the last meeting
     lds_barrier();
-    const int split = plan.kw_log2 - 2, sums = 16 * NT * a.m;   // of a wave's tiles: 16 NT rows of W, m rows of x
+    const int split = std::max(plan.kw_log2 - 2, 0), sums = 16 * NT * a.m;   // of a wave's tiles: 16 NT rows of W, m rows of x
     const int count = (slots * RT * sums) << split;
     for (int e0 = wave * 64; e0 < count; e0 += NW * 64) {
       const int i = e0 + lane, part = i & ((1 << split) - 1);
@@ -436,7 +441,9 @@ __device__ __forceinline__ void matvec_body(const MatvecArgs& a, const MvPlan& p
       const int t = q & (RT - 1), slot = q / RT, wr = nl + ROWS * ab;
       const float* const p = rf + (slot * NW + (t << plan.kw_log2) + 4 * part) * kWaveFloats + ((mr >> 4) * NT + j) * 256 +
                              ((wr >> 2) * 16 + (mr & 15)) * 4 + (wr & 3);
-      float v = __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[kWaveFloats]), p[2 * kWaveFloats]), p[3 * kWaveFloats]);
+      float v = p[0];
+      if (plan.kw_log2 > 0) v = __fadd_rn(v, p[kWaveFloats]);
+      if (plan.kw_log2 > 1) v = __fadd_rn(__fadd_rn(v, p[2 * kWaveFloats]), p[3 * kWaveFloats]);
       for (int s = 1; s < 1 << split; s <<= 1) v = __fadd_rn(v, __shfl_xor(v, s, 64));
       const int64_t row = (((group + (int64_t)slot * gridDim.x) * RT + t) * NT + j) * ROWS + nl;
       if constexpr (GATE) {
@@ -663,17 +670,23 @@ static void matvec_variant(const MatvecArgs& a, int64_t cus, F&& launch) {
   int u = 1, kw = 4;
   int64_t best = INT64_MAX;
   const auto groups_of = [&](int log2) { return (tiles + nt * (nw >> log2) - 1) / (nt * (nw >> log2)); };
-  constexpr int kMaxU = WT == kMx ? 4 : 2;               // what the registers hold
-  // With word scales, whose items need not divide K, a turn counts as a step more:
-  // its loads' latency (64 experts' 2048 x 1056 or 1312, three rows each: 27 us with
-  // items of one step, 24 of four; 2048 x 2080: 41, of two 36).
-  constexpr int kTurn = PART == kWordScales ? 1 : 0;
+  // With word scales and x staged, whose items need not divide K and whose waves
+  // may have a tile of their own, a turn costs its steps and half a one (its
+  // loads' latency), the meetings next to nothing; four waves a tile where equal,
+  // else fewer.  Over 28 shapes this is 1.7% above the best of U = 1, 2, 4 and KW =
+  // 1 .. 16, at most 7%: 64 experts' 2048 x 1056, three rows each, 24.3 us (the
+  // rule above and items of four steps: 28.5), 64 gated 768 x 2048 29.3 (33.7), one
+  // row of 14336 x 4096 10.5 (12.4), of 4096 x 14336 11.8 (12.7).
+  constexpr int kMaxU = WT == kMx && PART != kWordScales ? 4 : 2;   // what the registers hold
+  const bool fine = PART == kWordScales && staged;
+  const int order[5] = {2, fine ? 1 : 3, fine ? 0 : 4, 3, 4};
   for (int uu = staged ? kMaxU : 1; uu >= 1; uu >>= 1) {
     if (uu > 1 && PART == kByteScales && (a.k % (128 * uu) != 0 || !words)) continue;
-    for (int log2 = 2; log2 <= (nw == 16 ? 4 : 3); ++log2) {
+    for (const int log2 : order) {
+      if ((nw >> log2) == 0) continue;
       const int64_t rounds = (groups_of(log2) + cus - 1) / cus;
-      const int64_t cost =
-          rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2) * (uu + kTurn) + (rounds + batch - 1) / batch;
+      const int64_t turns = rounds * (((steps + uu - 1) / uu + (1 << log2) - 1) >> log2);
+      const int64_t cost = fine ? turns * (2 * uu + 1) : turns * uu + (rounds + batch - 1) / batch;
       if (cost < best) best = cost, u = uu, kw = log2;
     }
   }

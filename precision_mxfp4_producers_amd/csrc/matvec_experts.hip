@@ -1,7 +1,7 @@
 // Few-row products of sorted tokens with their experts' weights
 // (fp4_matvec_experts, fp4_swiglu_matvec_experts).
 //
-// A unit is up to sixteen rows of one expert's segment; a row of workgroups
+// A unit is a few rows of one expert's segment, sixteen at most; a row of workgroups
 // takes one, and walks the expert's weights as the plain product does.  Which
 // units there are is known on the device only: a launch has as many rows of
 // workgroups as so many sorted rows can make, and the spare ones end at once.
@@ -21,9 +21,8 @@ namespace mx {
 struct ExpertRows {
   const int32_t* offsets;                                // [experts + 1]
   int experts, rows;
+  int unit;                                              // rows of a unit, 16 at most
 };
-
-constexpr int kUnitRows = 16;
 
 // First row, number of rows and expert of unit `unit`; false past the last.
 __device__ __forceinline__ bool expert_unit(const ExpertRows& x, int unit, int& expert, int& first, int& count) {
@@ -33,15 +32,15 @@ __device__ __forceinline__ bool expert_unit(const ExpertRows& x, int unit, int& 
     const int e = at + lane;
     const int lo = std::min(std::max(x.offsets[std::min(e, x.experts)], 0), x.rows);
     const int hi = std::min(std::max(x.offsets[std::min(e + 1, x.experts)], lo), x.rows);
-    const int mine = (hi - lo + kUnitRows - 1) / kUnitRows;
+    const int mine = (int)((uint32_t)(hi - lo + x.unit - 1) / (uint32_t)x.unit);
     const int sum = wave_prefix_sum(mine);
     const uint64_t behind = __builtin_amdgcn_ballot_w64(unit < before + sum);
     if (behind) {
       const int src = __builtin_ctzll(behind);
       const int in = unit - before - __builtin_amdgcn_readlane(sum, src) + __builtin_amdgcn_readlane(mine, src);
       expert = at + src;
-      first = __builtin_amdgcn_readlane(lo, src) + in * kUnitRows;
-      count = std::min(__builtin_amdgcn_readlane(hi, src) - first, kUnitRows);
+      first = __builtin_amdgcn_readlane(lo, src) + in * x.unit;
+      count = std::min(__builtin_amdgcn_readlane(hi, src) - first, x.unit);
       return true;
     }
     before += __builtin_amdgcn_readlane(sum, 63);
@@ -105,15 +104,21 @@ __global__ __launch_bounds__(256) void matvec_experts_small_kernel(MatvecArgs a,
 }
 
 template <int XT, bool GATE>
-static fp4_status matvec_experts_launch(MatvecArgs a, const ExpertRows& x, hipStream_t stream) {
+static fp4_status matvec_experts_launch(MatvecArgs a, ExpertRows x, hipStream_t stream) {
   if ((GATE ? 2 : 1) * a.n * (a.k / 32) < 4) {
     const int64_t grid = std::min<int64_t>((x.rows * a.n + 255) / 256, 65536);
     hipLaunchKernelGGL((matvec_experts_small_kernel<XT, GATE>), dim3((unsigned)grid), dim3(256), 0, stream, a, x);
     return launch_status();
   }
-  a.m = std::min(x.rows, kUnitRows);                     // of a unit, at most
-  // every expert that can have a row, and a unit more for every sixteen rows
-  const int experts = std::min(x.experts, x.rows), units = experts + x.rows / kUnitRows;
+  const int experts = std::min(x.experts, x.rows);       // that can have a row
+  // Long rows of which LDS does not hold sixteen: units of as many as it holds, if
+  // the experts have no more of them each, on average (8 experts' 4096 x 14336,
+  // four rows each: 86 to 60 us, one to twelve: 100 to 85; the weights of an expert
+  // with more are read again).
+  const int64_t held = std::min<int64_t>(kStagedXBytes / stage_pitch(a.k), 16);
+  x.unit = held > 0 && x.rows <= held * experts ? (int)held : 16;
+  a.m = std::min(x.rows, x.unit);
+  const int units = experts + x.rows / x.unit;           // a unit an expert, and one more for all its rows
   const int64_t cus = std::max<int64_t>(kMatvecGrid / experts, 1);
   matvec_variant<kMx, GATE, kWordScales, false>(a, cus, [&](auto v, const MvPlan& plan, unsigned grid) {
     using V = decltype(v);
@@ -149,7 +154,7 @@ fp4_status fp4_matvec_experts(int64_t experts, int64_t rows, int64_t n, int64_t 
   if (st != FP4_OK || rows == 0 || n == 0) return st;
   if (reinterpret_cast<uintptr_t>(c) & 3) return FP4_EALIGN;
   const MatvecArgs a{0, n, k, x, ldx, x_scales, w_codes, w_scales, nullptr, 0, c, ldc, 0, nullptr};
-  const ExpertRows r{offsets, (int)experts, (int)rows};
+  const ExpertRows r{offsets, (int)experts, (int)rows, 0};
   return x_scales ? matvec_experts_launch<kXE4m3, false>(a, r, as_stream(stream))
                   : matvec_experts_launch<kXBf16, false>(a, r, as_stream(stream));
 }
@@ -162,7 +167,7 @@ fp4_status fp4_swiglu_matvec_experts(int64_t experts, int64_t rows, int64_t f, i
   if (st != FP4_OK || rows == 0 || f == 0) return st;
   if (reinterpret_cast<uintptr_t>(h) & 1) return FP4_EALIGN;
   const MatvecArgs a{0, f, d, x, ldx, x_scales, w13_codes, w13_scales, nullptr, 0, nullptr, 0, 0, h};
-  const ExpertRows r{offsets, (int)experts, (int)rows};
+  const ExpertRows r{offsets, (int)experts, (int)rows, 0};
   return x_scales ? matvec_experts_launch<kXE4m3, true>(a, r, as_stream(stream))
                   : matvec_experts_launch<kXBf16, true>(a, r, as_stream(stream));
 }

@@ -178,7 +178,8 @@ def test_swiglu_producer(gpu_lib, sizes, f, d, extra):
 
 
 FEW = [((1,), 16, 32), ((0, 2), 17, 64), ((1, 0, 0, 1), 33, 96), ((16, 17, 33), 48, 128), ((3,) * 70, 20, 160), ((15, 1), 512, 1024),
-       ((40, 0, 5), 100, 2080), ((2, 2), 4100, 512), ((9, 64), 256, 4096), ((1, 1), 64, 14336), ((5, 20), 40, 8192), ((0, 0), 8, 64)]
+       ((40, 0, 5), 100, 2080), ((2, 2), 4100, 512), ((9, 64), 256, 4096), ((1, 1), 64, 14336), ((5, 20), 40, 8192), ((0, 0), 8, 64),
+       ((9, 1, 0, 7, 8), 200, 9600), ((6, 2, 2, 1), 33, 14336), ((1, 0, 3), 17, 73248)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
@@ -209,7 +210,7 @@ def test_few(gpu_lib, sizes, n, k, align, extra, kind):
 
 
 FEW_GATED = [((1,), 8, 32), ((1,), 1, 32), ((0, 2, 1), 17, 96), ((16, 17, 33), 48, 128), ((2, 2), 1500, 4096), ((20, 3), 40, 8192),
-             ((3,) * 66, 24, 544)]
+             ((3,) * 66, 24, 544), ((9, 2, 0, 4), 40, 8192)]
 
 
 def check_gate(got, want, x64, w13):
@@ -320,3 +321,70 @@ def test_few_row_variants(gpu_lib, m, n, k, off, kind):
     got = gpu_lib.fp4_swiglu_matvec_experts(offsets, x, wc, ws, x_scales=scales)
     want = gpu_lib.fp4_swiglu_matvec(x, wc[0], ws[0], x_scales=scales)
     check_gate(got, want, x64, F.decode(w[0][0], w[1][0]))
+
+
+@pytest.mark.parametrize("k", [96, 160, 1056, 2080])
+def test_a_weight_row_does_not_reach_its_neighbours(gpu_lib, k):
+    """Scale byte 255, which stands for no number, in one row of W: that column of
+    C may hold anything, the others stay as they are."""
+    n, bad = 40, [1, 17, 39]
+    bits = synthetic.tensor((3, k), seed=k)
+    x = dev(bits.view(np.int16)).view(torch.bfloat16)
+    c, s = codes((1, n, k), 2)
+    offsets = dev(np.array([0, 3], np.int32))
+    broken = s.copy()
+    broken[0, bad] = 255
+    good = np.setdiff1d(np.arange(n), bad)
+
+    def run(s):
+        y = [gpu_lib.fp4_matvec_experts(offsets, x, dev(c), dev(s)), gpu_lib.fp4_matvec_act(x, dev(c[0]), dev(s[0]), dtype=torch.float32),
+             gpu_lib.fp4_matvec(x, dev(c[0]), dev(s[0]))]
+        return [host(v)[:, good] for v in y]
+
+    for name, got, want in zip(("experts", "act", "plain"), run(broken), run(s)):
+        assert np.array_equal(got, want), name
+
+
+@pytest.mark.parametrize("n,k", [(32, 96), (64, 288), (256, 544)])
+def test_rows_and_weights_do_not_reach_their_neighbours(gpu_lib, n, k):
+    """The same of a row of A and of B in the long products."""
+    sizes = (40, 0, 33)
+    offsets, rows = segments(sizes, 1)
+    a, b = codes((rows, k), 1), codes((len(sizes), n, k), 2)
+    ab, bb = a[1].copy(), b[1].copy()
+    ab[[0, 41, rows - 1]] = 255
+    bb[0, [0, n - 1]], bb[2, 7] = 255, 255
+    ok = np.zeros((rows, n), bool)
+    ok[:40, 1:n - 1] = True
+    ok[40:] = np.arange(n) != 7
+    ok[[0, 41, rows - 1]] = False
+
+    def run(sa, sb):
+        got = [host(gpu_lib.fp4_gemm_experts(dev(offsets), dev(a[0]), dev(sa), dev(b[0]), dev(sb)))[ok]]
+        y = host(gpu_lib.fp4_gemm_act(dev(a[0]), dev(sa), dev(b[0][0]), dev(sb[0]), dtype=torch.float32)[0])
+        good = np.ones((rows, n), bool)
+        good[[0, 41, rows - 1]], good[:, [0, n - 1]] = False, False
+        return got + [y[good]]
+
+    for got, want in zip(run(ab, bb), run(a[1], b[1])):
+        assert np.isfinite(want).all() and np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("sizes", [(32, 64, 32), (96, 32, 0, 160, 224), (288, 32, 512)])
+def test_tokens_do_not_reach_other_experts(gpu_lib, sizes):
+    """Scale bytes that stand for no number in one expert's tokens (a NaN in its
+    activations or gradients) leave the other experts' weight gradients as they are."""
+    offsets, tokens = segments(sizes, 32)
+    m, n = 64, 96
+    pad = -tokens % 256
+    a, b = codes((m, tokens + pad), 1), codes((n, tokens + pad), 2)
+    for e in range(len(sizes)):
+        at = slice(offsets[e] // 32, offsets[e + 1] // 32)
+        sa, sb = a[1].copy(), b[1].copy()
+        sa[:, at], sb[3, at] = 255, 255
+        sa[:, tokens // 32:], sb[:, tokens // 32:] = 255, 255
+        for dtype in (torch.float32, torch.bfloat16):
+            want = host(gpu_lib.fp4_gemm_experts_wgrad(dev(offsets), dev(a[0]), dev(a[1]), dev(b[0]), dev(b[1]), dtype=dtype))
+            got = host(gpu_lib.fp4_gemm_experts_wgrad(dev(offsets), dev(a[0]), dev(sa), dev(b[0]), dev(sb), dtype=dtype))
+            others = [i for i in range(len(sizes)) if i != e]
+            assert np.array_equal(got[others], want[others])
