@@ -683,7 +683,7 @@ int64_t fp4_act_backward_workspace(int64_t m, int64_t n);
  * whose blocks hold 32 tokens; align = 1 packs the rows for the few-row
  * products.  Sorted tensors have `capacity` rows; those behind the last segment
  * belong to no expert.  All of it stays on the device: no call waits for the
- * counts.
+ * counts.  offsets[0] is 0: rows before the first segment are left as they were.
  *   offsets [experts + 1] int32
  *   slots   [capacity] int32: the slot in a row, -1 where there is none
  *   rows    [t][k] int32: the row of a slot, -1 where it is not routed

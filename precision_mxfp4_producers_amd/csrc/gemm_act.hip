@@ -4,6 +4,12 @@
 // Method: "Format-Aware Fusion for Fast FP4 Pretraining", §2.3 (Eq. 4) for the
 // product, §3.1 (a boundary leaves its consumer's operands without a round
 // trip) for the epilogue.
+//
+// Bound by the matrix cores and, of the same workgroups, the store burst behind
+// each tile (one workgroup a CU: nothing else runs beside it).  8192 x 14336 x
+// 4096, 0.96 TFLOP: 259 us with a bf16 y (3.7 PFLOP/s; 275 with an fp32 one, the
+// plain product 280), 281 with z beside it, 291 with GELU, 305 with both (3.15
+// PFLOP/s) or with a residual.
 #include <hip/hip_runtime.h>
 
 #include "abi_common.h"

