@@ -81,7 +81,7 @@ def parse():
 TRAFFIC_SUMMARY = os.path.join(ROOT, "profiles", "gemm_fast_kernel_ffn_step_8192x4096x14336_traffic.md")
 # the sources gemm_fast_kernel is built from (its epilogue, main loop and helpers)
 GEMM_SOURCES = [os.path.join(ROOT, "precision_mxfp4_producers_amd", "csrc", f)
-                for f in ("gemm.hip", "gemm_core.h", "mx_device.h")]
+                for f in ("gemm.hip", "gemm_core.h", "gemm_store.h", "mx_device.h")]
 
 
 def gemm_source_hash():
