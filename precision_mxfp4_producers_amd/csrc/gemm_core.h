@@ -624,15 +624,38 @@ __device__ __forceinline__ void main_loop_fast(uint8_t* smem, const Operand& A, 
   PartB xb;
   Frags8 f0, f1;
   uint32_t sa[4], sb[2];
-  // every wave: stage 0 whole, then its stage-1 parts in registers
-  load_part_a<kMode>(p, 0, xa);
-  load_part_b<kMode>(p, 0, xb);
-  write_part_a(smem, p, 0u, xa);
-  write_part_b<kMode>(smem, p, 0u, 0, xb);
-  __builtin_amdgcn_sched_barrier(0);
-  load_part_a<kMode>(p, min(1, last), xa);
-  load_part_b<kMode>(p, min(1, last), xb);
-  if (__builtin_amdgcn_readfirstlane(wm) == 0) {
+  // every wave: stage 0 whole, and its stage-1 parts in registers; both in
+  // flight at once (the fragments' registers are not in use yet)
+  {
+    PartA xa0;
+    PartB xb0;
+    load_part_a<kMode>(p, 0, xa0);
+    load_part_b<kMode>(p, 0, xb0);
+    load_part_a<kMode>(p, min(1, last), xa);
+    load_part_b<kMode>(p, min(1, last), xb);
+    __builtin_amdgcn_sched_barrier(0);
+    write_part_a(smem, p, 0u, xa0);
+    write_part_b<kMode>(smem, p, 0u, 0, xb0);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  int group = __builtin_amdgcn_readfirstlane(wm);
+  if (group != 0) {
+    pp_sync();
+    for (int s = 0; s < nk; ++s) {
+      const uint32_t cur = (uint32_t)(s & 1), nxt = cur ^ 1u;
+      pp_memory<kSwiGLU, 0, true, false, kMode>(smem, p, q, cur, nxt, min(s + 1, last), min(s + 2, last), f0, f1, sa, sb, xa, xb);
+      pp_compute<0, false>(f0, f1, sa, sb, acc);
+      pp_memory<kSwiGLU, 1, false, true, kMode>(smem, p, q, cur, nxt, min(s + 1, last), min(s + 2, last), f0, f1, sa, sb, xa, xb);
+      pp_compute<1, false>(f0, f1, sa, sb, acc);
+    }
+    // nothing of the parts is left: without this the compiler keeps those that it
+    // loaded before the branch for the other group, in scratch memory
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm volatile("" : "=v"(xa.a[j]), "=v"(xb.b[j]));
+    asm volatile("" : "=v"(xb.s.x), "=v"(xb.s.y));
+  }
+  asm volatile("" : "+s"(group));                        // two branches, not one with two sides
+  if (group == 0) {
     // group 0 writes its A part of stage 1 now (its phase 4s-1 for s = 0),
     // loads A of stage 2, and reads its first fragments after the barrier
     write_part_a(smem, p, 1u, xa);
@@ -648,15 +671,6 @@ __device__ __forceinline__ void main_loop_fast(uint8_t* smem, const Operand& A, 
       pp_memory<kSwiGLU, 1, false, false, kMode>(smem, p, q, cur, nxt, min(s + 1, last), min(s + 2, last), f0, f1, sa, sb, xa, xb);
       pp_compute<1, true>(f0, f1, sa, sb, acc);
       pp_memory<kSwiGLU, 0, true, false, kMode>(smem, p, q, nxt, cur, min(s + 2, last), min(s + 3, last), f0, f1, sa, sb, xa, xb);
-    }
-  } else {
-    pp_sync();
-    for (int s = 0; s < nk; ++s) {
-      const uint32_t cur = (uint32_t)(s & 1), nxt = cur ^ 1u;
-      pp_memory<kSwiGLU, 0, true, false, kMode>(smem, p, q, cur, nxt, min(s + 1, last), min(s + 2, last), f0, f1, sa, sb, xa, xb);
-      pp_compute<0, false>(f0, f1, sa, sb, acc);
-      pp_memory<kSwiGLU, 1, false, true, kMode>(smem, p, q, cur, nxt, min(s + 1, last), min(s + 2, last), f0, f1, sa, sb, xa, xb);
-      pp_compute<1, false>(f0, f1, sa, sb, acc);
     }
   }
   __syncthreads();

@@ -5,7 +5,7 @@
 //
 // Where the experts' segments lie is known on the device only: a launch has the
 // tiles that its rows can need at most, and every workgroup finds its tile from
-// the segment offsets (64 of them a turn, one a lane; some 1 us).
+// the segment offsets (128 of them a turn, two a lane; under 1 us).
 //
 // Method: "Format-Aware Fusion for Fast FP4 Pretraining", §2.3 (Eq. 4-6) the
 // contractions, §3.2 the gated FFN.
@@ -43,38 +43,58 @@ struct ExpertTile {
 __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int experts, int rows, int unit, int tiles_n, int pid,
                                             ExpertTile& t) {
   const int lane = threadIdx.x & 63;
-  const auto segment = [&](int e, int& lo, int& hi) {
-    lo = std::min(std::max(offsets[std::min(e, experts)] & -unit, 0), rows);
-    hi = e < experts ? std::min(std::max(offsets[std::min(e + 1, experts)] & -unit, lo), rows) : (e == experts ? rows : lo);
+  // row tiles of the experts of a turn, two a lane (64 apart, so that their
+  // offsets come at once), summed up to and with each
+  int lo[2], hi[2], mine[2], sum[2];
+  const auto count = [&](int at) {
+    int from[2], to[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = at + 64 * h + lane;
+      from[h] = offsets[std::min(e, experts)];
+      to[h] = offsets[std::min(e + 1, experts)];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) asm volatile("" : "+v"(from[h]), "+v"(to[h]));   // all four in flight before the first use
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = at + 64 * h + lane;
+      lo[h] = std::min(std::max(from[h] & -unit, 0), rows);
+      const int end = std::min(std::max(to[h] & -unit, lo[h]), rows);
+      hi[h] = e < experts ? end : (e == experts ? rows : lo[h]);
+      mine[h] = (hi[h] - lo[h] + BM - 1) / BM;
+    }
+    sum[0] = wave_prefix_sum(mine[0]);
+    sum[1] = wave_prefix_sum(mine[1]) + __builtin_amdgcn_readlane(sum[0], 63);
+    return __builtin_amdgcn_readlane(sum[1], 63);
   };
-  // row tiles of the experts of a turn, summed up to and with each lane's
-  const auto count = [&](int at, int& lo, int& hi, int& mine) {
-    segment(at + lane, lo, hi);
-    mine = (hi - lo + BM - 1) / BM;
-    return wave_prefix_sum(mine);
-  };
-  int lo, hi, mine, sum = 0, total = 0;
-  for (int at = 0; at <= experts; at += 64) total += __builtin_amdgcn_readlane(sum = count(at, lo, hi, mine), 63);
+  int total = 0;
+  for (int at = 0; at <= experts; at += 128) total += count(at);
   total *= tiles_n;
   const int share = (total + 7) >> 3, l = (pid & 7) * share + (pid >> 3);
   if ((pid >> 3) >= share || l >= total) return false;
   int before = 0;                                        // row tiles of earlier turns
-  for (int at = 0; at <= experts; at += 64) {
-    if (experts >= 64) sum = count(at, lo, hi, mine);    // one turn: as it stands
-    const uint64_t behind = __builtin_amdgcn_ballot_w64(l < (before + sum) * tiles_n);
+  for (int at = 0; at <= experts; at += 128) {
+    if (experts >= 128) count(at);                       // one turn: as it stands
+    const uint64_t first_half = __builtin_amdgcn_ballot_w64(l < (before + sum[0]) * tiles_n);
+    const uint64_t behind = first_half ? first_half : __builtin_amdgcn_ballot_w64(l < (before + sum[1]) * tiles_n);
     if (behind) {
       const int src = __builtin_ctzll(behind);
-      const int tiles_m = __builtin_amdgcn_readlane(mine, src), first = before + __builtin_amdgcn_readlane(sum, src) - tiles_m;
+      const auto of = [&](const int (&v)[2]) {
+        const int a = __builtin_amdgcn_readlane(v[0], src), b = __builtin_amdgcn_readlane(v[1], src);
+        return first_half ? a : b;
+      };
+      const int tiles_m = of(mine), first = before + of(sum) - tiles_m;
       const int in = l - first * tiles_n, width = 8 * tiles_n, group = in / width;
       const int rest = in - group * width, height = std::min(tiles_m - 8 * group, 8);
       // the divisions run on the vector unit: back to scalar registers
-      t.expert = __builtin_amdgcn_readfirstlane(at + src);
-      t.end = __builtin_amdgcn_readlane(hi, src);
-      t.m0 = __builtin_amdgcn_readlane(lo, src) + __builtin_amdgcn_readfirstlane((8 * group + rest % height) * BM);
+      t.expert = __builtin_amdgcn_readfirstlane(at + (first_half ? 0 : 64) + src);
+      t.end = of(hi);
+      t.m0 = of(lo) + __builtin_amdgcn_readfirstlane((8 * group + rest % height) * BM);
       t.tn = __builtin_amdgcn_readfirstlane(rest / height);
       return true;
     }
-    before += __builtin_amdgcn_readlane(sum, 63);
+    before += __builtin_amdgcn_readlane(sum[1], 63);
   }
   return false;
 }
