@@ -15,6 +15,7 @@
 #include "abi_common.h"
 #include "gemm_core.h"
 #include "gemm_epilogue.h"
+#include "gemm_small.h"
 
 namespace mx {
 
@@ -36,6 +37,24 @@ __global__ __launch_bounds__(kFastThreads) void gemm_act_kernel(int64_t M, int64
   else main_loop_fast<false, kMode>(smem, A, B, m0, n0, 0, K, acc, wm, wn, nullptr, nullptr, k_range(0, (int)(K >> 5)));
   store_epilogue<false>(smem, acc, e, M, N, m0, n0, wave, lane, wm, wn, hl);
 }
+
+__global__ __launch_bounds__(kSmallThreads, 3) void gemm_act_small_kernel(int64_t M, int64_t N, int64_t K,
+                                                                       const uint8_t* __restrict__ a_codes,
+                                                                       const uint8_t* __restrict__ a_scales,
+                                                                       const uint8_t* __restrict__ b_codes,
+                                                                       const uint8_t* __restrict__ b_scales, Epilogue e) {
+  __shared__ __attribute__((aligned(16))) float smem[kSmallSmem / sizeof(float)];
+  int64_t tm, tn;
+  tile_coords((M + kSmallTile - 1) / kSmallTile, (N + kSmallTile - 1) / kSmallTile, tm, tn);
+  const Operand A{a_codes, a_scales, M}, B{b_codes, b_scales, N}, none{};
+  small_tile<false>(smem, A, B, none, none, tm * kSmallTile, tn * kSmallTile, K, K == 0, e);
+}
+
+// The most 64 x 64 tiles a product is given (large and small tiles, bias, GELU and
+// residual: 300 x 1024 x 1024, 80 small tiles, 20 and 7.0 us; 512 x 2048 x 2048, 256,
+// 24 and 8.8; 256 x 4096 x 14336, 256, 85 and 30; 1024 x 4096 x 4096, 1024, 37 and 31;
+// 2048 x 4096 x 1024, 2048, 24 and 25; 2048 x 4096 x 4096, 2048, 40 and 54).
+constexpr int64_t kSmallMost = 1024;
 
 }  // namespace mx
 
@@ -64,6 +83,12 @@ fp4_status fp4_gemm_act(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
     hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(kFastThreads), 0, as_stream(stream), m, n, k, a_codes,
                        a_scales, b_codes, b_scales, e);
   };
+  const int64_t small = tiles_of(m, kSmallTile, n, kSmallTile);
+  if (small > 0 && small <= kSmallMost) {
+    hipLaunchKernelGGL(gemm_act_small_kernel, dim3((unsigned)small), dim3(kSmallThreads), 0, as_stream(stream), m, n, k,
+                       a_codes, a_scales, b_codes, b_scales, e);
+    return launch_status();
+  }
   const int mode = k_mode(k);
   if (mode == kWhole) go(gemm_act_kernel<kWhole>);
   else if (mode == kWindow) go(gemm_act_kernel<kWindow>);

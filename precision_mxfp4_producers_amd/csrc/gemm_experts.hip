@@ -23,6 +23,7 @@
 #include "experts.h"
 #include "gemm_core.h"
 #include "gemm_epilogue.h"
+#include "gemm_small.h"
 #include "swiglu_epilogue.h"
 
 namespace mx {
@@ -40,6 +41,7 @@ struct ExpertTile {
 // columns).  The XCDs, to which the hardware deals workgroups in turn, take one
 // stretch each, so that an expert's weights pass through one L2.  `unit`: what
 // the caller's segments are multiples of (1 or 32; others are cut down to it).
+template <int TILE = BM>
 __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int experts, int rows, int unit, int tiles_n, int pid,
                                             ExpertTile& t) {
   const int lane = threadIdx.x & 63;
@@ -62,7 +64,7 @@ __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int experts,
       lo[h] = std::min(std::max(from[h] & -unit, 0), rows);
       const int end = std::min(std::max(to[h] & -unit, lo[h]), rows);
       hi[h] = e < experts ? end : (e == experts ? rows : lo[h]);
-      mine[h] = (hi[h] - lo[h] + BM - 1) / BM;
+      mine[h] = (hi[h] - lo[h] + TILE - 1) / TILE;
     }
     sum[0] = wave_prefix_sum(mine[0]);
     sum[1] = wave_prefix_sum(mine[1]) + __builtin_amdgcn_readlane(sum[0], 63);
@@ -90,7 +92,7 @@ __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int experts,
       // the divisions run on the vector unit: back to scalar registers
       t.expert = __builtin_amdgcn_readfirstlane(at + (first_half ? 0 : 64) + src);
       t.end = of(hi);
-      t.m0 = of(lo) + __builtin_amdgcn_readfirstlane((8 * group + rest % height) * BM);
+      t.m0 = of(lo) + __builtin_amdgcn_readfirstlane((8 * group + rest % height) * TILE);
       t.tn = __builtin_amdgcn_readfirstlane(rest / height);
       return true;
     }
@@ -125,6 +127,17 @@ __global__ __launch_bounds__(kFastThreads) void gemm_experts_kernel(ExpertsArgs 
     main_loop_fast<false, kMode>(smem, A, B, t.m0, n0, 0, a.k, acc, wm, wn, &A2, &B2, k_range(0, (int)(a.k >> 5)));
   }
   store_epilogue<true>(smem, acc, e, t.end, a.n, t.m0, n0, wave, lane, wm, wn, hl);
+}
+
+// The same in 64 x 64 tiles.
+__global__ __launch_bounds__(kSmallThreads, 3) void gemm_experts_small_kernel(ExpertsArgs a, Epilogue e) {
+  __shared__ __attribute__((aligned(16))) float smem[kSmallSmem / sizeof(float)];
+  ExpertTile t;
+  if (!expert_tile<kSmallTile>(a.offsets, a.experts, a.rows, 1, (int)((a.n + kSmallTile - 1) / kSmallTile), blockIdx.x, t)) return;
+  const int64_t wc = a.n * (a.k >> 1), ws = a.n * (a.k >> 5);
+  const Operand A{a.ac, a.as, t.end}, B{a.bc + t.expert * wc, a.bs + t.expert * ws, a.n};
+  const Operand A2{a.a2c, a.a2s, t.end}, B2{a.b2c + t.expert * wc, a.b2s + t.expert * ws, a.n};
+  small_tile<true>(smem, A, B, A2, B2, t.m0, (int64_t)t.tn * kSmallTile, a.k, t.expert == a.experts, e);
 }
 
 // dW_e = A[:, segment] B[:, segment]^T: rows of A and B hold `tokens` values.
@@ -191,10 +204,21 @@ __global__ __launch_bounds__(kFastThreads) void swiglu_experts_kernel(ExpertsArg
 // so many rows can make (a segment's last tile may be all but empty, and so may
 // that of the rows behind the last), times the column tiles, in eights (one of
 // each for an XCD); -1 past a grid.
-static int64_t experts_grid(int64_t rows, int64_t experts, int64_t n, int64_t bn) {
+static int64_t experts_grid(int64_t rows, int64_t experts, int64_t n, int64_t bn, int64_t bm = BM) {
   if (n > kMaxExpertRows) return -1;
-  const int64_t tm = rows / BM + std::min(experts + 1, rows), tn = (n + bn - 1) / bn;
+  const int64_t tm = rows / bm + std::min(experts + 1, rows), tn = (n + bn - 1) / bn;
   return tm > 0x7FFFFFF0 / tn ? -1 : (tm * tn + 7) / 8 * 8;
+}
+
+// Workgroups in 64 x 64 tiles, or 0 where the large ones are faster.  The small
+// ones are where they are few, the padding's and the last rows' counted (large and
+// small: 232 of them 7.5 and 4.4 us, 564 17 and 11, 712 8.8 and 5.3, 1344 28 and 27,
+// 1856 31 and 36, 2880 35 and 55), and where the experts have few rows, which fill a
+// small part of a large tile (64 experts' 2048 x 2048, 39 rows with their padding 45
+// and 30 us, 95 rows 50 and 45, 160 rows 58 and 67).
+static int64_t experts_small_grid(int64_t rows, int64_t experts, int64_t n) {
+  const int64_t grid = experts_grid(rows, experts, n, kSmallTile, kSmallTile);
+  return grid > 0 && (grid <= 1536 || rows <= 96 * experts) ? grid : 0;
 }
 
 static bool operands_aligned(const uint8_t* c, const uint8_t* s) { return aligned16(c) && aligned16(s); }
@@ -234,6 +258,11 @@ fp4_status fp4_gemm_experts(int64_t experts, int64_t rows, int64_t n, int64_t k,
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kFastThreads), 0, as_stream(stream), a, e);
   };
+  const int64_t small = experts_small_grid(rows, experts, n);
+  if (small > 0) {
+    hipLaunchKernelGGL(gemm_experts_small_kernel, dim3((unsigned)small), dim3(kSmallThreads), 0, as_stream(stream), a, e);
+    return launch_status();
+  }
   const int mode = k_mode(k);
   if (mode == kWhole) go(gemm_experts_kernel<kWhole>);
   else if (mode == kWindow) go(gemm_experts_kernel<kWindow>);

@@ -10,9 +10,9 @@ import subprocess
 
 import pytest
 
-from test_gpu_act import FEW as ACT_FEW, GEMMS, GRADS
+from test_gpu_act import FEW as ACT_FEW, GEMMS, GEMMS_LARGE, GRADS
 from test_gpu_experts import COMBINES, GATHERS, MANY_ROWS, SORTS
-from test_gpu_gemm_experts import FEW, FEW_GATED, ROWS, SWIGLU, UNALIGNED, VARIANTS, WGRAD
+from test_gpu_gemm_experts import FEW, FEW_GATED, ROWS, ROWS_LARGE, SWIGLU, UNALIGNED, VARIANTS, WGRAD
 from oracle import experts as X
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -46,7 +46,7 @@ def launches(program, calls):
 
 
 def calls_of_the_gpu_tests():
-    calls = [f"ga {m} {n} {k}" for m, n, k in GEMMS]
+    calls = [f"ga {m} {n} {k}" for m, n, k, *_ in GEMMS + GEMMS_LARGE]
     calls += [f"mva {m} {n} {k} {k} {e} 0" for m, n, k in ACT_FEW for e in (0, 1) if k or not e]
     calls += [f"ab {m} {n} {f32} {act} 1" for m, n in GRADS for f32 in (0, 1) for act in range(5)] + ["ab 0 64 0 2 1"]
     calls += [f"sort {t} {k} {e} {align} {size}" for t, k, e in SORTS for align in (1, 32, 256) for size in (4, 8)]
@@ -59,7 +59,7 @@ def calls_of_the_gpu_tests():
     def padded(sizes, align):
         return sum(-(-s // align) * align for s in sizes)
 
-    calls += [f"ge {len(s)} {padded(s, 32)} {n} {k}" for s, n, k in ROWS]
+    calls += [f"ge {len(s)} {padded(s, 32)} {n} {k}" for s, n, k, *_ in ROWS + ROWS_LARGE]
     calls += [f"gw {len(s)} {-(-padded(s, 32) // 256) * 256} {m} {n}" for s, m, n in WGRAD]
     calls += [f"sw {len(s)} {padded(s, 32)} {f} {d}" for s, f, d in SWIGLU]
     calls += [f"mve {len(s)} {sum(s)} {n} {k} {e} 0" for s, n, k in FEW for e in (0, 1)]

@@ -88,6 +88,25 @@ def test_gemm_act(gpu_lib, m, n, k, act):
             check(got_z, wz, tz, False)
 
 
+GEMMS_LARGE = [(2081, 2080, 256, A.GELU), (1030, 4128, 288, A.SILU), (4100, 1056, 96, A.RELU), (2050, 2112, 0, A.GELU_TANH),
+               (1100, 4096, 1056, A.NONE)]
+
+
+@pytest.mark.parametrize("m,n,k,act", GEMMS_LARGE)
+def test_gemm_act_of_many_tiles(gpu_lib, m, n, k, act):
+    test_gemm_act(gpu_lib, m, n, k, act)
+
+
+@pytest.mark.parametrize("k", [96, 288, 1024, 2080])
+def test_rows_do_not_depend_on_the_tile_size(gpu_lib, k):
+    """A product of few tiles and the same rows of one of many: the same sums in the same order."""
+    a, b = [dev(v) for v in operand(2081, k, 1)], [dev(v) for v in operand(2080, k, 2)]
+    y, z = gpu_lib.fp4_gemm_act(*a, *b, A.GELU, emit_z=True)
+    for m, n in ((1, 2080), (70, 2080), (2081, 96)):
+        got, got_z = gpu_lib.fp4_gemm_act(*[v[:m] for v in a], *[v[:n] for v in b], A.GELU, emit_z=True)
+        assert torch.equal(got, y[:m, :n]) and torch.equal(got_z, z[:m, :n])
+
+
 def test_gemm_act_without_an_epilogue_is_the_product(gpu_lib):
     for m, n, k in ((64, 96, 256), (288, 320, 1024)):
         ab = [*map(dev, operand(m, k, 1)), *map(dev, operand(n, k, 2))]

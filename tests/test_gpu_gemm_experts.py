@@ -80,6 +80,29 @@ def test_rows(gpu_lib, sizes, n, k, align, extra, f32):
     check(gpu_lib.fp4_gemm_experts(*args, dtype=dtype, pair=[*map(dev, a2), *map(dev, b2)]), ref + ref2, e + e2, 2 * k, f32)
 
 
+ROWS_LARGE = [((5000, 700, 0, 1281), 928, 96, 1, 0, True), ((5000, 700, 0, 1281), 928, 256, 1, 7, False),
+              ((0, 3000, 257, 1, 900), 1440, 288, 32, 0, False), ((300,) * 20, 1056, 512, 32, 96, True)]
+
+
+@pytest.mark.parametrize("sizes,n,k,align,extra,f32", ROWS_LARGE)
+def test_rows_of_many_tiles(gpu_lib, sizes, n, k, align, extra, f32):
+    test_rows(gpu_lib, sizes, n, k, align, extra, f32)
+
+
+@pytest.mark.parametrize("k", [288, 1024])
+def test_rows_do_not_depend_on_the_tile_size(gpu_lib, k):
+    """An expert's rows beside those of others, in large tiles, and alone, in small ones."""
+    offsets, rows = segments((5000, 0, 200, 1281), 1)
+    a, b = [dev(v) for v in codes((rows, k), 1)], [dev(v) for v in codes((4, 928, k), 2)]
+    pair = [dev(v) for v in (*codes((rows, k), 3), *codes((4, 928, k), 4))]
+    both, one = gpu_lib.fp4_gemm_experts(dev(offsets), *a, *b, pair=pair), gpu_lib.fp4_gemm_experts(dev(offsets), *a, *b)
+    at, alone = slice(offsets[2], offsets[3]), dev(np.array([0, 200], np.int32))
+    few = [[v[at] for v in a], [v[2:3] for v in b], [v[at] for v in pair[:2]] + [v[2:3] for v in pair[2:]]]
+    few = [[v.clone() for v in x] for x in few]            # slices may start off 16 bytes
+    assert torch.equal(gpu_lib.fp4_gemm_experts(alone, *few[0], *few[1]), one[at])
+    assert torch.equal(gpu_lib.fp4_gemm_experts(alone, *few[0], *few[1], pair=few[2]), both[at])
+
+
 @pytest.mark.parametrize("sizes,n,k", [((64, 32, 96), 96, 256), ((300, 20), 288, 1024), ((33,), 256, 288)])
 def test_rows_are_those_of_the_plain_product(gpu_lib, sizes, n, k):
     """One expert's rows by fp4_gemm: the same sums in the same order where K is whole steps, the same bound elsewhere."""
