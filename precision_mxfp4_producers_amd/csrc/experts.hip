@@ -308,7 +308,8 @@ __device__ __forceinline__ void load8_cached(const void* p, int64_t i, float (&v
 }
 
 // One thread per eight columns of a token, four of its rows in flight.  Bound by
-// memory: 8192 tokens x 4096 of two bf16 rows each, 268 MB, take 45 us, 5.9 TB/s.
+// memory: 8192 tokens x 4096 of two bf16 rows each, 268 MB, take 45 to 50
+// us, 5.4 to 5.9 TB/s.
 template <bool F32>
 __global__ __launch_bounds__(256) void expert_combine_kernel(CombineArgs a) {
   const int per = a.d >> 3;

@@ -9,7 +9,7 @@
 // each tile (one workgroup a CU: nothing else runs beside it).  8192 x 14336 x
 // 4096, 0.96 TFLOP: 259 us with a bf16 y (3.7 PFLOP/s; 275 with an fp32 one, the
 // plain product 280), 281 with z beside it, 291 with GELU, 305 with both (3.15
-// PFLOP/s) or with a residual.
+// PFLOP/s) or with a residual.  Products of few tiles take tiles of 64 x 64.
 #include <hip/hip_runtime.h>
 
 #include "abi_common.h"
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kSmallThreads, 3) void gemm_act_small_kernel(int64_
   int64_t tm, tn;
   tile_coords((M + kSmallTile - 1) / kSmallTile, (N + kSmallTile - 1) / kSmallTile, tm, tn);
   const Operand A{a_codes, a_scales, M}, B{b_codes, b_scales, N}, none{};
-  small_tile<false>(smem, A, B, none, none, tm * kSmallTile, tn * kSmallTile, K, K == 0, e);
+  small_tile<false>(smem, A, B, none, none, tm * kSmallTile, tn * kSmallTile, K, k_range(0, (int)(K >> 5)), e);
 }
 
 // The most 64 x 64 tiles a product is given (large and small tiles, bias, GELU and

@@ -11,10 +11,11 @@
 // contractions, §3.2 the gated FFN.
 //
 // Bound by the matrix cores, the tiles' start and end that short K leaves bare,
-// and the weight gradients' stores.  64 experts of 2048 x 2048, 65536 rows spread
-// as e^N(0, 1/2): rows 204 to 224 us (0.55 TFLOP, 2.6 PFLOP/s; a segment's last
-// tile is half empty on average, 13% of them all), weight gradients 296 to 318 us
-// (1.07 GB of fp32 at 3.5 TB/s; a fill of as much takes 158).
+// and the weight gradients' stores.  64 experts of 2048 x 2048, 65536 rows of a
+// router that likes some experts better: rows 207 to 217 us (0.55 TFLOP, 2.6
+// PFLOP/s; a segment's last tile is half empty on average, 13% of them all), weight
+// gradients 345 to 355 us (1.07 GB of fp32 at 3.1 TB/s; a fill of as much takes 158).
+// Few rows and few tiles take tiles of 64 x 64.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(kSmallThreads, 3) void gemm_experts_small_kernel(Ex
   const int64_t wc = a.n * (a.k >> 1), ws = a.n * (a.k >> 5);
   const Operand A{a.ac, a.as, t.end}, B{a.bc + t.expert * wc, a.bs + t.expert * ws, a.n};
   const Operand A2{a.a2c, a.a2s, t.end}, B2{a.b2c + t.expert * wc, a.b2s + t.expert * ws, a.n};
-  small_tile<true>(smem, A, B, A2, B2, t.m0, (int64_t)t.tn * kSmallTile, a.k, t.expert == a.experts, e);
+  small_tile<true>(smem, A, B, A2, B2, t.m0, (int64_t)t.tn * kSmallTile, a.k, k_range(0, t.expert == a.experts ? 0 : (int)(a.k >> 5)), e);
 }
 
 // dW_e = A[:, segment] B[:, segment]^T: rows of A and B hold `tokens` values.
@@ -172,6 +173,22 @@ __global__ __launch_bounds__(kFastThreads) void gemm_experts_wgrad_kernel(
   e.y = e.y_f32 ? static_cast<void*>(static_cast<float*>(e.y) + expert * M * N)
                 : static_cast<void*>(static_cast<uint16_t*>(e.y) + expert * M * N);
   store_epilogue<true>(smem, acc, e, M, N, m0, n0, wave, lane, wm, wn, hl);
+}
+
+// The same in 64 x 64 tiles, an expert's in turn.
+__global__ __launch_bounds__(kSmallThreads, 3) void gemm_experts_wgrad_small_kernel(
+    const int32_t* __restrict__ offsets, int64_t tokens, int64_t M, int64_t N, const uint8_t* __restrict__ ac,
+    const uint8_t* __restrict__ as, const uint8_t* __restrict__ bc, const uint8_t* __restrict__ bs, Epilogue e) {
+  __shared__ __attribute__((aligned(16))) float smem[kSmallSmem / sizeof(float)];
+  const int tiles_m = (int)((M + kSmallTile - 1) / kSmallTile), tiles = tiles_m * (int)((N + kSmallTile - 1) / kSmallTile);
+  const int expert = blockIdx.x / tiles, in = blockIdx.x - expert * tiles, blocks = (int)(tokens >> 5);
+  const int lo = std::min(std::max(offsets[expert] >> 5, 0), blocks), hi = std::min(std::max(offsets[expert + 1] >> 5, lo), blocks);
+  if (hi == lo && e.accumulate) return;
+  const Operand A{ac, as, M}, B{bc, bs, N}, none{};
+  e.y = e.y_f32 ? static_cast<void*>(static_cast<float*>(e.y) + expert * M * N)
+                : static_cast<void*>(static_cast<uint16_t*>(e.y) + expert * M * N);
+  small_tile<true>(smem, A, B, none, none, (int64_t)(in % tiles_m) * kSmallTile, (int64_t)(in / tiles_m) * kSmallTile, tokens,
+                   k_range(lo, hi), e);
 }
 
 struct SwigluOut {
@@ -220,6 +237,13 @@ static int64_t experts_small_grid(int64_t rows, int64_t experts, int64_t n) {
   const int64_t grid = experts_grid(rows, experts, n, kSmallTile, kSmallTile);
   return grid > 0 && (grid <= 1536 || rows <= 96 * experts) ? grid : 0;
 }
+
+// The most 64 x 64 tiles of the experts' weight gradients together (large and small:
+// 4 experts' 128 x 128, 65536 tokens in all, 16 small tiles, 75 and 27 us; 16 experts'
+// 32 x 1024, 32768, 256 tiles, 27 and 11; 64 experts' 256 x 256, 65536, 1024 tiles, 26
+// and 20; 4 experts' 1024 x 1024, 32768, 1024 tiles, 50 and 54; 8 experts' 1024 x 1024,
+// 2048, 2048 tiles, 15.0 and 15.2; 64 experts' 512 x 512, 65536, 4096 tiles, 31 and 48).
+constexpr int64_t kSmallGradients = 1024;
 
 static bool operands_aligned(const uint8_t* c, const uint8_t* s) { return aligned16(c) && aligned16(s); }
 
@@ -289,6 +313,12 @@ fp4_status fp4_gemm_experts_wgrad(int64_t experts, int64_t tokens, int64_t m, in
   e.y_f32 = c_type == FP4_F32;
   e.accumulate = accumulate;
   e.stream = streams(experts * m, n * (e.y_f32 ? 4 : 2));
+  const int64_t small = tiles_of(m, kSmallTile, n, kSmallTile) * experts;
+  if (small <= kSmallGradients) {
+    hipLaunchKernelGGL(gemm_experts_wgrad_small_kernel, dim3((unsigned)small), dim3(kSmallThreads), 0, as_stream(stream),
+                       offsets, tokens, m, n, a_codes, a_scales, b_codes, b_scales, e);
+    return launch_status();
+  }
   hipLaunchKernelGGL(gemm_experts_wgrad_kernel, dim3((unsigned)(tiles * experts)), dim3(kFastThreads), 0, as_stream(stream),
                      offsets, tokens, m, n, a_codes, a_scales, b_codes, b_scales, e);
   return launch_status();

@@ -1,4 +1,5 @@
-// Block-scaled E2M1 products of few tiles: 64 x 64 tiles, 32 x 32 a wave.
+// Block-scaled E2M1 products of few tiles: 64 x 64 tiles, 32 x 32 a wave, over a K
+// range as the fast main loop takes it.
 //
 // A product of few 256 x 256 tiles leaves most CUs without work, and a large tile
 // of few rows computes what nobody reads.  Here a tile is a sixteenth, a workgroup
@@ -40,13 +41,14 @@ struct SmallStep {
   uint2 scales;
 };
 
-// Rows past the operand and blocks past the row read as zero, their scales too:
-// a scale byte of another row may stand for no number.  (The range check covers
+// Rows past the operand and blocks outside the K range read as zero, their scales
+// too: a scale byte of another row may stand for no number.  (The range check covers
 // the lane offset, not the scalar one, which carries the K position.)
-__device__ __forceinline__ void load_small(const SmallOperand& a, const SmallOperand& b, int64_t K, int step, int wave, SmallStep& x) {
+__device__ __forceinline__ void load_small(const SmallOperand& a, const SmallOperand& b, int64_t K, const KRange& kr, int step, int wave,
+                                           SmallStep& x) {
   const int t = threadIdx.x, lsc = (int)(K >> 5);
   const uint32_t ldb = (uint32_t)(K >> 1), so = (uint32_t)step * BKB;
-  const uint32_t v = 8 * step + (t & 7) < lsc ? (uint32_t)(t >> 3) * ldb + (t & 7) * 16 : kOffNone;
+  const uint32_t v = (uint32_t)(8 * step + (t & 7) - kr.lo) < (uint32_t)kr.count ? (uint32_t)(t >> 3) * ldb + (t & 7) * 16 : kOffNone;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     x.a[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(a.codes, v + (uint32_t)(32 * j) * ldb, so, 0));
@@ -67,7 +69,8 @@ __device__ __forceinline__ void load_small(const SmallOperand& a, const SmallOpe
   }
 }
 
-__device__ __forceinline__ void write_small(uint8_t* stage, int64_t K, int step, int wave, const SmallStep& x) {
+__device__ __forceinline__ void write_small(uint8_t* stage, int64_t K, const KRange& kr, int step, int wave,
+                                            const SmallStep& x) {
   const int t = threadIdx.x;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -77,7 +80,9 @@ __device__ __forceinline__ void write_small(uint8_t* stage, int64_t K, int step,
   }
   if (wave > 1) return;
   const int moved = K >= 256 ? max(8 * step - ((int)(K >> 5) - 8), 0) : 0;
-  *reinterpret_cast<uint64_t*>(stage + kSmallScales + 8 * t) = __builtin_bit_cast(uint64_t, x.scales) >> (8 * moved);
+  const int from = max(kr.lo - 8 * step, 0), to = min(kr.lo + kr.count - 8 * step, 8);   // bytes of the range
+  const uint64_t in = (~(uint64_t)0 << (8 * from)) & (~(uint64_t)0 >> (8 * (8 - to)));
+  *reinterpret_cast<uint64_t*>(stage + kSmallScales + 8 * t) = (__builtin_bit_cast(uint64_t, x.scales) >> (8 * moved)) & in;
 }
 
 template <int S>
@@ -89,13 +94,13 @@ __device__ __forceinline__ void mfma_small(const uint8_t* stage, int ra, int rb,
 
 // Tile (m0, n0): rows up to A.rows, columns up to B.rows (a multiple of 32).  A2,
 // B2: a second pair of the same shapes, whose K steps follow; or null codes.
-// `empty`: a product of nothing.
+// Rows are K long, of which the range kr is taken; one of no steps gives zeros.
 template <bool PLAIN>
 __device__ __forceinline__ void small_tile(float* smem, const Operand& A, const Operand& B, const Operand& A2, const Operand& B2,
-                                           int64_t m0, int64_t n0, int64_t K, bool empty, const Epilogue& e) {
+                                           int64_t m0, int64_t n0, int64_t K, const KRange& kr, const Epilogue& e) {
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
   const int r = lane & 31, hl = lane >> 5, ra = 32 * (wave >> 1) + r, rb = 32 * (wave & 1) + r;
-  const int nk1 = empty ? 0 : (int)((K + 255) >> 8), nk = A2.codes ? 2 * nk1 : nk1;
+  const int nk1 = kr.steps, nk = A2.codes ? 2 * nk1 : nk1;
   const int64_t M = A.rows, N = B.rows;
   v16f acc;
 #pragma unroll
@@ -108,7 +113,7 @@ __device__ __forceinline__ void small_tile(float* smem, const Operand& A, const 
     const auto load = [&](int s, SmallStep& y) {
       if (s >= nk) return;
       const bool second = s >= nk1;
-      load_small(second ? a2 : a1, second ? b2 : b1, K, second ? s - nk1 : s, wave, y);
+      load_small(second ? a2 : a1, second ? b2 : b1, K, kr, kr.first + (second ? s - nk1 : s), wave, y);
     };
 #pragma unroll
     for (int u = 0; u < 4; ++u) load(u, x[u]);
@@ -120,7 +125,7 @@ __device__ __forceinline__ void small_tile(float* smem, const Operand& A, const 
         const int s = s0 + u;
         if (s >= nk) break;
         uint8_t* const stage = lds + (u & 1) * kSmallStage;
-        write_small(stage, K, s >= nk1 ? s - nk1 : s, wave, x[u]);
+        write_small(stage, K, kr, kr.first + (s >= nk1 ? s - nk1 : s), wave, x[u]);
         load(s + 4, x[u]);
         pp_sync();
         const uint32_t sa = *reinterpret_cast<const uint32_t*>(stage + kSmallScales + 8 * ra + 4 * hl);
@@ -171,6 +176,10 @@ __device__ __forceinline__ void small_tile(float* smem, const Operand& A, const 
     }
     if (e.y_f32) {
       float* const q = static_cast<float*>(e.y) + row * e.ldy + col;
+      if (PLAIN && e.accumulate) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = __fadd_rn(q[u], v[u]);
+      }
       *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4*>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
     } else {

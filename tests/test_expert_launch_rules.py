@@ -12,7 +12,7 @@ import pytest
 
 from test_gpu_act import FEW as ACT_FEW, GEMMS, GEMMS_LARGE, GRADS
 from test_gpu_experts import COMBINES, GATHERS, MANY_ROWS, SORTS
-from test_gpu_gemm_experts import FEW, FEW_GATED, ROWS, ROWS_LARGE, SWIGLU, UNALIGNED, VARIANTS, WGRAD
+from test_gpu_gemm_experts import FEW, FEW_GATED, ROWS, ROWS_LARGE, SWIGLU, UNALIGNED, VARIANTS, WGRAD, WGRAD_LARGE
 from oracle import experts as X
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -60,7 +60,7 @@ def calls_of_the_gpu_tests():
         return sum(-(-s // align) * align for s in sizes)
 
     calls += [f"ge {len(s)} {padded(s, 32)} {n} {k}" for s, n, k, *_ in ROWS + ROWS_LARGE]
-    calls += [f"gw {len(s)} {-(-padded(s, 32) // 256) * 256} {m} {n}" for s, m, n in WGRAD]
+    calls += [f"gw {len(s)} {-(-padded(s, 32) // 256) * 256} {m} {n}" for s, m, n, *_ in WGRAD + WGRAD_LARGE]
     calls += [f"sw {len(s)} {padded(s, 32)} {f} {d}" for s, f, d in SWIGLU]
     calls += [f"mve {len(s)} {sum(s)} {n} {k} {e} 0" for s, n, k in FEW for e in (0, 1)]
     calls += [f"sme {len(s)} {sum(s) + 2} {f} {d} {e} 0" for s, f, d in FEW_GATED for e in (0, 1)]

@@ -160,6 +160,23 @@ def test_wgrad(gpu_lib, sizes, m, n, align, extra):
     assert all(np.array_equal(host(c)[i], prev[i]) for i in range(len(sizes)) if sizes[i] == 0)
 
 
+WGRAD_LARGE = [((2000, 1, 0, 700), 1056, 1056, 32, 0), ((33,) * 9, 672, 704, 32, 256)]
+
+
+@pytest.mark.parametrize("sizes,m,n,align,extra", WGRAD_LARGE)
+def test_wgrad_of_many_tiles(gpu_lib, sizes, m, n, align, extra):
+    test_wgrad(gpu_lib, sizes, m, n, align, extra)
+
+
+def test_wgrad_does_not_depend_on_the_tile_size(gpu_lib):
+    offsets, rows = segments((2000, 1, 0, 700, 40), 32)
+    rows = -(-rows // 256) * 256
+    a, b = [dev(v) for v in codes((1056, rows), 1)], [dev(v) for v in codes((1024, rows), 2)]
+    want = gpu_lib.fp4_gemm_experts_wgrad(dev(offsets), *a, *b)
+    got = gpu_lib.fp4_gemm_experts_wgrad(dev(offsets), *[v[:96] for v in a], *[v[:160] for v in b])
+    assert torch.equal(got, want[:, :96, :160])
+
+
 SWIGLU = [((32,), 32, 32), ((5, 0, 70, 300), 64, 96), ((256, 257), 96, 256), ((33, 1, 0), 160, 288), ((40,) * 67, 32, 64),
           ((600, 8), 288, 512), ((0, 0), 64, 64)]
 
@@ -411,3 +428,40 @@ def test_tokens_do_not_reach_other_experts(gpu_lib, sizes):
             got = host(gpu_lib.fp4_gemm_experts_wgrad(dev(offsets), dev(a[0]), dev(sa), dev(b[0]), dev(sb), dtype=dtype))
             others = [i for i in range(len(sizes)) if i != e]
             assert np.array_equal(got[others], want[others])
+
+
+@pytest.mark.parametrize("k", [96, 288, 544])
+def test_rows_and_weights_of_many_tiles_do_not_reach_their_neighbours(gpu_lib, k):
+    sizes, n = (2400, 0, 800), 2080
+    offsets, rows = segments(sizes, 1)
+    a, b = codes((rows, k), 1), codes((len(sizes), n, k), 2)
+    ab, bb = a[1].copy(), b[1].copy()
+    broken = [0, 256, 2400, rows - 1]
+    ab[broken] = 255
+    bb[0, [0, n - 1]], bb[2, 7] = 255, 255
+    ok = np.ones((rows, n), bool)
+    ok[:2400, [0, n - 1]], ok[2400:, 7], ok[broken] = False, False, False
+    good = np.ones((rows, n), bool)
+    good[:, [0, n - 1]], good[broken] = False, False
+
+    def run(sa, sb):
+        ac, as_, bc, bs = dev(a[0]), dev(sa), dev(b[0]), dev(sb)
+        return [host(gpu_lib.fp4_gemm_experts(dev(offsets), ac, as_, bc, bs))[ok],
+                host(gpu_lib.fp4_gemm_act(ac, as_, bc[0], bs[0], dtype=torch.float32)[0])[good]]
+
+    for got, want in zip(run(ab, bb), run(a[1], b[1])):
+        assert np.isfinite(want).all() and np.array_equal(got, want)
+
+
+def test_tokens_of_many_tiles_do_not_reach_other_experts(gpu_lib):
+    sizes, m, n = (96, 32, 0, 160, 224), 1056, 1056
+    offsets, tokens = segments(sizes, 32)
+    a, b = codes((m, 512), 1), codes((n, 512), 2)
+    want = host(gpu_lib.fp4_gemm_experts_wgrad(dev(offsets), dev(a[0]), dev(a[1]), dev(b[0]), dev(b[1])))
+    for e in range(len(sizes)):
+        at = slice(offsets[e] // 32, offsets[e + 1] // 32)
+        sa, sb = a[1].copy(), b[1].copy()
+        sa[:, at], sb[3, at], sa[:, tokens // 32:] = 255, 255, 255
+        got = host(gpu_lib.fp4_gemm_experts_wgrad(dev(offsets), dev(a[0]), dev(sa), dev(b[0]), dev(sb)))
+        others = [i for i in range(len(sizes)) if i != e]
+        assert np.array_equal(got[others], want[others])
