@@ -314,7 +314,7 @@ fp4_status fp4_gemm_experts_wgrad(int64_t experts, int64_t tokens, int64_t m, in
   e.accumulate = accumulate;
   e.stream = streams(experts * m, n * (e.y_f32 ? 4 : 2));
   const int64_t small = tiles_of(m, kSmallTile, n, kSmallTile) * experts;
-  if (small <= kSmallGradients) {
+  if (small > 0 && small <= kSmallGradients) {   // below 0: more tiles than a launch holds
     hipLaunchKernelGGL(gemm_experts_wgrad_small_kernel, dim3((unsigned)small), dim3(kSmallThreads), 0, as_stream(stream),
                        offsets, tokens, m, n, a_codes, a_scales, b_codes, b_scales, e);
     return launch_status();

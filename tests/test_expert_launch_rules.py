@@ -115,3 +115,13 @@ def test_sorted_rows_have_their_workgroups(program):
         (st, made), = launches(program, [f"mve {experts} {min(rows, 65536)} {n} 256 0 0"])
         r = min(rows, 65536)
         assert made[0][1][1] == min(experts, r) + r // 16
+
+
+def test_sizes_whose_small_tiles_pass_a_grid_take_large_ones(program):
+    m = n = 1 << 21
+    for call in (f"gw 1 256 {m} {n}", f"ga {m} {n} 256", f"ge 1 {m} {n * 128} 256"):
+        (st, made), = launches(program, [call])
+        assert (st == 0 and "small" not in made[0][0] and 0 < made[0][1][0] < 1 << 31) or (st == 2 and not made), (call, st, made)
+    m = n = 1 << 22
+    (st, made), = launches(program, [f"gw 1 256 {m} {n}"])
+    assert st == 0 and "small" not in made[0][0] and made[0][1][0] == (m // 256) * (n // 256)
