@@ -612,7 +612,10 @@ typedef enum { FP4_ACT_NONE = 0, FP4_ACT_RELU = 1, FP4_ACT_GELU = 2, FP4_ACT_GEL
  * act: none; relu; gelu z erfc(-z / sqrt 2) / 2; gelu_tanh z / (1 + exp(-2 u)),
  * u = sqrt(2/pi) (z + 0.044715 z^3); silu z / (1 + exp(-z)).  It takes the fp32
  * z; z itself is kept rounded to bf16 for fp4_act_backward.  At minus infinity
- * the last three are their limit 0.
+ * the last three are their limit 0.  gelu for an fp32 y is within 2^-13 of itself
+ * down to z = -8 and 2^-11 below (beside 6e-8 |z|), for a bf16 y within 2^-9.9
+ * before its rounding of 2^-8; silu and gelu_tanh are 0 where their exponential
+ * leaves fp32 (z below -87 and -10).
  *   a_codes [m][k/2], a_scales [m][k/32]; b_codes [n][k/2], b_scales [n][k/32]
  *   bias      [n] bf16 or fp32 (bias_type), or NULL
  *   residual  [m][ldr] bf16, or NULL

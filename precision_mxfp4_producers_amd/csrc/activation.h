@@ -13,22 +13,45 @@ constexpr float kLog2e = 0x1.715476p+0f;
 constexpr float kTanhC = -2.30220818f;                   // -2 sqrt(2/pi) log2(e)
 constexpr float kTanhA = 0.044715f;
 
-// Normal distribution function at -a, a >= 0, as 2^P(a): P is a weighted
-// least-squares fit of log2(erfc(a / sqrt 2) / 2), the weights sharpened until
-// the largest error of the function and of a times it was least.  In fp32
-// arithmetic both are within 2.9e-7, and the function within 4e-4 of itself up to
-// a = 4.5 (a bf16 rounding is up to 4e-3); from 16 on it is 0.  A fit of degree 9 in
-// 1 / (1 + c a), with its reciprocal and one multiplication more, made the
-// epilogue of 8192 x 14336 16 us longer at no gain in the rounded result.
-__device__ __forceinline__ float normal_tail(float a) {
-  float p = -0x1.b4df74p-21f;
-  p = __builtin_fmaf(p, a, 0x1.51375ap-15f);
-  p = __builtin_fmaf(p, a, -0x1.986106p-11f);
-  p = __builtin_fmaf(p, a, 0x1.072842p-7f);
-  p = __builtin_fmaf(p, a, -0x1.b43ac0p-5f);
-  p = __builtin_fmaf(p, a, -0x1.d5f300p-2f);
-  p = __builtin_fmaf(p, a, -0x1.26b128p+0f);
-  return exp2_hw(__builtin_fmaf(p, a, -0x1.ffffe8p-1f));
+// Square root of the normal distribution function at -a, a >= 0, as 2^P(a): 2 P is a
+// minimax fit of log2(erfc(a / sqrt 2) / 2) up to a = 13.6, its tolerance a relative
+// error far out and an absolute one of the function near 0.  Of degree 10, for
+// values rounded to bf16, the function is within 1e-3 of itself (a bf16 rounding is up
+// to 4e-3) and gelu of normal z within 1.7e-7 in the 2-norm; of degree 12 (FINE) within
+// 8e-5 of itself up to 8 and 3e-4 up to 13, and gelu within 5.2e-8 (fp32's erfc:
+// 3.3e-8).  The root, since the hardware's 2^x is 0 below 2^-126, where a times the
+// function is still a normal number.  Even degrees with a negative last coefficient:
+// far out P is minus infinity.
+// 8192 x 14336 x 4096 with GELU: 300 us with a bf16 y, degree 12 instead 306; 324 with
+// an fp32 one.  A fit of degree 7, off by a tenth at a = 8, took 295 and 313.
+template <bool FINE>
+__device__ __forceinline__ float normal_tail_root(float a) {
+  float p;
+  if constexpr (FINE) {
+    p = __builtin_fmaf(-0x1.8b0816p-38f, a, 0x1.de93f0p-32f);
+    p = __builtin_fmaf(p, a, -0x1.f62538p-27f);
+    p = __builtin_fmaf(p, a, 0x1.29b9d6p-22f);
+    p = __builtin_fmaf(p, a, -0x1.b1f1c6p-19f);
+    p = __builtin_fmaf(p, a, 0x1.832ec6p-16f);
+    p = __builtin_fmaf(p, a, -0x1.5e8292p-14f);
+    p = __builtin_fmaf(p, a, -0x1.f74ef8p-14f);
+    p = __builtin_fmaf(p, a, 0x1.da4802p-9f);
+    p = __builtin_fmaf(p, a, -0x1.af2348p-6f);
+    p = __builtin_fmaf(p, a, -0x1.d62ed6p-3f);
+    p = __builtin_fmaf(p, a, -0x1.26af30p-1f);
+    return exp2_hw(__builtin_fmaf(p, a, -0x1.fffffcp-2f));
+  } else {
+    p = __builtin_fmaf(-0x1.7cfadep-32f, a, 0x1.4f6e56p-26f);
+    p = __builtin_fmaf(p, a, -0x1.ccada0p-22f);
+    p = __builtin_fmaf(p, a, 0x1.1a80f4p-18f);
+    p = __builtin_fmaf(p, a, -0x1.7b273ep-18f);
+    p = __builtin_fmaf(p, a, -0x1.467c74p-12f);
+    p = __builtin_fmaf(p, a, 0x1.fd49b4p-9f);
+    p = __builtin_fmaf(p, a, -0x1.b260d2p-6f);
+    p = __builtin_fmaf(p, a, -0x1.d60ad4p-3f);
+    p = __builtin_fmaf(p, a, -0x1.26b050p-1f);
+    return exp2_hw(__builtin_fmaf(p, a, -0x1.fffff2p-2f));
+  }
 }
 
 __device__ __forceinline__ float sigmoid_of_exponent(float e) {   // 1 / (1 + 2^e)
@@ -39,13 +62,18 @@ __device__ __forceinline__ float sigmoid_of_exponent(float e) {   // 1 / (1 + 2^
 // (a NaN comes with the factor).
 __device__ __forceinline__ float times_gate(float z, float gate) { return __fmul_rn(fmaxf(z, -128.0f), gate); }
 
-template <int ACT>
+// FINE: for an fp32 result; else it is rounded to bf16.
+template <int ACT, bool FINE>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == FP4_ACT_RELU) return z <= 0.0f ? 0.0f : z;
   if constexpr (ACT == FP4_ACT_GELU) {
-    // z for positive z, less |z| times the tail on both sides (which is 0 from 16
-    // on; a NaN comes with the tail)
-    return __builtin_fmaf(-fminf(fabsf(z), 16.0f), normal_tail(fabsf(z)), fmaxf(z, 0.0f));
+    // z for positive z, less |z| times the tail on both sides.  |z| times the root is
+    // below 1/2; the clamp, which is part of that multiplication, makes it 0 where |z|
+    // is infinite (infinity times 0), and a NaN comes with the root.
+    const float t = normal_tail_root<FINE>(fabsf(z));
+    const float u = __builtin_amdgcn_fmed3f(__fmul_rn(fabsf(z), t), 0.0f, 1.0f);
+    const float p = __int_as_float(std::max(__float_as_int(z), 0));   // max(z, 0) in one instruction
+    return __builtin_fmaf(-u, t, p);
   }
   if constexpr (ACT == FP4_ACT_GELU_TANH)
     return times_gate(z, sigmoid_of_exponent(__fmul_rn(kTanhC, __builtin_fmaf(__fmul_rn(__fmul_rn(z, z), z), kTanhA, z))));
@@ -61,9 +89,9 @@ __device__ __forceinline__ float act_slope(float z) {
   const float x = __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f);
   float d = 1.0f;
   if constexpr (ACT == FP4_ACT_GELU) {
-    const float q = normal_tail(fabsf(x));
-    const float density = __fmul_rn(0.39894228f, exp2_hw(__fmul_rn(__fmul_rn(x, x), -0.5f * kLog2e)));
-    d = __builtin_fmaf(x, density, x < 0.0f ? q : __fsub_rn(1.0f, q));
+    const float t = normal_tail_root<true>(fabsf(x)), q = __fmul_rn(t, t);
+    const float r = exp2_hw(__fmul_rn(__fmul_rn(x, x), -0.25f * kLog2e));   // root of e^(-x^2 / 2)
+    d = __builtin_fmaf(__fmul_rn(x, r), __fmul_rn(0.39894228f, r), x < 0.0f ? q : __fsub_rn(1.0f, q));
   } else if constexpr (ACT == FP4_ACT_GELU_TANH) {
     const float xx = __fmul_rn(x, x);
     const float s = sigmoid_of_exponent(__fmul_rn(kTanhC, __builtin_fmaf(__fmul_rn(xx, x), kTanhA, x)));

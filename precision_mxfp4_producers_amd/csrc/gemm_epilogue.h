@@ -149,7 +149,7 @@ __device__ __forceinline__ void store_epilogue_as(uint8_t* smem, const v16f (&ac
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int u = 0; u < W; ++u) v[k][u] = act_value<act()>(v[k][u]);
+            for (int u = 0; u < W; ++u) v[k][u] = act_value<act(), F32>(v[k][u]);
         });
       if (!PLAIN && e.residual) {
 #pragma unroll

@@ -166,8 +166,12 @@ __device__ __forceinline__ void small_tile(float* smem, const Operand& A, const 
       if (e.z) put_row(e.z + row * N + col, v, 0);
       if (e.act != FP4_ACT_NONE)
         with_act(e.act, [&](auto act) {
+          const auto apply = [&](auto fine) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = act_value<act()>(v[u]);
+            for (int u = 0; u < 8; ++u) v[u] = act_value<act(), fine()>(v[u]);
+          };
+          if (act() == FP4_ACT_GELU && e.y_f32) apply(std::true_type{});   // the others are the same for both
+          else apply(std::false_type{});
         });
       if (e.residual) {
 #pragma unroll

@@ -52,7 +52,7 @@ __device__ __forceinline__ void put_epilogue(const MvEpilogue& e, int mr, int64_
   if (e.bias)
     v = __fadd_rn(v, e.bias_f32 ? static_cast<const float*>(e.bias)[row]
                                 : bf16_bits_to_f32(static_cast<const uint16_t*>(e.bias)[row]));
-  with_act(e.act, [&](auto act) { v = act_value<act()>(v); });
+  with_act(e.act, [&](auto act) { v = act_value<act(), true>(v); });
   if (e.residual) v = __fadd_rn(v, bf16_bits_to_f32(e.residual[mr * e.ldr + row]));
   if (e.y_f32) static_cast<float*>(e.y)[mr * e.ldy + row] = v;
   else static_cast<uint16_t*>(e.y)[mr * e.ldy + row] = (uint16_t)bf16_pack2_rne(v, 0.0f);
