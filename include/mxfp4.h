@@ -624,7 +624,7 @@ typedef enum { FP4_ACT_NONE = 0, FP4_ACT_RELU = 1, FP4_ACT_GELU = 2, FP4_ACT_GEL
  * Any m; k = 0 gives z = bias.  Deterministic.
  * Errors: FP4_EINVAL bad type or act, or null pointer; FP4_ESHAPE m negative, n
  * or k not a non-negative multiple of 32, k >= 2^24, a leading dimension below
- * n, or more than 2^31 - 1 output tiles of 256 x 256; FP4_EALIGN an operand,
+ * n, or more than 2^31 - 2^16 output tiles of 256 x 256; FP4_EALIGN an operand,
  * residual, z or y not 16-byte aligned, bias not aligned to its element, ldr
  * or ldy (bf16) not a multiple of 8, or ldy (fp32) not a multiple of 4.
  */
@@ -793,8 +793,9 @@ fp4_status fp4_expert_combine_backward(int64_t t, int64_t k, int64_t d, int64_t 
  * Errors: FP4_EINVAL bad c_type, or null pointer (the second operands: all four
  * or none); FP4_ESHAPE experts outside 1 .. 1024, rows negative or above 2^30, n
  * or k not a non-negative multiple of 32, n above 2^30, k >= 2^24, ldc below n,
- * or more tiles than a launch holds; FP4_EALIGN an operand or c not 16-byte
- * aligned, offsets not 4-byte aligned, or ldc not a multiple of 8 (bf16) or 4.
+ * or more than 2^31 - 2^16 tiles of 256 x 256, one more row of them an expert
+ * counted; FP4_EALIGN an operand or c not 16-byte aligned, offsets not 4-byte
+ * aligned, or ldc not a multiple of 8 (bf16) or 4.
  */
 fp4_status fp4_gemm_experts(int64_t experts, int64_t rows, int64_t n, int64_t k, const int32_t* offsets,
                             const uint8_t* a_codes, const uint8_t* a_scales,
@@ -813,7 +814,7 @@ fp4_status fp4_gemm_experts(int64_t experts, int64_t rows, int64_t n, int64_t k,
  * Errors: FP4_EINVAL bad c_type, accumulate not 0 or 1, accumulate into bf16, or
  * null pointer; FP4_ESHAPE experts outside 1 .. 1024, tokens negative, not a
  * multiple of 256 or >= 2^24, m or n not a non-negative multiple of 32, or more
- * than 2^31 - 1 tiles; FP4_EALIGN as fp4_gemm_experts.
+ * than 2^31 - 2^16 tiles; FP4_EALIGN as fp4_gemm_experts.
  */
 fp4_status fp4_gemm_experts_wgrad(int64_t experts, int64_t tokens, int64_t m, int64_t n, const int32_t* offsets,
                                   const uint8_t* a_codes, const uint8_t* a_scales,

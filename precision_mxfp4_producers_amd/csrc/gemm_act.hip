@@ -27,7 +27,9 @@ __global__ __launch_bounds__(kFastThreads) void gemm_act_kernel(int64_t M, int64
                                                                 const uint8_t* __restrict__ b_scales, Epilogue e) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kSmemBytes];
   int64_t tm, tn;
-  tile_coords((M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
+  const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN, pid = grid_tile();
+  if (pid >= tiles_m * tiles_n) return;
+  tile_coords_of(pid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = tm * BM, n0 = tn * BN;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int wm = wave >> 2, wn = wave & 3, hl = lane >> 5;
@@ -80,7 +82,7 @@ fp4_status fp4_gemm_act(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
   const Epilogue e{y, ldy, bias, residual, ldr, z, (int)act, f32, bias_type == FP4_F32, 0,
                    streams(m, n * ((f32 ? 4 : 2) + (z ? 2 : 0)))};
   const auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(kFastThreads), 0, as_stream(stream), m, n, k, a_codes,
+    hipLaunchKernelGGL(kernel, tile_grid(tiles), dim3(kFastThreads), 0, as_stream(stream), m, n, k, a_codes,
                        a_scales, b_codes, b_scales, e);
   };
   const int64_t small = tiles_of(m, kSmallTile, n, kSmallTile);

@@ -200,11 +200,25 @@ __device__ __forceinline__ void zero_tile(v16f (&acc)[4][2]) {
 // Row lengths by the main loop's K range (see kWindow).
 inline int k_mode(int64_t k) { return k > 0 && k % 256 == 0 ? kWhole : (k >= 256 ? kWindow : kShort); }
 
-// Number of bm x bn tiles, or -1 when it exceeds a grid's 2^31 - 1 workgroups.
+// Most tiles of a launch.
+constexpr int64_t kMostTiles = 0x7FFF0000;
+
+// Number of bm x bn tiles, or -1 past kMostTiles.
 inline int64_t tiles_of(int64_t m, int64_t bm, int64_t n, int64_t bn) {
   const int64_t tm = (m - 1) / bm + 1, tn = (n - 1) / bn + 1;
   if (m == 0 || n == 0) return 0;
-  return tm > 0x7FFFFFFF / tn ? -1 : tm * tn;
+  return tm > kMostTiles / tn ? -1 : tm * tn;
 }
+
+// Workgroups of so many tiles, one each.  A launch's dimension holds less than 2^32
+// threads (a larger one wraps, with no error), which workgroups of 512 reach at 2^23
+// tiles: past half of that they go to a second dimension, in equal shares of whole
+// eights (one for each XCD).  The few spare ones come last.
+constexpr int64_t kGridTiles = 1 << 22;
+inline dim3 tile_grid(int64_t tiles) {
+  const int64_t y = (tiles + kGridTiles - 1) / kGridTiles;
+  return y > 1 ? dim3((unsigned)(((tiles + y - 1) / y + 7) / 8 * 8), (unsigned)y) : dim3((unsigned)tiles);
+}
+__device__ __forceinline__ int64_t grid_tile() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
 }  // namespace mx

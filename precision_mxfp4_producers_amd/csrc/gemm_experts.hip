@@ -115,7 +115,7 @@ template <int kMode>
 __global__ __launch_bounds__(kFastThreads) void gemm_experts_kernel(ExpertsArgs a, Epilogue e) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kSmemBytes];
   ExpertTile t;
-  if (!expert_tile(a.offsets, a.experts, a.rows, 1, (int)((a.n + BN - 1) / BN), blockIdx.x, t)) return;
+  if (!expert_tile(a.offsets, a.experts, a.rows, 1, (int)((a.n + BN - 1) / BN), (int)grid_tile(), t)) return;
   const int64_t n0 = (int64_t)t.tn * BN, wc = a.n * (a.k >> 1), ws = a.n * (a.k >> 5);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int wm = wave >> 2, wn = wave & 3, hl = lane >> 5;
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kFastThreads) void gemm_experts_kernel(ExpertsArgs 
 __global__ __launch_bounds__(kSmallThreads, 3) void gemm_experts_small_kernel(ExpertsArgs a, Epilogue e) {
   __shared__ __attribute__((aligned(16))) float smem[kSmallSmem / sizeof(float)];
   ExpertTile t;
-  if (!expert_tile<kSmallTile>(a.offsets, a.experts, a.rows, 1, (int)((a.n + kSmallTile - 1) / kSmallTile), blockIdx.x, t)) return;
+  if (!expert_tile<kSmallTile>(a.offsets, a.experts, a.rows, 1, (int)((a.n + kSmallTile - 1) / kSmallTile), (int)grid_tile(), t)) return;
   const int64_t wc = a.n * (a.k >> 1), ws = a.n * (a.k >> 5);
   const Operand A{a.ac, a.as, t.end}, B{a.bc + t.expert * wc, a.bs + t.expert * ws, a.n};
   const Operand A2{a.a2c, a.a2s, t.end}, B2{a.b2c + t.expert * wc, a.b2s + t.expert * ws, a.n};
@@ -143,9 +143,9 @@ __global__ __launch_bounds__(kSmallThreads, 3) void gemm_experts_small_kernel(Ex
 
 // dW_e = A[:, segment] B[:, segment]^T: rows of A and B hold `tokens` values.
 // The K range of a segment starts and ends inside a K step: the loop masks the
-// blocks of the neighbours' tokens.
+// blocks of the neighbours' tokens.  `num`: tiles of all experts.
 __global__ __launch_bounds__(kFastThreads) void gemm_experts_wgrad_kernel(
-    const int32_t* __restrict__ offsets, int64_t tokens, int64_t M, int64_t N, const uint8_t* __restrict__ ac,
+    const int32_t* __restrict__ offsets, int num, int64_t tokens, int64_t M, int64_t N, const uint8_t* __restrict__ ac,
     const uint8_t* __restrict__ as, const uint8_t* __restrict__ bc, const uint8_t* __restrict__ bs, Epilogue e) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kSmemBytes];
   const int tiles_m = (int)((M + BM - 1) / BM), tiles_n = (int)((N + BN - 1) / BN), tiles = tiles_m * tiles_n;
@@ -154,7 +154,8 @@ __global__ __launch_bounds__(kFastThreads) void gemm_experts_wgrad_kernel(
   // length.  (64 experts, 2048 x 2048, 1024 tokens each on average, spread as e^N(0,
   // 1/2): 306 us; in turns of 32 328, in one stretch an XCD 324, 8 x 1 blocks 325.
   // Where all are as long, one stretch of 4 x 8 blocks is faster: 291 against 301.)
-  const int pid = blockIdx.x, turn = pid >> 6, l = turn == (int)(gridDim.x >> 6) ? pid : (turn << 6) + ((pid & 7) << 3) + ((pid >> 3) & 7);
+  if (grid_tile() >= num) return;
+  const int pid = (int)grid_tile(), turn = pid >> 6, l = turn == num >> 6 ? pid : (turn << 6) + ((pid & 7) << 3) + ((pid >> 3) & 7);
   const int expert = l / tiles, in = l - expert * tiles;
   const int group = in / (4 * tiles_n), rest = in - group * 4 * tiles_n, height = std::min(tiles_m - 4 * group, 4);
   const int64_t m0 = (int64_t)(4 * group + rest % height) * BM, n0 = (int64_t)(rest / height) * BN;
@@ -202,7 +203,7 @@ template <int kMode>
 __global__ __launch_bounds__(kFastThreads) void swiglu_experts_kernel(ExpertsArgs a, SwigluOut o) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kSmemBytes];
   ExpertTile t;
-  if (!expert_tile(a.offsets, a.experts, a.rows, 32, (int)((a.n + 127) / 128), blockIdx.x, t)) return;
+  if (!expert_tile(a.offsets, a.experts, a.rows, 32, (int)((a.n + 127) / 128), (int)grid_tile(), t)) return;
   const int64_t n0 = (int64_t)t.tn * 128, wc = a.n * a.k, ws = a.n * (a.k >> 4);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int wm = wave >> 2, wn = wave & 3, hl = lane >> 5;
@@ -220,11 +221,11 @@ __global__ __launch_bounds__(kFastThreads) void swiglu_experts_kernel(ExpertsArg
 // Workgroups of a product over sorted rows: the row tiles that any segments of
 // so many rows can make (a segment's last tile may be all but empty, and so may
 // that of the rows behind the last), times the column tiles, in eights (one of
-// each for an XCD); -1 past a grid.
+// each for an XCD); -1 past kMostTiles.
 static int64_t experts_grid(int64_t rows, int64_t experts, int64_t n, int64_t bn, int64_t bm = BM) {
   if (n > kMaxExpertRows) return -1;
   const int64_t tm = rows / bm + std::min(experts + 1, rows), tn = (n + bn - 1) / bn;
-  return tm > 0x7FFFFFF0 / tn ? -1 : (tm * tn + 7) / 8 * 8;
+  return tm > kMostTiles / tn ? -1 : (tm * tn + 7) / 8 * 8;
 }
 
 // Workgroups in 64 x 64 tiles, or 0 where the large ones are faster.  The small
@@ -280,11 +281,11 @@ fp4_status fp4_gemm_experts(int64_t experts, int64_t rows, int64_t n, int64_t k,
   e.y_f32 = c_type == FP4_F32;
   e.stream = streams(rows, n * (e.y_f32 ? 4 : 2));
   const auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kFastThreads), 0, as_stream(stream), a, e);
+    hipLaunchKernelGGL(kernel, tile_grid(grid), dim3(kFastThreads), 0, as_stream(stream), a, e);
   };
   const int64_t small = experts_small_grid(rows, experts, n);
   if (small > 0) {
-    hipLaunchKernelGGL(gemm_experts_small_kernel, dim3((unsigned)small), dim3(kSmallThreads), 0, as_stream(stream), a, e);
+    hipLaunchKernelGGL(gemm_experts_small_kernel, tile_grid(small), dim3(kSmallThreads), 0, as_stream(stream), a, e);
     return launch_status();
   }
   const int mode = k_mode(k);
@@ -303,7 +304,7 @@ fp4_status fp4_gemm_experts_wgrad(int64_t experts, int64_t tokens, int64_t m, in
   if (m == 0 || n == 0) return FP4_OK;
   if (!offsets || !c || (tokens > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return FP4_EINVAL;
   const int64_t tiles = tiles_of(m, BM, n, BN);
-  if (tiles < 0 || tiles > 0x7FFFFFFF / experts) return FP4_ESHAPE;
+  if (tiles < 0 || tiles > kMostTiles / experts) return FP4_ESHAPE;
   if (!operands_aligned(a_codes, a_scales) || !operands_aligned(b_codes, b_scales) || !aligned16(c) ||
       (reinterpret_cast<uintptr_t>(offsets) & 3))
     return FP4_EALIGN;
@@ -319,8 +320,8 @@ fp4_status fp4_gemm_experts_wgrad(int64_t experts, int64_t tokens, int64_t m, in
                        offsets, tokens, m, n, a_codes, a_scales, b_codes, b_scales, e);
     return launch_status();
   }
-  hipLaunchKernelGGL(gemm_experts_wgrad_kernel, dim3((unsigned)(tiles * experts)), dim3(kFastThreads), 0, as_stream(stream),
-                     offsets, tokens, m, n, a_codes, a_scales, b_codes, b_scales, e);
+  hipLaunchKernelGGL(gemm_experts_wgrad_kernel, tile_grid(tiles * experts), dim3(kFastThreads), 0, as_stream(stream),
+                     offsets, (int)(tiles * experts), tokens, m, n, a_codes, a_scales, b_codes, b_scales, e);
   return launch_status();
 }
 
@@ -345,7 +346,7 @@ fp4_status fp4_swiglu_producer_experts(int64_t experts, int64_t rows, int64_t f,
                       nullptr, nullptr};
   const SwigluOut o{a_bf16, b_bf16, h_codes, h_scales, ht_codes, ht_scales, sign_mask16 & 0xFFFFu};
   const auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kFastThreads), 0, as_stream(stream), a, o);
+    hipLaunchKernelGGL(kernel, tile_grid(grid), dim3(kFastThreads), 0, as_stream(stream), a, o);
   };
   const int mode = k_mode(d);
   if (mode == kWhole) go(swiglu_experts_kernel<kWhole>);
