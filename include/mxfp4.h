@@ -99,8 +99,8 @@ typedef enum { FP4_RTN = 0, FP4_SR = 1 } fp4_round;
  *   x       [rows][ldx] bf16, reads rows x cols
  *   codes   [rows][cols/2] u8,   scales [rows][cols/32] u8
  * Errors: FP4_EINVAL bad mode or null pointer; FP4_ESHAPE rows < 0, cols not
- * a non-negative multiple of 32, or ldx < cols; FP4_EALIGN x or codes not
- * 16-byte aligned, or ldx not a multiple of 8.
+ * a non-negative multiple of 32 up to 2^35 - 2048, or ldx < cols; FP4_EALIGN x
+ * or codes not 16-byte aligned, or ldx not a multiple of 8.
  */
 fp4_status fp4_quantize_rows(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx,
                              uint8_t* codes, uint8_t* scales,
@@ -118,8 +118,8 @@ fp4_status fp4_quantize_rows(const uint16_t* x, int64_t rows, int64_t cols, int6
  *   x        [rows][ldx] bf16
  *   codes_t  [cols][rows/2] u8,   scales_t [cols][rows/32] u8
  * Errors: FP4_EINVAL hadamard not 0 or 32, or null pointer; FP4_ESHAPE rows
- * or cols not a non-negative multiple of 32, ldx < cols, or rows > 8388480
- * (more than 65535 tiles of 128 tokens); FP4_EALIGN x or codes_t not 16-byte
+ * or cols not a non-negative multiple of 32, ldx < cols, cols > 2^31 - 128 or
+ * rows > 8388480 (more than 65535 tiles of 128 tokens); FP4_EALIGN x or codes_t not 16-byte
  * aligned, or ldx not a multiple of 8.
  */
 fp4_status fp4_quantize_cols(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx,
@@ -137,8 +137,8 @@ fp4_status fp4_quantize_cols(const uint16_t* x, int64_t rows, int64_t cols, int6
  *   row_codes [rows][cols/2], row_scales [rows][cols/32]
  *   codes_t   [cols][rows/2], scales_t   [cols][rows/32]
  * Errors as the two calls (FP4_EINVAL for a bad mode or hadamard; FP4_ESHAPE
- * also for rows > 8388480, more than 65535 tiles of 128 tokens; FP4_EALIGN
- * also for row_codes).
+ * also for rows > 8388480, more than 65535 tiles of 128 tokens, or cols > 2^31 -
+ * 256; FP4_EALIGN also for row_codes).
  */
 fp4_status fp4_quantize_dual(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx,
                              uint8_t* row_codes, uint8_t* row_scales,
@@ -178,8 +178,8 @@ fp4_status fp4_quantize_w2d32(const uint16_t* w, int64_t n, int64_t k, int64_t l
  *   a_codes [m][k/2], a_scales [m][k/32]; b_codes [n][k/2], b_scales [n][k/32]
  *   c       [m][ldc] fp32
  * Errors: FP4_EINVAL accumulate not 0 or 1, or null pointer; FP4_ESHAPE m, n
- * or k not a non-negative multiple of 32, ldc < n, or more than 2^31 - 1
- * output tiles of 256 x 256; FP4_EALIGN an operand or c not 16-byte aligned,
+ * or k not a non-negative multiple of 32, ldc < n, or more than 2^23 - 1
+ * output tiles of 256 x 256 (2^24 - 1 for k not whole 256s); FP4_EALIGN an operand or c not 16-byte aligned,
  * or ldc not a multiple of 4.
  */
 fp4_status fp4_gemm(int64_t m, int64_t n, int64_t k,
@@ -224,7 +224,7 @@ fp4_status fp4_gemm_pair(int64_t m, int64_t n, int64_t k,
  * with FP4_EINVAL (for the pair form all four of a2_codes, a2_scales,
  * b2_codes, b2_scales must be non-NULL, otherwise all four NULL); FP4_ESHAPE,
  * FP4_EALIGN as those calls, and FP4_ESHAPE when the problems together have
- * more than 2^31 - 1 tiles.  Every problem is checked before anything is
+ * more than 2^23 - 1 tiles.  Every problem is checked before anything is
  * enqueued.
  */
 #define FP4_GEMM_GROUP_MAX 4
@@ -265,8 +265,8 @@ fp4_status fp4_gemm_grouped(const fp4_gemm_problem* problems, int count, hipStre
  *   ht_codes [f][t/2], ht_scales [f][t/32]     (optional; both or neither)
  * Errors: FP4_EINVAL exactly one of ht_codes, ht_scales NULL, or another null
  * pointer (the operands may be NULL when d = 0); FP4_ESHAPE t, f or d not a
- * non-negative multiple of 32, or more than 2^31 - 1 tiles of 256 tokens x
- * 128 columns; FP4_EALIGN an operand, a_bf16, b_bf16, h_codes or ht_codes not
+ * non-negative multiple of 32, or more than 2^23 - 1 tiles of 256 tokens x
+ * 128 columns (2^24 - 1 for d not whole 256s); FP4_EALIGN an operand, a_bf16, b_bf16, h_codes or ht_codes not
  * 16-byte aligned.
  */
 fp4_status fp4_swiglu_producer(int64_t t, int64_t f, int64_t d,
@@ -284,8 +284,8 @@ fp4_status fp4_swiglu_producer(int64_t t, int64_t f, int64_t d,
  *   dA = bf16(((dH*b)*sig) * (1 + a*(1 - sig))),   dB = bf16(dH*(a*sig))
  *   dh [t][lddh] fp32; a_bf16, b_bf16, da_bf16, db_bf16 [t][f]
  * Errors: FP4_EINVAL null pointer; FP4_ESHAPE t or f not a non-negative
- * multiple of 32, or lddh < f; FP4_EALIGN a pointer not 16-byte aligned, or
- * lddh not a multiple of 4.
+ * multiple of 32, f > 2^35 - 2048 or lddh < f; FP4_EALIGN a pointer not 16-byte
+ * aligned, or lddh not a multiple of 4.
  */
 fp4_status fp4_swiglu_backward(int64_t t, int64_t f, const float* dh, int64_t lddh,
                                const uint16_t* a_bf16, const uint16_t* b_bf16,
@@ -337,7 +337,7 @@ fp4_status fp4_swiglu_backward_producer(int64_t t, int64_t f, const float* dh, i
  * Errors: FP4_EINVAL null pointer; FP4_ESHAPE t, f or d not a non-negative
  * multiple of 32, d not a positive multiple of 256 (the fused main loop's K
  * step), f >= 2^22 or d >= 2^24 (32-bit offsets within a 256-row panel), or
- * more than 2^31 - 1 tiles; FP4_EALIGN an operand, a_bf16, b_bf16 or a code
+ * more than 2^23 - 1 tiles; FP4_EALIGN an operand, a_bf16, b_bf16 or a code
  * buffer not 16-byte aligned.
  */
 fp4_status fp4_gemm_swiglu_backward_producer(int64_t t, int64_t f, int64_t d,
@@ -379,8 +379,8 @@ fp4_status fp4_gemm_swiglu_backward_producer(int64_t t, int64_t f, int64_t d,
  *   factors    [ceil(rows/256)] fp32,  panel_amax [ceil(rows/256)] fp32
  * Three kernels: zero the maxima, reduce them (atomic max), quantize.
  * Errors: FP4_EINVAL bad mode or null pointer; FP4_ESHAPE rows < 0, cols not a
- * non-negative multiple of 32, ldx < cols, or rows > 2097120 (65535 groups of
- * 32 rows); FP4_EALIGN x or codes not 16-byte aligned, or ldx not a multiple
+ * non-negative multiple of 32 up to 2^35 - 2048, ldx < cols, or rows > 2097120
+ * (65535 groups of 32 rows); FP4_EALIGN x or codes not 16-byte aligned, or ldx not a multiple
  * of 8.
  */
 fp4_status fp4_nv_quantize_rows(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx,
@@ -419,7 +419,7 @@ fp4_status fp4_nv_quantize_w2d16(const uint16_t* w, int64_t n, int64_t k, int64_
  *   c       [m][ldc] fp32
  * Errors: FP4_EINVAL accumulate not 0 or 1, negative stride or null pointer;
  * FP4_ESHAPE m or n not a non-negative multiple of 32, k not a non-negative
- * multiple of 64, ldc < n, k >= 2^24, or more than 2^31 - 1 output tiles;
+ * multiple of 64, ldc < n, k >= 2^24, or more than 2^23 - 1 output tiles;
  * FP4_EALIGN a code buffer or c not 16-byte aligned, or ldc not a multiple
  * of 4.  k = 0 writes C = 0 (unchanged when accumulating).
  */

@@ -25,6 +25,10 @@ inline fp4_status launch_status() {
   return FP4_OK;
 }
 
+// Most workgroups in one dimension of a launch, which holds less than 2^32 threads
+// (a larger one wraps, with no error).
+constexpr int64_t max_groups(int threads) { return 0xFFFFFFFFll / threads; }
+
 inline hipStream_t as_stream(hipStream_t s) { return s; }
 
 }  // namespace mx

@@ -243,7 +243,7 @@ extern "C" fp4_status fp4_gemm_swiglu_backward_producer(
   // 32-bit buffer offsets: a 256-row panel of a, b and of the operands
   if (f >= ((int64_t)1 << 22) || d >= ((int64_t)1 << 24)) return FP4_ESHAPE;
   const int64_t tm = (t + BM - 1) / BM, tn = (f + BN - 1) / BN;
-  if (tm > 0x7FFFFFFF / tn) return FP4_ESHAPE;
+  if (tm > max_groups(kFastThreads) / tn) return FP4_ESHAPE;
   const DbOut oa{da_codes, da_scales, dat_codes, dat_scales, offset_a};
   const DbOut ob{db_codes, db_scales, dbt_codes, dbt_scales, offset_b};
   hipLaunchKernelGGL(dgrad_swiglu_bwd_kernel, dim3((unsigned)(tm * tn)), dim3(kFastThreads), 0, as_stream(stream), t,

@@ -285,12 +285,12 @@ using namespace mx;
 // 5-15 us each, and the kernels after them too; the 134 MB outputs lost
 // about 7 us each, so they keep ordinary stores).
 // Number of (bm x bn) output tiles of an m x n result, or -1 when it exceeds
-// the 2^31 - 1 workgroups of a one-dimensional grid (checked before the
-// product, which could overflow int64 for huge m, n).
-static int64_t grid_tiles(int64_t m, int64_t bm, int64_t n, int64_t bn) {
+// the workgroups of `threads` that a one-dimensional grid holds (checked before
+// the product, which could overflow int64 for huge m, n).
+static int64_t grid_tiles(int64_t m, int64_t bm, int64_t n, int64_t bn, int threads) {
   const int64_t tm = (m + bm - 1) / bm, tn = (n + bn - 1) / bn;
   if (tm == 0 || tn == 0) return 0;
-  if (tm > 0x7FFFFFFF / tn) return -1;
+  if (tm > max_groups(threads) / tn) return -1;
   return tm * tn;
 }
 
@@ -331,7 +331,7 @@ static fp4_status check_problem(const fp4_gemm_problem& p, int64_t& tiles) {
   if (p.m == 0 || p.n == 0) return FP4_OK;                // empty C
   if (!p.c) return FP4_EINVAL;
   if (p.k == 0) {                                         // C = 0, or unchanged when accumulating
-    if (!p.accumulate && (p.n + 255) / 256 > 0x7FFFFFFF) return FP4_ESHAPE;
+    if (!p.accumulate && (p.n + 255) / 256 > max_groups(256)) return FP4_ESHAPE;
     return FP4_OK;
   }
   const bool pair = p.a2_codes || p.a2_scales || p.b2_codes || p.b2_scales;
@@ -343,7 +343,7 @@ static fp4_status check_problem(const fp4_gemm_problem& p, int64_t& tiles) {
   if (pair && (!aligned16(p.a2_codes) || !aligned16(p.b2_codes) || !aligned16(p.a2_scales) ||
                !aligned16(p.b2_scales)))
     return FP4_EALIGN;
-  tiles = grid_tiles(p.m, BM, p.n, BN);
+  tiles = grid_tiles(p.m, BM, p.n, BN, fast_k(p.k) ? kFastThreads : kGemmThreads);
   if (tiles < 0) return FP4_ESHAPE;
   return FP4_OK;
 }
@@ -421,7 +421,7 @@ fp4_status fp4_gemm_grouped(const fp4_gemm_problem* problems, int count, hipStre
     if (st != FP4_OK) return st;
     if (fast_k(problems[q].k)) total += tiles[q];
   }
-  if (total > 0x7FFFFFFF) return FP4_ESHAPE;
+  if (total > max_groups(kFastThreads)) return FP4_ESHAPE;
   hipStream_t s = as_stream(stream);
   // the shared launch: longest K per tile first (pair form: both K ranges)
   int order[FP4_GEMM_GROUP_MAX];
@@ -462,10 +462,11 @@ fp4_status fp4_swiglu_producer(int64_t t, int64_t f, int64_t d, const uint8_t* x
   if (!aligned16(x_codes) || !aligned16(w13_codes) || !aligned16(h_codes) || !aligned16(x_scales) ||
       !aligned16(w13_scales) || !aligned16(a_bf16) || !aligned16(b_bf16) || (ht_codes && !aligned16(ht_codes)))
     return FP4_EALIGN;
-  const int64_t tiles = grid_tiles(t, BM, f, 128);
+  const bool fast = (d % 256) == 0 && 256 * (d / 2) < 0x7FFFFFFF;
+  const int64_t tiles = grid_tiles(t, BM, f, 128, fast ? kFastThreads : kGemmThreads);
   if (tiles < 0) return FP4_ESHAPE;
   hipStream_t s = as_stream(stream);
-  if ((d % 256) == 0 && 256 * (d / 2) < 0x7FFFFFFF)
+  if (fast)
     hipLaunchKernelGGL(swiglu_fast_kernel, dim3((unsigned)tiles), dim3(kFastThreads), 0, s, t, f, d, x_codes, x_scales,
                        w13_codes, w13_scales, a_bf16, b_bf16, h_codes, h_scales, ht_codes, ht_scales,
                        sign_mask16 & 0xFFFFu);

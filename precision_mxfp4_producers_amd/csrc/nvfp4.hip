@@ -568,7 +568,7 @@ fp4_status fp4_nv_quantize_rows(const uint16_t* x, int64_t rows, int64_t cols, i
   if (rows == 0 || cols == 0) return FP4_OK;
   if (!x || !codes || !scales || !factors || !panel_amax) return FP4_EINVAL;
   const int64_t gx = ceil_div(cols / 8, 256);
-  if (gx > 0x7FFFFFFF || ceil_div(rows, 32) > 65535) return FP4_ESHAPE;
+  if (gx > max_groups(256) || ceil_div(rows, 32) > 65535) return FP4_ESHAPE;
   if (!aligned16(x) || !aligned16(codes) || (ldx % 8) != 0) return FP4_EALIGN;
   const int64_t panels = ceil_div(rows, kNvPanel);
   const int nb = nv_amax_batches(gx, rows);
@@ -600,7 +600,7 @@ fp4_status fp4_nv_quantize_w2d16(const uint16_t* w, int64_t n, int64_t k, int64_
   if (!w || !row_codes || !row_scales || !col_codes || !col_scales || !factor || !amax_out) return FP4_EINVAL;
   const int64_t gxa = ceil_div(k / 8, 256);
   const int64_t gk = ceil_div(k, 128), gy = ceil_div(n, 128);
-  if (gxa > 0x7FFFFFFF || n / 32 > 65535 || ldw >= ((int64_t)1 << 22)) return FP4_ESHAPE;
+  if (gxa > max_groups(256) || n / 32 > 65535 || ldw >= ((int64_t)1 << 22)) return FP4_ESHAPE;
   if (!aligned16(w) || !aligned16(row_codes) || !aligned16(col_codes) || (ldw % 8) != 0) return FP4_EALIGN;
   const int nb = nv_amax_batches(gxa, n);
   // about 512 long-running workgroups, each walking a run of macro tiles along K
@@ -627,7 +627,7 @@ fp4_status fp4_nv_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes, 
   if (m == 0 || n == 0) return FP4_OK;
   if (!c) return FP4_EINVAL;
   const int64_t tm = ceil_div(m, 256), tn = ceil_div(n, 256);
-  if (tm > 0x7FFFFFFF / tn) return FP4_ESHAPE;
+  if (tm > max_groups(512) / tn) return FP4_ESHAPE;
   if (k == 0) return fp4_gemm(m, n, 0, nullptr, nullptr, nullptr, nullptr, c, ldc, accumulate, stream);
   if (!a_codes || !a_scales || !a_factors || !b_codes || !b_scales || !b_factors) return FP4_EINVAL;
   if (!aligned16(a_codes) || !aligned16(b_codes) || !aligned16(c) || (ldc % 4) != 0) return FP4_EALIGN;

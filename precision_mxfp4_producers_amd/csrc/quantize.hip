@@ -25,7 +25,6 @@ thread_local int g_last_hip_error = 0;
 
 constexpr int kThreads = 256;
 constexpr int kMaxGridY = 65535;
-constexpr int64_t kMaxGridX = 0x7FFFFFFF;
 constexpr int64_t kTargetBlocks = 8192;                  // 32 workgroups per CU
 
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -475,7 +474,7 @@ fp4_status fp4_quantize_rows(const uint16_t* x, int64_t rows, int64_t cols, int6
   if (!aligned16(x) || !aligned16(codes) || (ldx % 8) != 0) return FP4_EALIGN;
   const int64_t cpr = cols >> 3;
   const int64_t gx = (cpr + kThreads - 1) / kThreads;
-  if (gx > kMaxGridX) return FP4_ESHAPE;
+  if (gx > max_groups(kThreads)) return FP4_ESHAPE;
   // about kTargetBlocks workgroups, each taking whole passes of kRowsPerPass rows
   int64_t gy = std::max<int64_t>(1, kTargetBlocks / gx);
   gy = std::min<int64_t>(gy, (rows + kRowsPerPass - 1) / kRowsPerPass);
@@ -503,7 +502,7 @@ fp4_status fp4_quantize_cols(const uint16_t* x, int64_t rows, int64_t cols, int6
   if (!x || !codes_t || !scales_t) return FP4_EINVAL;
   if (!aligned16(x) || !aligned16(codes_t) || (ldx % 8) != 0) return FP4_EALIGN;
   const int64_t gx = (cols + kColW - 1) / kColW, gy = (rows + kColTok - 1) / kColTok;
-  if (gy > kMaxGridY || gx > kMaxGridX) return FP4_ESHAPE;
+  if (gy > kMaxGridY || gx > max_groups(kThreads)) return FP4_ESHAPE;
   dim3 grid((unsigned)gx, (unsigned)gy);
   hipStream_t s = as_stream(stream);
   if (hadamard == 32)
@@ -526,7 +525,7 @@ fp4_status fp4_quantize_dual(const uint16_t* x, int64_t rows, int64_t cols, int6
   if (!x || !row_codes || !row_scales || !codes_t || !scales_t) return FP4_EINVAL;
   if (!aligned16(x) || !aligned16(row_codes) || !aligned16(codes_t) || (ldx % 8) != 0) return FP4_EALIGN;
   const int64_t gx = (cols + kDualW - 1) / kDualW, gy = (rows + kDualTok - 1) / kDualTok;
-  if (gy > kMaxGridY || gx > kMaxGridX) return FP4_ESHAPE;
+  if (gy > kMaxGridY || gx > max_groups(kDualThreads)) return FP4_ESHAPE;
   dim3 grid((unsigned)gx, (unsigned)gy);
   hipStream_t s = as_stream(stream);
   const uint32_t m16 = hadamard == 32 ? (sign_mask16 & 0xFFFFu) : 0u;

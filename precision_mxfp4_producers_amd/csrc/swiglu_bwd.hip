@@ -21,7 +21,6 @@ namespace mx {
 
 constexpr int kBwdThreads = 256;
 constexpr int kMaxGridY = 65535;
-constexpr int64_t kMaxGridX = 0x7FFFFFFF;
 
 // One lane handles 8 consecutive elements of a row.
 __global__ __launch_bounds__(kBwdThreads) void swiglu_bwd_kernel(
@@ -297,7 +296,7 @@ extern "C" fp4_status fp4_swiglu_backward(int64_t t, int64_t f, const float* dh,
     return FP4_EALIGN;
   const int64_t cpr = f >> 3;
   const int64_t gx = (cpr + kBwdThreads - 1) / kBwdThreads;
-  if (gx > kMaxGridX) return FP4_ESHAPE;
+  if (gx > max_groups(kBwdThreads)) return FP4_ESHAPE;
   dim3 grid((unsigned)gx, (unsigned)(t < kMaxGridY ? t : kMaxGridY));
   hipLaunchKernelGGL(swiglu_bwd_kernel, grid, dim3(kBwdThreads), 0, as_stream(stream), t, f, dh, lddh, a_bf16,
                      b_bf16, da_bf16, db_bf16);
@@ -318,7 +317,7 @@ extern "C" fp4_status fp4_swiglu_backward_producer(
       !aligned16(db_codes) || !aligned16(dat_codes) || !aligned16(dbt_codes) || (lddh % 4) != 0)
     return FP4_EALIGN;
   const int64_t gx = (f + kFbCols - 1) / kFbCols, gy = (t + kFbTok - 1) / kFbTok;
-  if (gy > kMaxGridY || gx > kMaxGridX || lddh >= (int64_t(1) << 23)) return FP4_ESHAPE;   // 32-bit buffer offsets
+  if (gy > kMaxGridY || gx > max_groups(kFbThreads) || lddh >= (int64_t(1) << 23)) return FP4_ESHAPE;   // 32-bit buffer offsets
   const FbOut oa{da_codes, da_scales, dat_codes, dat_scales, offset_a};
   const FbOut ob{db_codes, db_scales, dbt_codes, dbt_scales, offset_b};
   if (t <= (int64_t(1) << 34) / f)                        // t * f <= 2^34: counters below 2^32
