@@ -53,9 +53,10 @@ __global__ __launch_bounds__(kSmallThreads, 3) void gemm_act_small_kernel(int64_
 }
 
 // The most 64 x 64 tiles a product is given (large and small tiles, bias, GELU and
-// residual: 300 x 1024 x 1024, 80 small tiles, 20 and 7.0 us; 512 x 2048 x 2048, 256,
-// 24 and 8.8; 256 x 4096 x 14336, 256, 85 and 30; 1024 x 4096 x 4096, 1024, 37 and 31;
-// 2048 x 4096 x 1024, 2048, 24 and 25; 2048 x 4096 x 4096, 2048, 40 and 54).
+// residual, operands from memory: 300 x 1024 x 1024, 80 small tiles, 21 and 7.5 us; 512 x
+// 2048 x 2048, 256, 30 and 11.5; 256 x 4096 x 14336, 256, 121 and 39; 1024 x 4096 x 4096,
+// 1024, 45 and 36; 1024 x 4096 x 14336, 1024, 107 and 93; 2048 x 4096 x 1024, 2048, 28 and
+// 30; 2048 x 4096 x 4096, 2048, 47 and 61).
 constexpr int64_t kSmallMost = 1024;
 
 }  // namespace mx

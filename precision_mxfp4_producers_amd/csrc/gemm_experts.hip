@@ -228,22 +228,29 @@ static int64_t experts_grid(int64_t rows, int64_t experts, int64_t n, int64_t bn
   return tm > kMostTiles / tn ? -1 : (tm * tn + 7) / 8 * 8;
 }
 
-// Workgroups in 64 x 64 tiles, or 0 where the large ones are faster.  The small
-// ones are where they are few, the padding's and the last rows' counted (large and
-// small: 232 of them 7.5 and 4.4 us, 564 17 and 11, 712 8.8 and 5.3, 1344 28 and 27,
-// 1856 31 and 36, 2880 35 and 55), and where the experts have few rows, which fill a
-// small part of a large tile (64 experts' 2048 x 2048, 39 rows with their padding 45
-// and 30 us, 95 rows 50 and 45, 160 rows 58 and 67).
-static int64_t experts_small_grid(int64_t rows, int64_t experts, int64_t n) {
+// Workgroups in 64 x 64 tiles, or 0 where the large ones are faster.  The small ones
+// are where they are few, the padding's and the last rows' counted (large and small:
+// 232 of them 7.5 and 4.5 us, 712 9.9 and 6.5, 1088 37 and 34, 1344 37 and 38, 1856 22
+// and 26), and where the experts have few rows, which fill a small part of a large tile:
+// 80 rows an expert, padding counted (64 experts' 2048 x 2048: 40 rows 48 and 42 us, 96
+// rows 60 and 59, 128 rows 64 and 72), or 48 where rows of W of more than 2048 values
+// and large tiles for every CU leave little of their start bare (8 experts' 14336 x
+// 4096: 8 rows 64 and 58 us, 64 rows 71 and 85, 96 rows 80 and 111; 16 experts' 4096 x
+// 4096: 48 rows 61 and 50, 64 rows 45 and 57).  Over 148 calls with operands from memory
+// this is 0.8% above the better of the two, at most 16%.
+static int64_t experts_small_grid(int64_t rows, int64_t experts, int64_t n, int64_t k) {
   const int64_t grid = experts_grid(rows, experts, n, kSmallTile, kSmallTile);
-  return grid > 0 && (grid <= 1536 || rows <= 96 * experts) ? grid : 0;
+  const int64_t few = k > 2048 && experts * ((n + BN - 1) / BN) >= 256 ? 48 : 80;
+  return grid > 0 && (grid <= 1200 || rows <= few * experts) ? grid : 0;
 }
 
-// The most 64 x 64 tiles of the experts' weight gradients together (large and small:
-// 4 experts' 128 x 128, 65536 tokens in all, 16 small tiles, 75 and 27 us; 16 experts'
-// 32 x 1024, 32768, 256 tiles, 27 and 11; 64 experts' 256 x 256, 65536, 1024 tiles, 26
-// and 20; 4 experts' 1024 x 1024, 32768, 1024 tiles, 50 and 54; 8 experts' 1024 x 1024,
-// 2048, 2048 tiles, 15.0 and 15.2; 64 experts' 512 x 512, 65536, 4096 tiles, 31 and 48).
+// The most 64 x 64 tiles of the experts' weight gradients together (large and small,
+// operands from memory: 4 experts' 128 x 128, 65536 tokens in all, 16 small tiles, 90
+// and 39 us; 16 experts' 32 x 1024, 32768, 256 tiles, 31 and 14; 64 experts' 256 x 256,
+// 65536, 1024 tiles, 43 and 24; 4 experts' 1024 x 1024, 32768, 1024 tiles, 65 and 62 (50
+// and 54 from the caches); 5 experts' 1024 x 1024, 16384, 1280 tiles, 48 and 38; 3
+// experts' 1408 x 1408, 16384, 1452 tiles, 54 and 59; 8 experts' 1024 x 1024, 2048, 2048
+// tiles, 16.5 and 16.9; 64 experts' 512 x 512, 65536, 4096 tiles, 53 and 60).
 constexpr int64_t kSmallGradients = 1024;
 
 static bool operands_aligned(const uint8_t* c, const uint8_t* s) { return aligned16(c) && aligned16(s); }
@@ -283,7 +290,7 @@ fp4_status fp4_gemm_experts(int64_t experts, int64_t rows, int64_t n, int64_t k,
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, tile_grid(grid), dim3(kFastThreads), 0, as_stream(stream), a, e);
   };
-  const int64_t small = experts_small_grid(rows, experts, n);
+  const int64_t small = experts_small_grid(rows, experts, n, k);
   if (small > 0) {
     hipLaunchKernelGGL(gemm_experts_small_kernel, tile_grid(small), dim3(kSmallThreads), 0, as_stream(stream), a, e);
     return launch_status();
