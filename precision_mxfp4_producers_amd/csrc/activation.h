@@ -81,18 +81,25 @@ __device__ __forceinline__ float act_value(float z) {
   return z;
 }
 
-// The derivative; beyond |z| = 128 all are 0 or 1 in fp32, and taken at 128.
+// The derivative; beyond |z| = 128 all are 0 or 1 in fp32 (the last two are taken there).
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == FP4_ACT_NONE) return 1.0f;
   if constexpr (ACT == FP4_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+  if constexpr (ACT == FP4_ACT_GELU) {
+    // At -|z| the tail less |z| times the density, at |z| one less that.  Both as
+    // squares of their roots (the density is in range where 2^x of it is not); far out
+    // the tail is a tenth of it or less, so that the shorter fit leaves 1e-4.  The clamp
+    // as above: 0 where z is infinite, and a NaN comes with the roots.
+    const float t = normal_tail_root<false>(fabsf(z));
+    const float r = exp2_hw(__builtin_fmaf(__fmul_rn(z, z), -0.25f * kLog2e, -0.66287406f));   // log2(2 pi) / -4
+    const float u = __builtin_amdgcn_fmed3f(__fmul_rn(fabsf(z), r), 0.0f, 1.0f);
+    const float v = __builtin_fmaf(-u, r, __fmul_rn(t, t));
+    return z < 0.0f ? v : __fsub_rn(1.0f, v);
+  }
   const float x = __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f);
   float d = 1.0f;
-  if constexpr (ACT == FP4_ACT_GELU) {
-    const float t = normal_tail_root<true>(fabsf(x)), q = __fmul_rn(t, t);
-    const float r = exp2_hw(__fmul_rn(__fmul_rn(x, x), -0.25f * kLog2e));   // root of e^(-x^2 / 2)
-    d = __builtin_fmaf(__fmul_rn(x, r), __fmul_rn(0.39894228f, r), x < 0.0f ? q : __fsub_rn(1.0f, q));
-  } else if constexpr (ACT == FP4_ACT_GELU_TANH) {
+  if constexpr (ACT == FP4_ACT_GELU_TANH) {
     const float xx = __fmul_rn(x, x);
     const float s = sigmoid_of_exponent(__fmul_rn(kTanhC, __builtin_fmaf(__fmul_rn(xx, x), kTanhA, x)));
     const float inner = __builtin_fmaf(xx, 1.5957691f * 3.0f * kTanhA, 1.5957691f);   // 2 sqrt(2/pi) (1 + 3 A x^2)
