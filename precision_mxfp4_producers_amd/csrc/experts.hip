@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kSortThreads) void expert_count_kernel(SortArgs a) 
 // a slot's row is the expert's first row, plus the expert's slots in earlier
 // workgroups, waves and turns, plus those in lower lanes (found by comparing
 // the expert's bits across the wave).  Latency: 65536 slots of 64 experts take
-// 4.9 (count) and 6.3 us (32 workgroups), two slots 2.8 (one, no count).
+// 4.7 (count) and 6.6 us (32 workgroups), two slots 2.8 (one, no count).
 template <bool I64>
 __global__ __launch_bounds__(kSortThreads) void expert_sort_kernel(SortArgs a) {
   __shared__ uint32_t counts[kSortWaves * kMaxExperts];   // [waves][experts]
@@ -230,8 +230,8 @@ __global__ __launch_bounds__(256) void expert_where_kernel(GatherArgs a) {
   }
 }
 
-// (3 us) and then a wave takes 2048 columns of a token to all its rows: those
-// without codes, 311 MB in 55 to 58 us, 5.4 TB/s, as a copy does.  where[s] may hold
+// (4.7 us) and then a wave takes 2048 columns of a token to all its rows: those
+// without codes, 311 MB in 59 us, 5.3 TB/s, as a copy does.  where[s] may hold
 // anything if no row has slot s, and holds one of them if several have: a row
 // counts as the slot's if its slot is that.  The workgroups behind those of the
 // tokens take the rows that are no slot's: those without a token, and others than
@@ -308,8 +308,7 @@ __device__ __forceinline__ void load8_cached(const void* p, int64_t i, float (&v
 }
 
 // One thread per eight columns of a token, four of its rows in flight.  Bound by
-// memory: 8192 tokens x 4096 of two bf16 rows each, 268 MB, take 45 to 50
-// us, 5.4 to 5.9 TB/s.
+// memory: 8192 tokens x 4096 of two bf16 rows each, 268 MB, take 50 us, 5.4 TB/s.
 template <bool F32>
 __global__ __launch_bounds__(256) void expert_combine_kernel(CombineArgs a) {
   const int per = a.d >> 3;
@@ -359,8 +358,8 @@ struct CombineGradArgs {
 
 // dz[r] = w dy[t] and dw = <dy[t], z[r]>: a wave a slot, so that a token's waves
 // read dy from the cache; the workgroups behind them clear the rows without a
-// token.  Bound by memory: 8192 tokens x 2048, eight rows each, 579 MB, take 111
-// to 120 us, 5.0 TB/s (dz past the caches was slower).
+// token.  Bound by memory: 8192 tokens x 2048, eight rows each, 579 MB, take 113
+// us, 5.1 TB/s (dz past the caches was slower).
 template <bool DYF32, bool ZF32>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(CombineGradArgs a) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;

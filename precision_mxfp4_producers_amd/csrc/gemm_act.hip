@@ -7,9 +7,10 @@
 //
 // Bound by the matrix cores and, of the same workgroups, the store burst behind
 // each tile (one workgroup a CU: nothing else runs beside it).  8192 x 14336 x
-// 4096, 0.96 TFLOP: 259 us with a bf16 y (3.7 PFLOP/s; 275 with an fp32 one, the
-// plain product 280), 281 with z beside it, 291 with GELU, 305 with both (3.15
-// PFLOP/s) or with a residual.  Products of few tiles take tiles of 64 x 64.
+// 4096, 0.96 TFLOP, medians with operands from memory: 269 us with a bf16 y (3.6
+// PFLOP/s; 296 with an fp32 one and a bias, the plain product 291), 312 with bias and z
+// beside it, 308 with bias and GELU, 330 with all of them (2.9 PFLOP/s), 341 with bias
+// and residual.  Products of few tiles take tiles of 64 x 64.
 #include <hip/hip_runtime.h>
 
 #include "abi_common.h"

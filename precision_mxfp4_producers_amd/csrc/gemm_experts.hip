@@ -11,11 +11,13 @@
 // contractions, §3.2 the gated FFN.
 //
 // Bound by the matrix cores, the tiles' start and end that short K leaves bare,
-// and the weight gradients' stores.  64 experts of 2048 x 2048, 65536 rows of a
-// router that likes some experts better: rows 207 to 217 us (0.55 TFLOP, 2.6
-// PFLOP/s; a segment's last tile is half empty on average, 13% of them all), weight
-// gradients 345 to 355 us (1.07 GB of fp32 at 3.1 TB/s; a fill of as much takes 158).
-// Few rows and few tiles take tiles of 64 x 64.
+// and the weight gradients' stores.  Medians, operands from memory: 64 experts of 2048 x
+// 2048, 65536 rows of a router that likes some experts better: rows 218 us (0.55 TFLOP,
+// 2.5 PFLOP/s; a segment's last tile is half empty on average, 13% of them all), weight
+// gradients 353 us (1.07 GB of fp32 at 3.1 TB/s; a fill of as much takes 158), the gated
+// producer 583 (1.1 TFLOP, 1.9 PFLOP/s: its epilogue of three passes, and 830 MB
+// written).  Few rows and few tiles take tiles of 64 x 64, but for the gated producer: 64
+// experts' 2048 x 2048 with eight rows each, 285 MB, take it 139 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -8,10 +8,11 @@
 // than a load takes.  Sums run over K in the order of the plain product, so that
 // the tile size does not show in a result.  Bound by latency, and by the caches
 // where tiles are many: every operand byte is read four times as often as by the
-// large tile.  64 x 4096 x 4096, 64 tiles, take 11 us (large tiles 26), 2048 x 2048 x
-// 2048, 1024 tiles, 19 (27).  (A wave taking every fourth K step of the whole tile, the
-// partial sums added in LDS: 10 and 19, with 2048 tiles 32 against 25; fragments loaded
-// straight to their lanes, 64 lines an instruction: 20.)
+// large tile.  With bias, GELU and residual, operands from memory: 64 x 4096 x 4096, 64
+// tiles, 16 us (large tiles 33), 2048 x 2048 x 2048, 1024 tiles, 23 (31); from the caches
+// 11 and 19.  (There, a wave taking every fourth K step of the whole tile, the partial
+// sums added in LDS: 10 and 19, with 2048 tiles 32 against 25; fragments loaded straight
+// to their lanes, 64 lines an instruction: 20.)
 #pragma once
 
 #include "gemm_epilogue.h"

@@ -6,7 +6,7 @@
 //
 // Bound by the weights' way from memory, and where they are few by the start, x's
 // way to LDS, the decode and the meeting of the sums: one row of 4096 x 14336
-// (31 MB) 10 to 12 us, a bare loop of its loads 7.2; of 14336 x 4096 10.5; of 57344
+// (31 MB) 11 us, a bare loop of its loads 7.2; of 14336 x 4096 10.3; of 57344
 // x 8192 (250 MB) 54, 4.6 TB/s; without products behind the loads 1 to 2 us less.
 #include <hip/hip_runtime.h>
 

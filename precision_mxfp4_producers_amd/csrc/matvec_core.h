@@ -676,7 +676,9 @@ static void matvec_variant(const MatvecArgs& a, int64_t cus, F&& launch) {
   // else fewer.  Over 28 shapes this is 1.7% above the best of U = 1, 2, 4 and KW =
   // 1 .. 16, at most 7%: 64 experts' 2048 x 1056, three rows each, 24.3 us (the
   // rule above and items of four steps: 28.5), 64 gated 768 x 2048 29.3 (33.7), one
-  // row of 14336 x 4096 10.5 (12.4), of 4096 x 14336 11.8 (12.7).
+  // row of 14336 x 4096 10.5 (12.4), of 4096 x 14336 11.8 (12.7).  The calls without an
+  // epilogue, whose scales come whole or byte by byte, keep the rule above, which was
+  // measured for them (9.7 and 11.0 on these two).
   constexpr int kMaxU = WT == kMx && PART != kWordScales ? 4 : 2;   // what the registers hold
   const bool fine = PART == kWordScales && staged;
   const int order[5] = {2, fine ? 1 : 3, fine ? 0 : 4, 3, 4};

@@ -10,9 +10,11 @@
 // §2.4 row layouts, §3.2 gated FFN.
 //
 // Bound as the plain product: two of eight experts' gated 14336 x 4096, one row
-// each (125 MB), 23 us, all eight (499 MB), two rows each, 90 us, 5.5 TB/s; 64
-// experts' 2048 x 1056, three rows each (73 MB), 24 us, 19 without products behind
-// the loads.
+// each (125 MB), 24 us, all eight (499 MB), two rows each, 103 us, 4.8 TB/s; 64
+// experts' 2048 x 1056, three rows each (73 MB), 26 us, 19 without products behind
+// the loads.  The CUs are shared out evenly among the experts, whatever the router
+// does: of 64 experts' 192 rows, 129 on one expert and one on each other take 39 us, all
+// on one 24 for 1 MB of weights.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
