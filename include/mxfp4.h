@@ -621,6 +621,7 @@ typedef enum { FP4_ACT_NONE = 0, FP4_ACT_RELU = 1, FP4_ACT_GELU = 2, FP4_ACT_GEL
  *   residual  [m][ldr] bf16, or NULL
  *   z         [m][n] bf16, or NULL
  *   y         [m][ldy] bf16 or fp32 (y_type); y may be the residual (bf16, ldy = ldr)
+ * Outputs overlap no input otherwise.
  * Any m; k = 0 gives z = bias.  Deterministic.
  * Errors: FP4_EINVAL bad type or act, or null pointer; FP4_ESHAPE m negative, n
  * or k not a non-negative multiple of 32, k >= 2^24, a leading dimension below
@@ -691,6 +692,7 @@ int64_t fp4_act_backward_workspace(int64_t m, int64_t n);
  *   slots   [capacity] int32: the slot in a row, -1 where there is none
  *   rows    [t][k] int32: the row of a slot, -1 where it is not routed
  * ids outside 0 .. experts - 1 are not routed (padded tokens, dropped choices).
+ * Outputs of the calls below overlap no input, but where that is said.
  * The calls below check no index on the host; one that is out of its range is
  * taken for "none", and segments that are not ascending are cut, so that no
  * access leaves a tensor.
